@@ -8,7 +8,8 @@
  * rows into the page pool.  Around it: the rotary embedding (with an optional
  * per-head RMS norm) fused into the append, a shared-prefix decode that reads
  * a common prefix once per KV head, several causal query tokens per sequence,
- * and a host radix cache of prompt prefixes over the pool.
+ * a host radix cache of prompt prefixes over the pool, and the append and the
+ * attention of a cache held in 8 bits.
  *
  * Where the operations are defined (page title, section):
  *   - CacheIR, "Compiler Example": the decode graph lowers attention into
@@ -84,13 +85,18 @@ typedef enum pkv_status {
     PKV_ERR_REFCOUNT = 8       /* retain/release of a page that is not allocated */
 } pkv_status;
 
-typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype;
+typedef enum pkv_dtype {
+    PKV_F16 = 0,
+    PKV_BF16 = 1,
+    PKV_E4M3 = 2 /* elements of a pool made by kv8_pool_create; nowhere else */
+} pkv_dtype;
 
 /* Bits of the device status word. */
 #define PKV_DEV_BAD_PAGE 0x1u   /* a page id outside [0, num_pages) was skipped */
 #define PKV_DEV_BAD_LEN  0x2u   /* a length/position beyond the table row was clamped/skipped */
 #define PKV_DEV_TIMEOUT  0x4u   /* a bounded wait on a copy gave up (copy never landed) */
 #define PKV_DEV_BAD_PREFIX 0x8u /* a table row does not start with the shared prefix's pages */
+#define PKV_DEV_BAD_SEQ 0x10u   /* a sequence id outside [0, n_seqs) was skipped */
 
 typedef struct CUstream_st* pkv_stream; /* same type as cudaStream_t */
 typedef struct pkv_pool pkv_pool;       /* opaque */
@@ -583,6 +589,130 @@ pkv_status paged_decode_attention_no_alloc(const void* q, const void* k_pool, co
                                            int page_size, int num_pages, pkv_dtype dtype,
                                            float scale, void* out, int num_workers,
                                            pkv_decode_variant variant, pkv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit cache.
+ * (CacheIR, "Current Capabilities": persistent page-backed KV pools and
+ *  batched decode over shared page tables; the 8-bit form is this library's.)
+ *
+ * Half the bytes of the 16-bit pools, so twice the tokens in the same memory
+ * and about half the time of a decode.  Elements are e4m3 (largest value 448,
+ * no infinity); every block of 16 tokens of a page has one scale 2^e for each
+ * KV head and side (K, V), stored as E8M0 (the byte e + 127):
+ *     k_pool, v_pool  e4m3 [num_pages][n_kv_heads][page_size][head_dim]
+ *     scales          E8M0 [num_pages][n_kv_heads][page_size / 16][2]  (K, V)
+ *     value = element * 2^e
+ * Page tables, the page allocator and the prefix cache are those of the
+ * 16-bit pools.  Queries, new rows and outputs are fp16 or bf16 (dtype).
+ * Supported: head_dim 64 or 128, page_size a multiple of 16, at most 256;
+ * every device pointer 16-byte aligned; num_pages * n_kv_heads * page_size at
+ * most 2^31 - 1 for the attention calls (else UNSUPPORTED).
+ *
+ * How a block gets its scale: the appended tokens of one block (a run) need
+ * the smallest e with max|x| <= 448 * 2^e, e within [-60, 40] (all zeros:
+ * -60).  A run that starts at the block's first slot sets e to that and takes
+ * nothing over from what the block held; any other run sets e to the larger of
+ * that and the block's e, and when e grows the rows of the block's lower slots
+ * are rounded to the new scale (exact but for values that become subnormal:
+ * the scales are powers of two).  Slots above the run are not touched.  An
+ * element that is not finite is stored as NaN and does not set the scale; a
+ * finite one beyond 448 * 2^40 is stored as that; below 2^-70 it is zero.
+ * ------------------------------------------------------------------------ */
+
+/* A pool of 8-bit pages.  k_pool, v_pool, scales (device): all NULL -> the
+ * pool allocates them (the scales zeroed) and owns the memory; all non-NULL ->
+ * it borrows them.  Allocator, retain / release, info (dtype PKV_E4M3) and
+ * destroy are those of kv_pool_create's pools; kv_append, kv_append_rope and
+ * kv_gather answer UNSUPPORTED for it.  Errors as kv_pool_create. */
+pkv_status kv8_pool_create(int num_pages, int page_size, int n_kv_heads, int head_dim,
+                           void* k_pool, void* v_pool, void* scales, pkv_pool** out);
+
+/* Device address of the scales (NULL for a NULL handle or a 16-bit pool). */
+void* kv8_pool_scales(const pkv_pool* pool);
+
+/* Append n_tokens new tokens -- the single tokens of a step, or the prompts of
+ * several sequences laid end to end.  k_new, v_new [n_tokens][n_kv_heads]
+ * [head_dim] (dtype); positions int32 [n_tokens]: the token's position in its
+ * sequence, < 0 to skip it; seq_ids int32 [n_tokens]: its row of page_table
+ * [n_seqs][table_stride], or NULL: token i belongs to row i (n_tokens <=
+ * n_seqs, else INVALID_ARG).  The tokens of one sequence that fall into one
+ * block must stand next to each other at consecutive positions: a token that
+ * follows one of the same block and sequence at any other position is skipped
+ * (PKV_DEV_BAD_LEN), and two stretches of one block elsewhere in the same call
+ * leave that block with the bytes of either (no other block is affected).
+ * Blocks of different sequences must be different blocks.  dev_status (device,
+ * nullable): receives PKV_DEV_BAD_PAGE / BAD_LEN / BAD_SEQ bits (ORed in) for
+ * skipped runs.  n_tokens = 0 launches nothing; else one launch.  A pool made
+ * by kv_pool_create: UNSUPPORTED; inputs that overlap the pool: ALIAS. */
+pkv_status kv8_append(const pkv_pool* pool, const void* k_new, const void* v_new, pkv_dtype dtype,
+                      const int32_t* page_table, int table_stride, int n_seqs,
+                      const int32_t* positions, const int32_t* seq_ids, int n_tokens,
+                      uint32_t* dev_status, pkv_stream stream);
+
+/* The same with the rotary embedding of kv_append_rope (rotate-half, base
+ * rope_theta > 0), and with a norm weight [head_dim] its per-head RMS norm
+ * before it, on the way: q [n_tokens][n_q_heads][head_dim] is rotated into
+ * q_out (which may be q) and rounded once to dtype -- every token's, also the
+ * skipped ones' -- and k_new is rotated in fp32 and rounded once, to e4m3.
+ * The angle is formed as an exact 64-bit fraction of a turn, then cos / sin
+ * and the rotation in fp32.  One launch. */
+pkv_status kv8_append_rope(const pkv_pool* pool, const void* q, const void* k_new,
+                           const void* v_new, pkv_dtype dtype, const int32_t* page_table,
+                           int table_stride, int n_seqs, const int32_t* positions,
+                           const int32_t* seq_ids, int n_tokens, int n_q_heads,
+                           double rope_theta, const void* q_norm_weight,
+                           const void* k_norm_weight, float norm_eps, void* q_out,
+                           uint32_t* dev_status, pkv_stream stream);
+
+/* Bytes of the workspace of the three calls below (n_queries = 1 for the
+ * decode and the step).  A workspace serves one call at a time: calls that may
+ * overlap on the GPU, replayed graphs among them, need one each. */
+pkv_status paged_decode_kv8_workspace_size(int batch, int n_queries, int n_q_heads,
+                                           int n_kv_heads, int head_dim, int num_workers,
+                                           size_t* bytes);
+
+/* paged_decode_attention over an 8-bit cache: q, out [batch][n_q_heads]
+ * [head_dim] in dtype; arithmetic in fp32 on the stored values (e4m3 enters
+ * the products exactly; the softmax weights with 11 bits), out rounded once.
+ * A NaN in a row that a query attends to gives NaN, elsewhere (behind a
+ * sequence's end) none; V scales outside [2^-60, 2^40] are taken as the
+ * nearer end, which no append writes.  Results do not depend on page ids or
+ * timing.  Errors and status bits as for paged_decode_attention. */
+pkv_status paged_decode_attention_kv8(const void* q, const void* k_pool, const void* v_pool,
+                                      const void* scales, const int32_t* page_table,
+                                      int table_stride, const int32_t* context_lens, int batch,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                      int num_pages, pkv_dtype dtype, float scale, void* out,
+                                      void* workspace, size_t ws_bytes, int num_workers,
+                                      pkv_stream stream);
+
+/* paged_decode_attention_multi over an 8-bit cache: q, out [batch][n_queries]
+ * [n_q_heads][head_dim], 1 <= n_queries <= 64 (more: UNSUPPORTED), query j of
+ * sequence b attends to tokens 0 .. context_lens[b] - n_queries + j (none:
+ * zeros). */
+pkv_status paged_decode_attention_multi_kv8(
+    const void* q, const void* k_pool, const void* v_pool, const void* scales,
+    const int32_t* page_table, int table_stride, const int32_t* context_lens, int batch,
+    int n_queries, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int num_pages,
+    pkv_dtype dtype, float scale, void* out, void* workspace, size_t ws_bytes, int num_workers,
+    pkv_stream stream);
+
+/* One whole decode step: kv8_append (rope_theta = 0; norm weights must be NULL
+ * then) or kv8_append_rope (rope_theta > 0) of one new token per sequence at
+ * positions [batch], then paged_decode_attention_kv8 -- the same results.  With
+ * the rotation the rotated queries pass through `out`, as in
+ * paged_decode_step_rope; q stays as given.  Append errors are reported
+ * through the workspace status.  k_new, v_new, positions and the pools as for
+ * kv8_append, everything else as for paged_decode_attention_kv8. */
+pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int32_t* positions,
+                                 const void* q, void* k_pool, void* v_pool, void* scales,
+                                 const int32_t* page_table, int table_stride,
+                                 const int32_t* context_lens, int batch, int n_q_heads,
+                                 int n_kv_heads, int head_dim, int page_size, int num_pages,
+                                 pkv_dtype dtype, float scale, double rope_theta,
+                                 const void* q_norm_weight, const void* k_norm_weight,
+                                 float norm_eps, void* out, void* workspace, size_t ws_bytes,
+                                 int num_workers, pkv_stream stream);
 
 /* Copy the status of the last plan/decode/step call on this workspace to
  * *status_out (host): the OR of the PKV_DEV_* bits of its kernels.  This call

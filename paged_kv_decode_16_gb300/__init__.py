@@ -29,6 +29,9 @@ __all__ = [
     "paged_decode_plan", "paged_decode_run", "paged_decode_combine", "paged_decode_attention",
     "paged_decode_step", "paged_decode_attention_no_alloc", "NO_ALLOC_SCRATCH_BYTES",
     "paged_decode_step_host", "paged_decode_step_host_workspace_size", "alloc_step_host_workspace",
+    "kv8_pool_create", "kv8_append", "kv8_append_rope", "paged_decode_kv8_workspace_size",
+    "alloc_kv8_workspace", "paged_decode_attention_kv8", "paged_decode_attention_multi_kv8",
+    "paged_decode_step_kv8", "DEV_BAD_SEQ",
     "pkv_read_device_status", "pkv_read_no_alloc_status", "alloc_workspace", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT",
     "VARIANT_AUTO", "VARIANT_CUDA_CORES", "VARIANT_TENSOR_CORES", "VARIANT_TCGEN05",
 ]
@@ -38,6 +41,7 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_ALIAS", 4: "PKV_ERR_OUT_OF_PAGES", 5: "PKV_ERR_WORKSPACE",
                 6: "PKV_ERR_CUDA", 7: "PKV_ERR_DEVICE_CHECK", 8: "PKV_ERR_REFCOUNT"}
 DEV_BAD_PAGE, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_PREFIX = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_SEQ = 0x10
 # decode kernels (pkv_decode_variant)
 VARIANT_AUTO, VARIANT_CUDA_CORES, VARIANT_TENSOR_CORES, VARIANT_TCGEN05 = 0, 1, 2, 3
 # size of the library's fixed device scratch (PKV_NO_ALLOC_SCRATCH_BYTES)
@@ -119,6 +123,18 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         "paged_decode_step_host": ([V, V, V, V, V, V, V, I, V, I, I, I, I, I, I, I, F, V, V, Z, I,
                                     I, V], I),
         "paged_decode_step_host_workspace_size": ([I, I, I, I, I, I, I, ctypes.POINTER(Z)], I),
+        "kv8_pool_create": ([I, I, I, I, V, V, V, ctypes.POINTER(V)], I),
+        "kv8_pool_scales": ([V], V),
+        "kv8_append": ([V, V, V, I, V, I, I, V, V, I, V, V], I),
+        "kv8_append_rope": ([V, V, V, V, I, V, I, I, V, V, I, I, ctypes.c_double, V, V, F, V, V,
+                             V], I),
+        "paged_decode_kv8_workspace_size": ([I, I, I, I, I, I, ctypes.POINTER(Z)], I),
+        "paged_decode_attention_kv8": ([V, V, V, V, V, I, V, I, I, I, I, I, I, I, F, V, V, Z, I,
+                                        V], I),
+        "paged_decode_attention_multi_kv8": ([V, V, V, V, V, I, V, I, I, I, I, I, I, I, I, F, V,
+                                              V, Z, I, V], I),
+        "paged_decode_step_kv8": ([V, V, V, V, V, V, V, V, I, V, I, I, I, I, I, I, I, F,
+                                   ctypes.c_double, V, V, F, V, V, Z, I, V], I),
         "pkv_read_device_status": ([V, ctypes.POINTER(ctypes.c_uint32)], I),
         "pkv_read_no_alloc_status": ([ctypes.POINTER(ctypes.c_uint32)], I),
     }
@@ -219,6 +235,10 @@ class Pool:
 
     def v_ptr(self) -> int:
         return load_library().kv_pool_v(self.handle) or 0
+
+    def scales_ptr(self) -> int:
+        """The block scales of an 8-bit pool (0: a 16-bit pool)."""
+        return load_library().kv8_pool_scales(self.handle) or 0
 
     def alloc_pages(self, n: int) -> list[int]:
         ids = (ctypes.c_int32 * max(n, 1))()
@@ -753,6 +773,201 @@ def paged_decode_combine(out: torch.Tensor, n_kv_heads: int, workspace: torch.Te
     _check(load_library().paged_decode_combine(
         B, Hq, n_kv_heads, D, _dtype_code(out), _ptr(out), _ptr(workspace), workspace.numel(),
         int(num_workers), int(variant), _stream(stream)), "paged_decode_combine")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit cache: e4m3 pools with a power-of-two scale (E8M0) for each block of 16
+# tokens, KV head and side
+# ---------------------------------------------------------------------------
+_SCALE_DTYPES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _kv8_pools(k_pool, v_pool, scales):
+    _dev(k_pool, "k_pool", torch.float8_e4m3fn, 4)
+    _dev(v_pool, "v_pool", torch.float8_e4m3fn, 4)
+    _dev(scales, "scales", None, 4)
+    if scales.dtype not in _SCALE_DTYPES:
+        raise ValueError(f"scales must be float8_e8m0fnu (or its bytes), got {scales.dtype}")
+    NP, Hkv, P, D = k_pool.shape
+    if v_pool.shape != k_pool.shape or scales.shape != (NP, Hkv, P // 16, 2):
+        raise ValueError("k_pool/v_pool must be [NP, Hkv, P, D] and scales [NP, Hkv, P / 16, 2]")
+    return NP, Hkv, P, D
+
+
+def kv8_pool_create(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                    k_pool: torch.Tensor | None = None, v_pool: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None) -> Pool:
+    """Create an 8-bit pool; with k_pool / v_pool (float8_e4m3fn [NP, Hkv, P, D])
+    and scales (float8_e8m0fnu [NP, Hkv, P / 16, 2], K then V) the pool borrows
+    them, otherwise it allocates device memory itself."""
+    given = [t is not None for t in (k_pool, v_pool, scales)]
+    if any(given) and not all(given):
+        raise ValueError("give k_pool, v_pool and scales, or none of them")
+    if all(given):
+        if _kv8_pools(k_pool, v_pool, scales) != (num_pages, n_kv_heads, page_size, head_dim):
+            raise ValueError(f"k_pool shape {tuple(k_pool.shape)} != "
+                             f"{(num_pages, n_kv_heads, page_size, head_dim)}")
+    h = ctypes.c_void_p()
+    _check(load_library().kv8_pool_create(num_pages, page_size, n_kv_heads, head_dim,
+                                          _ptr(k_pool), _ptr(v_pool), _ptr(scales),
+                                          ctypes.byref(h)), "kv8_pool_create")
+    pool = Pool(h.value, k_pool, v_pool, num_pages, page_size, n_kv_heads, head_dim,
+                torch.float8_e4m3fn)
+    pool._keep = (k_pool, v_pool, scales)
+    return pool
+
+
+def _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status):
+    if pool.dtype != torch.float8_e4m3fn:
+        raise ValueError("pool must be an 8-bit pool (kv8_pool_create)")
+    _dev(k_new, "k_new", None, 3)
+    dt = _dtype_code(k_new)
+    _dev(v_new, "v_new", k_new.dtype, 3)
+    _dev(page_table, "page_table", torch.int32, 2)
+    _dev(positions, "positions", torch.int32, 1)
+    N = positions.shape[0]
+    if k_new.shape != (N, pool.n_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
+        raise ValueError("k_new/v_new must be [tokens, Hkv, D] matching the pool and positions")
+    if seq_ids is not None:
+        _dev(seq_ids, "seq_ids", torch.int32, 1)
+        if seq_ids.shape[0] != N:
+            raise ValueError("seq_ids must have one entry per token")
+    elif page_table.shape[0] < N:
+        raise ValueError("page_table has fewer rows than tokens (give seq_ids)")
+    if dev_status is not None:
+        _dev(dev_status, "dev_status", torch.int32)
+    return N, dt
+
+
+def kv8_append(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor,
+               positions: torch.Tensor, seq_ids: torch.Tensor | None = None,
+               dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Append k_new/v_new [tokens, Hkv, D] (float16 or bfloat16) at positions[i]
+    of sequence seq_ids[i] (default: token i's is row i of page_table): single
+    tokens of a step, or prompts laid end to end."""
+    N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
+    _check(load_library().kv8_append(pool.handle, _ptr(k_new), _ptr(v_new), dt, _ptr(page_table),
+                                     page_table.shape[1], page_table.shape[0], _ptr(positions),
+                                     _ptr(seq_ids), N, _ptr(dev_status), _stream(stream)),
+           "kv8_append")
+
+
+def kv8_append_rope(pool: Pool, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                    page_table: torch.Tensor, positions: torch.Tensor, rope_theta: float,
+                    q_out: torch.Tensor, seq_ids: torch.Tensor | None = None,
+                    dev_status: torch.Tensor | None = None, stream=None,
+                    q_norm_weight: torch.Tensor | None = None,
+                    k_norm_weight: torch.Tensor | None = None,
+                    norm_eps: float = 1e-6) -> torch.Tensor:
+    """kv8_append with the rotary embedding of q [tokens, Hq, D] (into q_out) and
+    of k_new; with a norm weight [D], the per-head RMS norm of that side first."""
+    N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
+    _dev(q, "q", k_new.dtype, 3)
+    _dev(q_out, "q_out", k_new.dtype, 3)
+    if q.shape[0] != N or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
+        raise ValueError("q/q_out must be [tokens, Hq, D] matching the pool and positions")
+    _norm_weights(q_norm_weight, k_norm_weight, q.dtype, pool.head_dim)
+    _check(load_library().kv8_append_rope(
+        pool.handle, _ptr(q), _ptr(k_new), _ptr(v_new), dt, _ptr(page_table),
+        page_table.shape[1], page_table.shape[0], _ptr(positions), _ptr(seq_ids), N, q.shape[1],
+        float(rope_theta), _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps),
+        _ptr(q_out), _ptr(dev_status), _stream(stream)), "kv8_append_rope")
+    return q_out
+
+
+def paged_decode_kv8_workspace_size(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                    n_queries: int = 1, num_workers: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().paged_decode_kv8_workspace_size(
+        batch, n_queries, n_q_heads, n_kv_heads, head_dim, int(num_workers), ctypes.byref(n)),
+        "paged_decode_kv8_workspace_size")
+    return n.value
+
+
+def alloc_kv8_workspace(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                        n_queries: int = 1, num_workers: int = 0, device=None) -> torch.Tensor:
+    """A torch uint8 buffer of the size the 8-bit attention calls need."""
+    n = paged_decode_kv8_workspace_size(batch, n_q_heads, n_kv_heads, head_dim, n_queries,
+                                        num_workers)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out, workspace, ndim):
+    _dev(q, "q", None, ndim)
+    dt = _dtype_code(q)
+    _dev(out, "out", q.dtype, ndim)
+    NP, Hkv, P, D = _kv8_pools(k_pool, v_pool, scales)
+    _dev(page_table, "page_table", torch.int32, 2)
+    _dev(context_lens, "context_lens", torch.int32, 1)
+    _dev(workspace, "workspace", torch.uint8)
+    B = q.shape[0]
+    if q.shape[-1] != D or out.shape != q.shape:
+        raise ValueError("q/out [..., Hq, D] and pools [NP, Hkv, P, D] disagree")
+    if page_table.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("page_table rows or context_lens != batch")
+    return B, Hkv, D, P, NP, dt
+
+
+def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                               scales: torch.Tensor, page_table: torch.Tensor,
+                               context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                               workspace: torch.Tensor, num_workers: int = 0,
+                               stream=None) -> torch.Tensor:
+    """paged_decode_attention over an 8-bit cache: q, out [B, Hq, D] in float16
+    or bfloat16, pools float8_e4m3fn, scales float8_e8m0fnu."""
+    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                     workspace, 3)
+    _check(load_library().paged_decode_attention_kv8(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(scales), _ptr(page_table), page_table.shape[1],
+        _ptr(context_lens), B, q.shape[1], Hkv, D, P, NP, dt, float(scale), _ptr(out),
+        _ptr(workspace), workspace.numel(), int(num_workers), _stream(stream)),
+        "paged_decode_attention_kv8")
+    return out
+
+
+def paged_decode_attention_multi_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                     scales: torch.Tensor, page_table: torch.Tensor,
+                                     context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                                     workspace: torch.Tensor, num_workers: int = 0,
+                                     stream=None) -> torch.Tensor:
+    """paged_decode_attention_multi over an 8-bit cache: q, out [B, Qn, Hq, D],
+    query j of sequence b attends causally to tokens 0 .. context_lens[b] - Qn + j."""
+    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                     workspace, 4)
+    _check(load_library().paged_decode_attention_multi_kv8(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(scales), _ptr(page_table), page_table.shape[1],
+        _ptr(context_lens), B, q.shape[1], q.shape[2], Hkv, D, P, NP, dt, float(scale),
+        _ptr(out), _ptr(workspace), workspace.numel(), int(num_workers), _stream(stream)),
+        "paged_decode_attention_multi_kv8")
+    return out
+
+
+def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                          q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                          scales: torch.Tensor, page_table: torch.Tensor,
+                          context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                          workspace: torch.Tensor, rope_theta: float = 0.0, num_workers: int = 0,
+                          stream=None, q_norm_weight: torch.Tensor | None = None,
+                          k_norm_weight: torch.Tensor | None = None,
+                          norm_eps: float = 1e-6) -> torch.Tensor:
+    """One decode step over an 8-bit cache: append k_new/v_new [B, Hkv, D] at
+    positions[b], then decode attention into out; with rope_theta > 0 the rotary
+    embedding of q and k_new (after the optional per-head RMS norm) comes first."""
+    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                     workspace, 3)
+    _dev(k_new, "k_new", q.dtype, 3)
+    _dev(v_new, "v_new", q.dtype, 3)
+    _dev(positions, "positions", torch.int32, 1)
+    if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D) or positions.shape[0] != B:
+        raise ValueError("k_new/v_new must be [B, Hkv, D] and positions [B]")
+    _norm_weights(q_norm_weight, k_norm_weight, q.dtype, D)
+    _check(load_library().paged_decode_step_kv8(
+        _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q), _ptr(k_pool), _ptr(v_pool),
+        _ptr(scales), _ptr(page_table), page_table.shape[1], _ptr(context_lens), B, q.shape[1],
+        Hkv, D, P, NP, dt, float(scale), float(rope_theta), _ptr(q_norm_weight),
+        _ptr(k_norm_weight), float(norm_eps), _ptr(out), _ptr(workspace), workspace.numel(),
+        int(num_workers), _stream(stream)), "paged_decode_step_kv8")
+    return out
 
 
 def pkv_read_device_status(workspace: torch.Tensor) -> int:

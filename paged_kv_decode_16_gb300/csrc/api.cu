@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "kernels_aux.cuh"
+#include "kv8.cuh"
 #include "merge.cuh"
 #include "pool_impl.hpp"
 
@@ -70,29 +71,37 @@ inline bool valid_variant(int v) {
            v == PKV_VARIANT_TENSOR_CORES || v == PKV_VARIANT_TCGEN05;
 }
 
+// KernelPick::variant of the 8-bit cache's decode kernel (not a caller's choice).
+constexpr int kVariantKv8 = 100;
+
 // The decode kernel chosen for a call: an entry of one instantiation table.
 // A worker is a warp, except on the tcgen05 kernel, where it is a CTA.
 struct KernelPick {
-    int variant = 0;  // PKV_VARIANT_CUDA_CORES, _TENSOR_CORES or _TCGEN05
+    int variant = 0;  // PKV_VARIANT_CUDA_CORES, _TENSOR_CORES, _TCGEN05 or kVariantKv8
     DecodeKernelInfo cc{};
     DecodeMmaInfo mma{};
     DecodeUmmaInfo um{};
+    pkv::Kv8DecodeInfo q8{};
     const void* fn() const {
+        if (variant == kVariantKv8) return reinterpret_cast<const void*>(q8.fn);
         return variant == PKV_VARIANT_TCGEN05     ? reinterpret_cast<const void*>(um.fn)
                : variant == PKV_VARIANT_TENSOR_CORES ? reinterpret_cast<const void*>(mma.fn)
                                                      : reinterpret_cast<const void*>(cc.fn);
     }
     int threads() const {
+        if (variant == kVariantKv8) return q8.warps * 32;
         return variant == PKV_VARIANT_TCGEN05       ? um.threads
                : variant == PKV_VARIANT_TENSOR_CORES ? mma.warps * 32
                                                      : cc.warps * 32;
     }
     int warps() const {  // workers per CTA
+        if (variant == kVariantKv8) return q8.warps;
         return variant == PKV_VARIANT_TCGEN05       ? 1
                : variant == PKV_VARIANT_TENSOR_CORES ? mma.warps
                                                      : cc.warps;
     }
     int smem() const {
+        if (variant == kVariantKv8) return q8.smem_bytes;
         return variant == PKV_VARIANT_TCGEN05       ? um.smem_bytes
                : variant == PKV_VARIANT_TENSOR_CORES ? mma.smem_bytes
                                                      : cc.smem_bytes;
@@ -643,6 +652,7 @@ pkv_status kv_append(const pkv_pool* pool, const void* k_new, const void* v_new,
                      const int32_t* page_table, int table_stride, const int32_t* positions,
                      int batch, uint32_t* dev_status, pkv_stream stream) {
     if (!pool || batch < 0 || table_stride <= 0) return PKV_ERR_INVALID_ARG;
+    if (pool->dtype == PKV_E4M3) return PKV_ERR_UNSUPPORTED;  // kv8_append
     if (batch == 0) return PKV_OK;
     if (!k_new || !v_new || !page_table || !positions) return PKV_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(pool->k) || !aligned16(pool->v))
@@ -668,6 +678,7 @@ pkv_status kv_append_rope(const pkv_pool* pool, const void* q, const void* k_new
                           const void* q_norm_weight, const void* k_norm_weight, float norm_eps,
                           void* q_out, uint32_t* dev_status, pkv_stream stream) {
     if (!pool || batch < 0 || table_stride <= 0 || n_q_heads <= 0) return PKV_ERR_INVALID_ARG;
+    if (pool->dtype == PKV_E4M3) return PKV_ERR_UNSUPPORTED;  // kv8_append_rope
     if (!(rope_theta > 0.0 && isfinite(rope_theta))) return PKV_ERR_INVALID_ARG;
     if (!norm_args_ok(q_norm_weight, k_norm_weight, norm_eps)) return PKV_ERR_INVALID_ARG;
     if (batch == 0) return PKV_OK;
@@ -708,6 +719,7 @@ pkv_status kv_gather(const pkv_pool* pool, const int32_t* page_table, int table_
                      const int32_t* context_lens, int batch, int max_len, void* k_out,
                      void* v_out, uint32_t* dev_status, pkv_stream stream) {
     if (!pool || batch < 0 || max_len < 0 || table_stride <= 0) return PKV_ERR_INVALID_ARG;
+    if (pool->dtype == PKV_E4M3) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || max_len == 0) return PKV_OK;
     if (batch > 65535 || pool->n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
     if (!page_table || !context_lens || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
@@ -1407,6 +1419,382 @@ pkv_status paged_decode_attention_multi(const void* q, const void* k_pool, const
                      cs)) != PKV_OK)
         return st;
     return do_combine(batch, n_q_heads, head_dim, dtype, out, workspace, s, cs);
+}
+
+}  // extern "C"
+
+// --- 8-bit cache (kv8.cuh) ---------------------------------------------------
+namespace {
+
+// Rows of a unit: at most 32 (four tiles of 8).  One query a sequence: the
+// query group, cut evenly when it is larger; several: as for the 16-bit kernel.
+constexpr int kKv8UnitRows = 32;
+
+pkv_status setup_kv8(int batch, int n_queries, int n_q_heads, int n_kv_heads, int head_dim,
+                     int page_size, pkv_dtype dtype, int num_workers, DecodeSetup* s) {
+    pkv_status st = check_shapes(batch, n_q_heads, n_kv_heads, head_dim, page_size);
+    if (st != PKV_OK) return st;
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    if (num_workers < 0 || n_queries < 1) return PKV_ERR_INVALID_ARG;
+    if (n_queries > kMaxQueries) return PKV_ERR_UNSUPPORTED;
+    s->group = n_q_heads / n_kv_heads;
+    const int t0 = (n_queries + kKv8UnitRows - 1) / kKv8UnitRows;
+    const int qpu = (n_queries + t0 - 1) / t0;
+    const int tiles = (n_queries + qpu - 1) / qpu;
+    int hpu = 1;
+    for (int d = 1; d <= s->group; ++d)
+        if (s->group % d == 0 && qpu * d <= kKv8UnitRows) hpu = d;
+    s->gs = qpu * hpu;
+    s->sub_groups = (s->group / hpu) * tiles;
+    s->rs = pkv::RowShape{n_queries, qpu, hpu, s->group / hpu, s->group, n_q_heads};
+    s->units_per_b = n_kv_heads * s->sub_groups;
+    s->units = (long long)batch * s->units_per_b;
+    if (s->units > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    s->kernel = KernelPick();
+    s->kernel.variant = kVariantKv8;
+    s->kernel.q8 = dtype == PKV_BF16 ? pkv::kv8_decode_info_bf16(head_dim, s->gs)
+                                     : pkv::kv8_decode_info_f16(head_dim, s->gs);
+    st = prepare_kernel(s->kernel, &s->workers_auto);
+    if (st != PKV_OK) return st;
+    s->workers = num_workers > 0 ? num_workers : s->workers_auto;
+    s->ws = ws_layout(batch, s->units, s->gs, head_dim, s->workers);
+    return PKV_OK;
+}
+
+// A side of the pool as a 2-D tensor of rows of head_dim bytes; a box is one
+// block (16 whole rows), swizzled over a row's width so that the kernel's
+// 16-byte reads of it spread over the banks.
+pkv_status kv8_map(const void* pool, long long rows, int head_dim, CUtensorMap* out) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return PKV_ERR_CUDA;
+    memset(out, 0, sizeof(*out));
+    const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)pkv::kChunk};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+struct Kv8Call {
+    const void* q;
+    const void* k_pool;
+    const void* v_pool;
+    const void* scales;
+    const int32_t* table;
+    int table_stride;
+    const int32_t* lens;
+    int batch, n_queries, n_q_heads, n_kv_heads, head_dim, page_size, num_pages;
+    pkv_dtype dtype;
+    float scale;
+    void* out;
+    void* workspace;
+    size_t ws_bytes;
+    int num_workers;
+    size_t qo_bytes() const { return (size_t)batch * n_queries * n_q_heads * head_dim * 2; }
+    size_t pool_bytes() const { return (size_t)num_pages * n_kv_heads * page_size * head_dim; }
+    size_t scale_bytes() const {
+        return (size_t)num_pages * n_kv_heads * (page_size / pkv::kChunk) * 2;
+    }
+};
+
+// Host-only argument checks (no CUDA call is made), in the order of
+// validate_decode_args.
+pkv_status validate_kv8(const Kv8Call& c) {
+    pkv_status st = check_shapes(c.batch, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size);
+    if (st != PKV_OK) return st;
+    if (c.dtype != PKV_F16 && c.dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    if (c.num_pages <= 0 || c.table_stride <= 0 || c.num_workers < 0 || c.n_queries < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (c.n_queries > kMaxQueries) return PKV_ERR_UNSUPPORTED;
+    if (!isfinite(c.scale)) return PKV_ERR_INVALID_ARG;
+    if (c.batch == 0) return PKV_OK;
+    if (!c.q || !c.k_pool || !c.v_pool || !c.scales || !c.table || !c.out || !c.lens)
+        return PKV_ERR_INVALID_ARG;
+    if (!c.workspace || (reinterpret_cast<uintptr_t>(c.workspace) & 255u))
+        return PKV_ERR_WORKSPACE;
+    if (!aligned16(c.q) || !aligned16(c.k_pool) || !aligned16(c.v_pool) || !aligned16(c.out) ||
+        !aligned16(c.scales))
+        return PKV_ERR_INVALID_ARG;
+    if ((long long)c.num_pages * c.n_kv_heads * c.page_size > 0x7fffffffLL)
+        return PKV_ERR_UNSUPPORTED;  // 32-bit tensor row coordinate
+    const size_t qo = c.qo_bytes(), pool = c.pool_bytes();
+    if (overlaps(c.out, qo, c.q, qo) || overlaps(c.out, qo, c.k_pool, pool) ||
+        overlaps(c.out, qo, c.v_pool, pool) || overlaps(c.out, qo, c.scales, c.scale_bytes()) ||
+        overlaps(c.out, qo, c.table, (size_t)c.batch * c.table_stride * 4) ||
+        overlaps(c.out, qo, c.lens, (size_t)c.batch * 4) ||
+        overlaps(c.out, qo, c.workspace, c.ws_bytes))
+        return PKV_ERR_ALIAS;
+    return PKV_OK;
+}
+
+// Decode and combine on a planned workspace; q: the call's, or the rotated ones.
+pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, cudaStream_t stream) {
+    uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+    pkv::Kv8DecodeParams kp;
+    pkv::DecodeParams& p = kp.d;
+    p.q = q;
+    p.k_pool = c.k_pool;
+    p.v_pool = c.v_pool;
+    p.table = c.table;
+    p.lens_eff = reinterpret_cast<const int32_t*>(ws + s.ws.lens_eff);
+    p.prefix = reinterpret_cast<const int32_t*>(ws + s.ws.prefix);
+    p.wstart = reinterpret_cast<const int32_t*>(ws + s.ws.wstart);
+    p.units = (int)s.units;
+    p.hdr = reinterpret_cast<const WsHeader*>(ws);
+    p.status = &reinterpret_cast<WsHeader*>(ws)->status;
+    p.partials = reinterpret_cast<float*>(ws + s.ws.partials);
+    p.unit_done = nullptr;
+    p.all_partials = 0;
+    p.rows = s.rs;
+    p.out = c.out;
+    p.table_stride = c.table_stride;
+    p.batch = c.batch;
+    p.n_q_heads = c.n_q_heads;
+    p.n_kv_heads = c.n_kv_heads;
+    p.page_size = c.page_size;
+    p.num_pages = c.num_pages;
+    p.group = s.group;
+    p.sub_groups = s.sub_groups;
+    p.scale_log2 = c.scale * 1.4426950408889634f;
+    kp.scales = static_cast<const uint16_t*>(c.scales);
+    kp.gs = s.gs;
+    CUtensorMap km, vm;
+    const long long rows = (long long)c.num_pages * c.n_kv_heads * c.page_size;
+    pkv_status st = kv8_map(c.k_pool, rows, c.head_dim, &km);
+    if (st == PKV_OK) st = kv8_map(c.v_pool, rows, c.head_dim, &vm);
+    if (st != PKV_OK) return st;
+    const int warps = s.kernel.warps();
+    st = cuda_status(pkv::launch_pdl(s.kernel.q8.fn, dim3((s.workers + warps - 1) / warps),
+                                     dim3(warps * 32), s.kernel.smem(), stream, kp, km, vm));
+    if (st != PKV_OK) return st;
+    return do_combine(c.batch, c.n_q_heads, c.head_dim, c.dtype, c.out, c.workspace, s, stream);
+}
+
+pkv_status kv8_attention(const Kv8Call& c, cudaStream_t stream) {
+    pkv_status st = validate_kv8(c);
+    if (st != PKV_OK || c.batch == 0) return st;
+    DecodeSetup s;
+    st = setup_kv8(c.batch, c.n_queries, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size,
+                   c.dtype, c.num_workers, &s);
+    if (st == PKV_OK) st = check_workspace(c.workspace, c.ws_bytes, s);
+    if (st == PKV_OK)
+        st = do_plan(c.lens, c.table, c.batch, c.page_size, c.table_stride, c.num_workers,
+                     c.workspace, s, nullptr, stream);
+    return st == PKV_OK ? kv8_run(c, c.q, s, stream) : st;
+}
+
+// theta^(-2i/D) / 2 pi, its fraction as a 64-bit binary one.
+void set_turns(uint64_t* turns, double theta, int head_dim) {
+    for (int i = 0; i < 64; ++i) {
+        double f = 0.0;
+        if (i < head_dim / 2) {
+            f = pow(theta, -2.0 * i / head_dim) / 6.283185307179586476925;
+            f -= floor(f);
+            if (!(f >= 0.0 && f < 1.0)) f = 0.0;  // beyond double's range
+        }
+        turns[i] = (uint64_t)ldexp(f, 64);
+    }
+}
+
+// The append's arguments, checked on the host.  ALIAS: an output (the pools,
+// the scales, q_out) overlaps an input or another output; q_out may be q.
+pkv_status check_kv8_append(const pkv::Kv8AppendArgs& a, int head_dim) {
+    if (!a.k_new || !a.v_new || !a.table || !a.positions || (a.q && !a.q_out))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(a.k_new) || !aligned16(a.v_new) || !aligned16(a.q) || !aligned16(a.q_out) ||
+        !aligned16(a.k_pool) || !aligned16(a.v_pool) || !aligned16(a.scales))
+        return PKV_ERR_INVALID_ARG;
+    const size_t pool = (size_t)a.num_pages * a.n_kv_heads * a.page_size * head_dim;
+    const size_t sc = (size_t)a.num_pages * a.n_kv_heads * (a.page_size / pkv::kChunk) * 2;
+    const size_t row = (size_t)a.n_tokens * a.n_kv_heads * head_dim * 2;
+    const size_t qb = a.q ? (size_t)a.n_tokens * a.n_q_heads * head_dim * 2 : 0;
+    const void* outs[4] = {a.k_pool, a.v_pool, a.scales, a.q_out};
+    const size_t out_bytes[4] = {pool, pool, sc, qb};
+    const void* ins[8] = {a.k_new,     a.v_new,   a.q == a.q_out ? nullptr : a.q,
+                          a.table,     a.positions, a.seq_ids, a.q_norm_w, a.k_norm_w};
+    const size_t in_bytes[8] = {row, row, qb, (size_t)a.n_seqs * a.table_stride * 4,
+                                (size_t)a.n_tokens * 4, (size_t)a.n_tokens * 4,
+                                (size_t)head_dim * 2, (size_t)head_dim * 2};
+    for (int x = 0; x < 4; ++x) {
+        for (int y = 0; y < 8; ++y)
+            if (overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y])) return PKV_ERR_ALIAS;
+        for (int y = x + 1; y < 4; ++y)
+            if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return PKV_ERR_ALIAS;
+    }
+    return PKV_OK;
+}
+
+pkv_status kv8_append_impl(const pkv_pool* pool, const void* q, const void* k_new,
+                           const void* v_new, pkv_dtype dtype, const int32_t* page_table,
+                           int table_stride, int n_seqs, const int32_t* positions,
+                           const int32_t* seq_ids, int n_tokens, int n_q_heads, bool rope,
+                           double rope_theta, const void* q_norm_weight,
+                           const void* k_norm_weight, float norm_eps, void* q_out,
+                           uint32_t* dev_status, cudaStream_t stream) {
+    if (!pool || n_tokens < 0 || n_seqs < 0 || table_stride <= 0 || (rope && n_q_heads <= 0))
+        return PKV_ERR_INVALID_ARG;
+    if (pool->dtype != PKV_E4M3) return PKV_ERR_UNSUPPORTED;
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    if (rope && !(rope_theta > 0.0 && isfinite(rope_theta))) return PKV_ERR_INVALID_ARG;
+    if (!norm_args_ok(q_norm_weight, k_norm_weight, norm_eps)) return PKV_ERR_INVALID_ARG;
+    if (!seq_ids && n_tokens > n_seqs) return PKV_ERR_INVALID_ARG;
+    if (n_tokens == 0) return PKV_OK;
+    if (rope && !q) return PKV_ERR_INVALID_ARG;
+    pkv::Kv8AppendArgs a = {};
+    a.q = q;
+    a.q_out = q_out;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_pool = static_cast<uint8_t*>(pool->k);
+    a.v_pool = static_cast<uint8_t*>(pool->v);
+    a.scales = static_cast<uint8_t*>(pool->scales);
+    a.table = page_table;
+    a.positions = positions;
+    a.seq_ids = seq_ids;
+    a.n_tokens = n_tokens;
+    a.n_seqs = n_seqs;
+    a.table_stride = table_stride;
+    a.n_q_heads = n_q_heads;
+    a.n_kv_heads = pool->n_kv_heads;
+    a.page_size = pool->page_size;
+    a.num_pages = pool->num_pages;
+    a.bf16 = dtype == PKV_BF16;
+    a.rope = rope;
+    a.q_norm_w = q_norm_weight;
+    a.k_norm_w = k_norm_weight;
+    a.norm_eps = norm_eps;
+    if (rope) set_turns(a.turns, rope_theta, pool->head_dim);
+    const pkv_status st = check_kv8_append(a, pool->head_dim);
+    if (st != PKV_OK) return st;
+    return cuda_status(pkv::launch_kv8_append(a, pool->head_dim, dev_status, stream));
+}
+}  // namespace
+
+extern "C" {
+
+pkv_status kv8_append(const pkv_pool* pool, const void* k_new, const void* v_new, pkv_dtype dtype,
+                      const int32_t* page_table, int table_stride, int n_seqs,
+                      const int32_t* positions, const int32_t* seq_ids, int n_tokens,
+                      uint32_t* dev_status, pkv_stream stream) {
+    return kv8_append_impl(pool, nullptr, k_new, v_new, dtype, page_table, table_stride, n_seqs,
+                           positions, seq_ids, n_tokens, 0, false, 0.0, nullptr, nullptr, 0.f,
+                           nullptr, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status kv8_append_rope(const pkv_pool* pool, const void* q, const void* k_new,
+                           const void* v_new, pkv_dtype dtype, const int32_t* page_table,
+                           int table_stride, int n_seqs, const int32_t* positions,
+                           const int32_t* seq_ids, int n_tokens, int n_q_heads,
+                           double rope_theta, const void* q_norm_weight,
+                           const void* k_norm_weight, float norm_eps, void* q_out,
+                           uint32_t* dev_status, pkv_stream stream) {
+    return kv8_append_impl(pool, q, k_new, v_new, dtype, page_table, table_stride, n_seqs,
+                           positions, seq_ids, n_tokens, n_q_heads, true, rope_theta,
+                           q_norm_weight, k_norm_weight, norm_eps, q_out, dev_status,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_decode_kv8_workspace_size(int batch, int n_queries, int n_q_heads,
+                                           int n_kv_heads, int head_dim, int num_workers,
+                                           size_t* bytes) {
+    if (!bytes) return PKV_ERR_INVALID_ARG;
+    *bytes = 0;
+    DecodeSetup s;
+    const pkv_status st = setup_kv8(batch, n_queries, n_q_heads, n_kv_heads, head_dim, 16,
+                                    PKV_BF16, num_workers, &s);
+    if (st == PKV_OK) *bytes = s.ws.total;
+    return st;
+}
+
+pkv_status paged_decode_attention_kv8(const void* q, const void* k_pool, const void* v_pool,
+                                      const void* scales, const int32_t* page_table,
+                                      int table_stride, const int32_t* context_lens, int batch,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                      int num_pages, pkv_dtype dtype, float scale, void* out,
+                                      void* workspace, size_t ws_bytes, int num_workers,
+                                      pkv_stream stream) {
+    const Kv8Call c = {q, k_pool, v_pool, scales, page_table, table_stride, context_lens, batch,
+                       1, n_q_heads, n_kv_heads, head_dim, page_size, num_pages, dtype, scale,
+                       out, workspace, ws_bytes, num_workers};
+    return kv8_attention(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_decode_attention_multi_kv8(
+    const void* q, const void* k_pool, const void* v_pool, const void* scales,
+    const int32_t* page_table, int table_stride, const int32_t* context_lens, int batch,
+    int n_queries, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int num_pages,
+    pkv_dtype dtype, float scale, void* out, void* workspace, size_t ws_bytes, int num_workers,
+    pkv_stream stream) {
+    const Kv8Call c = {q, k_pool, v_pool, scales, page_table, table_stride, context_lens, batch,
+                       n_queries, n_q_heads, n_kv_heads, head_dim, page_size, num_pages, dtype,
+                       scale, out, workspace, ws_bytes, num_workers};
+    return kv8_attention(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int32_t* positions,
+                                 const void* q, void* k_pool, void* v_pool, void* scales,
+                                 const int32_t* page_table, int table_stride,
+                                 const int32_t* context_lens, int batch, int n_q_heads,
+                                 int n_kv_heads, int head_dim, int page_size, int num_pages,
+                                 pkv_dtype dtype, float scale, double rope_theta,
+                                 const void* q_norm_weight, const void* k_norm_weight,
+                                 float norm_eps, void* out, void* workspace, size_t ws_bytes,
+                                 int num_workers, pkv_stream stream) {
+    if (!(rope_theta >= 0.0 && isfinite(rope_theta))) return PKV_ERR_INVALID_ARG;
+    const bool rope = rope_theta > 0.0;
+    if (!rope && (q_norm_weight || k_norm_weight)) return PKV_ERR_INVALID_ARG;
+    if (!norm_args_ok(q_norm_weight, k_norm_weight, norm_eps)) return PKV_ERR_INVALID_ARG;
+    const Kv8Call c = {q, k_pool, v_pool, scales, page_table, table_stride, context_lens, batch,
+                       1, n_q_heads, n_kv_heads, head_dim, page_size, num_pages, dtype, scale,
+                       out, workspace, ws_bytes, num_workers};
+    pkv_status st = validate_kv8(c);
+    if (st != PKV_OK || batch == 0) return st;
+    pkv::Kv8AppendArgs a = {};
+    a.q = rope ? q : nullptr;
+    a.q_out = rope ? out : nullptr;  // the decode reads the rotated q from here
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_pool = static_cast<uint8_t*>(k_pool);
+    a.v_pool = static_cast<uint8_t*>(v_pool);
+    a.scales = static_cast<uint8_t*>(scales);
+    a.table = page_table;
+    a.positions = positions;
+    a.n_tokens = batch;
+    a.n_seqs = batch;
+    a.table_stride = table_stride;
+    a.n_q_heads = n_q_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.bf16 = dtype == PKV_BF16;
+    a.rope = rope;
+    a.q_norm_w = q_norm_weight;
+    a.k_norm_w = k_norm_weight;
+    a.norm_eps = norm_eps;
+    if ((st = check_kv8_append(a, head_dim)) != PKV_OK) return st;
+    const size_t row = (size_t)batch * n_kv_heads * head_dim * 2;
+    if (overlaps(out, c.qo_bytes(), k_new, row) || overlaps(out, c.qo_bytes(), v_new, row) ||
+        overlaps(out, c.qo_bytes(), positions, (size_t)batch * 4))
+        return PKV_ERR_ALIAS;
+    if (rope) set_turns(a.turns, rope_theta, head_dim);
+    DecodeSetup s;
+    st = setup_kv8(batch, 1, n_q_heads, n_kv_heads, head_dim, page_size, dtype, num_workers, &s);
+    if (st == PKV_OK) st = check_workspace(workspace, ws_bytes, s);
+    if (st != PKV_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if ((st = do_plan(context_lens, page_table, batch, page_size, table_stride, num_workers,
+                      workspace, s, nullptr, cs)) != PKV_OK)
+        return st;
+    WsHeader* hdr = static_cast<WsHeader*>(workspace);
+    if ((st = cuda_status(pkv::launch_kv8_append(a, head_dim, &hdr->status, cs))) != PKV_OK)
+        return st;
+    return kv8_run(c, rope ? out : q, s, cs);
 }
 
 }  // extern "C"

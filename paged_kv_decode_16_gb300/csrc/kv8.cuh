@@ -1,0 +1,109 @@
+// kv8.cuh -- the 8-bit cache: its element and scale formats, and the launchers
+// of the kernels that write and read it.
+//
+// Elements are e4m3 (4 exponent bits, 3 of fraction, largest value 448, no
+// infinity); every block of 16 tokens of a page has, for each KV head and each
+// side (K, V), one scale 2^e, stored as E8M0 (the byte e + 127) in
+// scales[page][head][block][side].  Powers of two because a block fills up one
+// token at a time: when a later token needs a larger scale, the rows already
+// there move to it with no second rounding, except where they fall below
+// e4m3's smallest normal value.  (A scale of amax / 448 would round every
+// earlier row again at each step up.)
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace pkv {
+
+// Range of the scales' exponents.  100 binary orders: the attention keeps one
+// running maximum for p * 2^e and the softmax's sum alike, and fp32 holds the
+// sum's terms of both ends beside each other that far apart (kv8_decode.cuh).
+constexpr int kKv8MinExp = -60;
+constexpr int kKv8MaxExp = 40;
+
+// The smallest e with a <= 448 * 2^e, within the range; a >= 0, finite.
+__host__ __device__ __forceinline__ int kv8_need_exp(float a) {
+#ifdef __CUDA_ARCH__
+    const uint32_t u = __float_as_uint(a);
+#else
+    union { float f; uint32_t u; } x = {a};
+    const uint32_t u = x.u;
+#endif
+    // a = m 2^x, m in [1, 2): 448 = 1.75 * 2^8 (subnormal a: below the range)
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < kKv8MinExp ? kKv8MinExp : (e > kKv8MaxExp ? kKv8MaxExp : e);
+}
+
+__host__ __device__ __forceinline__ int kv8_clamp_exp(int e) {
+    return e < kKv8MinExp ? kKv8MinExp : (e > kKv8MaxExp ? kKv8MaxExp : e);
+}
+
+// 2^e, e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Four e4m3 bytes -> two half2 words (every e4m3 value is an fp16 value).
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// Two floats -> two e4m3 bytes (a in the low one), to nearest even, beyond 448
+// to 448; NaN stays NaN.
+__device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// --- decode (kv8_decode.cuh) ------------------------------------------------
+struct Kv8DecodeParams {
+    DecodeParams d;          // q, out 16-bit; pools e4m3
+    const uint16_t* scales;  // one word a block: the K scale's byte, then the V scale's
+    int gs;                  // rows of a full unit (the partial states' layout)
+};
+
+// Launch configuration of one instantiation (the kernel also takes the K and V
+// tensor maps).
+struct Kv8DecodeInfo {
+    void (*fn)(Kv8DecodeParams, CUtensorMap, CUtensorMap) = nullptr;
+    int warps = 0;
+    int stages = 0;
+    int smem_bytes = 0;
+};
+
+// rows: query rows of a unit, 1 .. 32.
+Kv8DecodeInfo kv8_decode_info_bf16(int head_dim, int rows);
+Kv8DecodeInfo kv8_decode_info_f16(int head_dim, int rows);
+
+// --- append (kv8_append.cu) -------------------------------------------------
+struct Kv8AppendArgs {
+    const void* q;       // [tokens][Hq][D] (null: no queries to rotate)
+    void* q_out;
+    const void* k_new;   // [tokens][Hkv][D]
+    const void* v_new;
+    uint8_t* k_pool;     // [NP][Hkv][P][D] e4m3
+    uint8_t* v_pool;
+    uint8_t* scales;     // [NP][Hkv][P / 16][2]
+    const int32_t* table;      // [n_seqs][table_stride]
+    const int32_t* positions;  // [tokens], < 0: not appended
+    const int32_t* seq_ids;    // [tokens] table row of each token; null: token i's is row i
+    int n_tokens, n_seqs, table_stride, n_q_heads, n_kv_heads, page_size, num_pages;
+    int bf16;            // element type of q, k_new, v_new: bf16, else fp16
+    int rope;            // rotate q and k_new
+    const void* q_norm_w;  // null: no norm on that side
+    const void* k_norm_w;
+    float norm_eps;
+    uint64_t turns[64];  // theta^(-2i/D) / 2 pi, its fraction times 2^64
+};
+
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* status,
+                              cudaStream_t stream);
+
+}  // namespace pkv

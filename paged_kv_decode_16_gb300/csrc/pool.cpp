@@ -17,50 +17,107 @@
 
 extern "C" {
 
-pkv_status kv_pool_create(int num_pages, int page_size, int n_kv_heads, int head_dim,
-                          pkv_dtype dtype, void* k_pool, void* v_pool, pkv_pool** out) {
-    if (!out) return PKV_ERR_INVALID_ARG;
-    *out = nullptr;
-    if (num_pages <= 0 || page_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
-        return PKV_ERR_INVALID_ARG;
-    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
-    if ((k_pool == nullptr) != (v_pool == nullptr)) return PKV_ERR_INVALID_ARG;
-    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    if (page_size % 16 != 0 || page_size > 256) return PKV_ERR_UNSUPPORTED;
-    if (k_pool && ((reinterpret_cast<uintptr_t>(k_pool) | reinterpret_cast<uintptr_t>(v_pool)) & 15))
-        return PKV_ERR_INVALID_ARG;
+// Everything of a pool but its memory; nullptr without host memory for it.
+static pkv_pool* new_pool(int num_pages, int page_size, int n_kv_heads, int head_dim,
+                          pkv_dtype dtype) {
     pkv_pool* p = new (std::nothrow) pkv_pool();
-    if (!p) return PKV_ERR_INVALID_ARG;
+    if (!p) return nullptr;
     p->num_pages = num_pages;
     p->page_size = page_size;
     p->n_kv_heads = n_kv_heads;
     p->head_dim = head_dim;
     p->dtype = dtype;
-    if (k_pool) {
-        p->k = k_pool;
-        p->v = v_pool;
-        p->owned = false;
-    } else {
-        const size_t bytes = (size_t)num_pages * n_kv_heads * page_size * head_dim * 2;
-        if (cudaGetDevice(&p->device) != cudaSuccess || cudaMalloc(&p->k, bytes) != cudaSuccess) {
-            delete p;
-            return PKV_ERR_CUDA;
-        }
-        if (cudaMalloc(&p->v, bytes) != cudaSuccess) {
-            cudaFree(p->k);
-            delete p;
-            return PKV_ERR_CUDA;
-        }
-        p->owned = true;
-    }
     try {
         p->refcount.assign(num_pages, 0);
         p->free_list.resize(num_pages);
         for (int i = 0; i < num_pages; ++i) p->free_list[i] = num_pages - 1 - i;
     } catch (...) {
-        if (p->owned) { cudaFree(p->k); cudaFree(p->v); }
         delete p;
+        return nullptr;
+    }
+    return p;
+}
+
+static pkv_status check_pool_shape(int num_pages, int page_size, int n_kv_heads, int head_dim) {
+    if (num_pages <= 0 || page_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
         return PKV_ERR_INVALID_ARG;
+    return PKV_OK;
+}
+
+static pkv_status check_pool_built(int page_size, int head_dim) {
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0 || page_size > 256) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// Device memory of an owned pool: `bytes` for each side and, unless 0,
+// scale_bytes for the scales (zeroed: the smallest scale).
+static pkv_status allocate_pool(pkv_pool* p, size_t bytes, size_t scale_bytes) {
+    bool ok = cudaGetDevice(&p->device) == cudaSuccess &&
+              cudaMalloc(&p->k, bytes) == cudaSuccess && cudaMalloc(&p->v, bytes) == cudaSuccess;
+    if (ok && scale_bytes)
+        ok = cudaMalloc(&p->scales, scale_bytes) == cudaSuccess &&
+             cudaMemset(p->scales, 0, scale_bytes) == cudaSuccess;
+    if (ok) {
+        p->owned = true;
+        return PKV_OK;
+    }
+    cudaFree(p->k);
+    cudaFree(p->v);
+    cudaFree(p->scales);
+    return PKV_ERR_CUDA;
+}
+
+pkv_status kv_pool_create(int num_pages, int page_size, int n_kv_heads, int head_dim,
+                          pkv_dtype dtype, void* k_pool, void* v_pool, pkv_pool** out) {
+    if (!out) return PKV_ERR_INVALID_ARG;
+    *out = nullptr;
+    pkv_status st = check_pool_shape(num_pages, page_size, n_kv_heads, head_dim);
+    if (st != PKV_OK) return st;
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    if ((k_pool == nullptr) != (v_pool == nullptr)) return PKV_ERR_INVALID_ARG;
+    if ((st = check_pool_built(page_size, head_dim)) != PKV_OK) return st;
+    if (k_pool && ((reinterpret_cast<uintptr_t>(k_pool) | reinterpret_cast<uintptr_t>(v_pool)) & 15))
+        return PKV_ERR_INVALID_ARG;
+    pkv_pool* p = new_pool(num_pages, page_size, n_kv_heads, head_dim, dtype);
+    if (!p) return PKV_ERR_INVALID_ARG;
+    p->k = k_pool;
+    p->v = v_pool;
+    if (!k_pool) {
+        st = allocate_pool(p, (size_t)num_pages * n_kv_heads * page_size * head_dim * 2, 0);
+        if (st != PKV_OK) {
+            delete p;
+            return st;
+        }
+    }
+    *out = p;
+    return PKV_OK;
+}
+
+pkv_status kv8_pool_create(int num_pages, int page_size, int n_kv_heads, int head_dim,
+                           void* k_pool, void* v_pool, void* scales, pkv_pool** out) {
+    if (!out) return PKV_ERR_INVALID_ARG;
+    *out = nullptr;
+    pkv_status st = check_pool_shape(num_pages, page_size, n_kv_heads, head_dim);
+    if (st != PKV_OK) return st;
+    if ((k_pool == nullptr) != (v_pool == nullptr) || (k_pool == nullptr) != (scales == nullptr))
+        return PKV_ERR_INVALID_ARG;
+    if ((st = check_pool_built(page_size, head_dim)) != PKV_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(k_pool) | reinterpret_cast<uintptr_t>(v_pool) |
+         reinterpret_cast<uintptr_t>(scales)) & 15)
+        return PKV_ERR_INVALID_ARG;
+    pkv_pool* p = new_pool(num_pages, page_size, n_kv_heads, head_dim, PKV_E4M3);
+    if (!p) return PKV_ERR_INVALID_ARG;
+    p->k = k_pool;
+    p->v = v_pool;
+    p->scales = scales;
+    if (!k_pool) {
+        const size_t rows = (size_t)num_pages * n_kv_heads * page_size;
+        st = allocate_pool(p, rows * head_dim, rows / 16 * 2);
+        if (st != PKV_OK) {
+            delete p;
+            return st;
+        }
     }
     *out = p;
     return PKV_OK;
@@ -75,6 +132,7 @@ pkv_status kv_pool_destroy(pkv_pool* pool) {
         if (prev != pool->device) cudaSetDevice(pool->device);
         if (cudaFree(pool->k) != cudaSuccess) st = PKV_ERR_CUDA;
         if (cudaFree(pool->v) != cudaSuccess) st = PKV_ERR_CUDA;
+        if (cudaFree(pool->scales) != cudaSuccess) st = PKV_ERR_CUDA;
         if (prev != pool->device) cudaSetDevice(prev);
     }
     delete pool;
@@ -83,6 +141,7 @@ pkv_status kv_pool_destroy(pkv_pool* pool) {
 
 void* kv_pool_k(const pkv_pool* pool) { return pool ? pool->k : nullptr; }
 void* kv_pool_v(const pkv_pool* pool) { return pool ? pool->v : nullptr; }
+void* kv8_pool_scales(const pkv_pool* pool) { return pool ? pool->scales : nullptr; }
 
 pkv_status kv_pool_info(const pkv_pool* pool, int* num_pages, int* page_size, int* n_kv_heads,
                         int* head_dim, pkv_dtype* dtype) {

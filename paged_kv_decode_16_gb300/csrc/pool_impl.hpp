@@ -11,7 +11,8 @@ struct pkv_pool {
     pkv_dtype dtype = PKV_BF16;
     void* k = nullptr;
     void* v = nullptr;
-    bool owned = false;   // k / v were allocated by kv_pool_create
+    void* scales = nullptr;  // 8-bit pools: [page][head][block][side] E8M0 bytes
+    bool owned = false;   // k / v (and scales) were allocated by the create call
     int device = 0;       // device of owned memory
     std::mutex mu;        // guards the allocator state below
     std::vector<int32_t> free_list;  // stack; back() is handed out next
