@@ -1533,47 +1533,81 @@ pkv_status validate_kv8(const Kv8Call& c) {
     return PKV_OK;
 }
 
-// Decode and combine on a planned workspace; q: the call's, or the rotated ones.
-pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, cudaStream_t stream) {
+// Words of the workspace's flags: the workers' (whole CTAs), then the CTAs' of
+// a step's append.
+int kv8_flag_words(const DecodeSetup& s, int batch) {
+    const int warps = s.kernel.warps();
+    return (s.workers + warps - 1) / warps * warps + pkv::kv8_append_ctas(batch);
+}
+
+size_t kv8_ws_bytes(const DecodeSetup& s, int batch) {
+    return s.ws.total + align256((size_t)kv8_flag_words(s, batch) * 4);
+}
+
+pkv_status check_kv8_workspace(const Kv8Call& c, const DecodeSetup& s) {
+    return c.ws_bytes < kv8_ws_bytes(s, c.batch) ? PKV_ERR_WORKSPACE : PKV_OK;
+}
+
+// The decode: the plan kernel for large batches, the decode kernel, the
+// combine.  q: the call's queries, or the rotated ones; append_flags: whether a
+// step's append left its flags.
+pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool append_flags,
+                   cudaStream_t stream) {
     uint8_t* ws = static_cast<uint8_t*>(c.workspace);
-    pkv::Kv8DecodeParams kp;
-    pkv::DecodeParams& p = kp.d;
+    const int warps = s.kernel.warps();
+    const int ctas = (s.workers + warps - 1) / warps;
+    pkv::Kv8DecodeParams p = {};
     p.q = q;
-    p.k_pool = c.k_pool;
-    p.v_pool = c.v_pool;
-    p.table = c.table;
-    p.lens_eff = reinterpret_cast<const int32_t*>(ws + s.ws.lens_eff);
-    p.prefix = reinterpret_cast<const int32_t*>(ws + s.ws.prefix);
-    p.wstart = reinterpret_cast<const int32_t*>(ws + s.ws.wstart);
-    p.units = (int)s.units;
-    p.hdr = reinterpret_cast<const WsHeader*>(ws);
-    p.status = &reinterpret_cast<WsHeader*>(ws)->status;
-    p.partials = reinterpret_cast<float*>(ws + s.ws.partials);
-    p.unit_done = nullptr;
-    p.all_partials = 0;
-    p.rows = s.rs;
     p.out = c.out;
-    p.table_stride = c.table_stride;
+    p.table = c.table;
+    p.lens = c.lens;
+    p.scales = static_cast<const uint16_t*>(c.scales);
+    p.hdr = reinterpret_cast<WsHeader*>(ws);
+    p.prefix = reinterpret_cast<int32_t*>(ws + s.ws.prefix);
+    p.flags = reinterpret_cast<uint32_t*>(ws + s.ws.total);
+    p.partials = reinterpret_cast<float*>(ws + s.ws.partials);
+    p.rows = s.rs;
+    p.gs = s.gs;
+    p.self_plan = c.batch <= pkv::kKv8SelfPlan;
+    p.unit_cost = p.self_plan ? pkv::kKv8UnitCost : 0;
+    p.workers_req = c.num_workers;
+    p.workers_auto = s.workers_auto;
     p.batch = c.batch;
-    p.n_q_heads = c.n_q_heads;
     p.n_kv_heads = c.n_kv_heads;
-    p.page_size = c.page_size;
-    p.num_pages = c.num_pages;
-    p.group = s.group;
     p.sub_groups = s.sub_groups;
+    p.units_per_b = s.units_per_b;
+    p.num_pages = c.num_pages;
+    p.table_stride = c.table_stride;
+    p.chunks_per_page = c.page_size / pkv::kChunk;
+    p.cap = (long long)c.table_stride * c.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
-    kp.scales = static_cast<const uint16_t*>(c.scales);
-    kp.gs = s.gs;
     CUtensorMap km, vm;
     const long long rows = (long long)c.num_pages * c.n_kv_heads * c.page_size;
     pkv_status st = kv8_map(c.k_pool, rows, c.head_dim, &km);
     if (st == PKV_OK) st = kv8_map(c.v_pool, rows, c.head_dim, &vm);
+    if (st == PKV_OK && !p.self_plan)
+        st = do_plan(c.lens, nullptr, c.batch, c.page_size, c.table_stride, c.num_workers,
+                     c.workspace, s, nullptr, stream);
+    if (st == PKV_OK)
+        st = cuda_status(pkv::launch_pdl(s.kernel.q8.fn, dim3(ctas), dim3(warps * 32),
+                                         s.kernel.smem(), stream, p, km, vm));
     if (st != PKV_OK) return st;
-    const int warps = s.kernel.warps();
-    st = cuda_status(pkv::launch_pdl(s.kernel.q8.fn, dim3((s.workers + warps - 1) / warps),
-                                     dim3(warps * 32), s.kernel.smem(), stream, kp, km, vm));
-    if (st != PKV_OK) return st;
-    return do_combine(c.batch, c.n_q_heads, c.head_dim, c.dtype, c.out, c.workspace, s, stream);
+    pkv::Kv8CombineArgs a = {};
+    a.partials = p.partials;
+    a.prefix = p.prefix;
+    a.hdr = p.hdr;
+    a.flags = p.flags;
+    a.n_flags = ctas * warps + (append_flags ? pkv::kv8_append_ctas(c.batch) : 0);
+    a.self_plan = p.self_plan;
+    a.unit_cost = p.unit_cost;
+    a.out = c.out;
+    a.units = (int)s.units;
+    a.units_per_b = s.units_per_b;
+    a.sub_groups = s.sub_groups;
+    a.gs = s.gs;
+    a.rows = s.rs;
+    return cuda_status(
+        pkv::launch_kv8_combine(c.dtype == PKV_BF16, c.head_dim, a, s.workers, stream));
 }
 
 pkv_status kv8_attention(const Kv8Call& c, cudaStream_t stream) {
@@ -1582,11 +1616,8 @@ pkv_status kv8_attention(const Kv8Call& c, cudaStream_t stream) {
     DecodeSetup s;
     st = setup_kv8(c.batch, c.n_queries, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size,
                    c.dtype, c.num_workers, &s);
-    if (st == PKV_OK) st = check_workspace(c.workspace, c.ws_bytes, s);
-    if (st == PKV_OK)
-        st = do_plan(c.lens, c.table, c.batch, c.page_size, c.table_stride, c.num_workers,
-                     c.workspace, s, nullptr, stream);
-    return st == PKV_OK ? kv8_run(c, c.q, s, stream) : st;
+    if (st == PKV_OK) st = check_kv8_workspace(c, s);
+    return st == PKV_OK ? kv8_run(c, c.q, s, false, stream) : st;
 }
 
 // theta^(-2i/D) / 2 pi, its fraction as a 64-bit binary one.
@@ -1672,7 +1703,7 @@ pkv_status kv8_append_impl(const pkv_pool* pool, const void* q, const void* k_ne
     if (rope) set_turns(a.turns, rope_theta, pool->head_dim);
     const pkv_status st = check_kv8_append(a, pool->head_dim);
     if (st != PKV_OK) return st;
-    return cuda_status(pkv::launch_kv8_append(a, pool->head_dim, dev_status, stream));
+    return cuda_status(pkv::launch_kv8_append(a, pool->head_dim, dev_status, nullptr, stream));
 }
 }  // namespace
 
@@ -1708,7 +1739,7 @@ pkv_status paged_decode_kv8_workspace_size(int batch, int n_queries, int n_q_hea
     DecodeSetup s;
     const pkv_status st = setup_kv8(batch, n_queries, n_q_heads, n_kv_heads, head_dim, 16,
                                     PKV_BF16, num_workers, &s);
-    if (st == PKV_OK) *bytes = s.ws.total;
+    if (st == PKV_OK) *bytes = kv8_ws_bytes(s, batch);
     return st;
 }
 
@@ -1785,16 +1816,14 @@ pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int
     if (rope) set_turns(a.turns, rope_theta, head_dim);
     DecodeSetup s;
     st = setup_kv8(batch, 1, n_q_heads, n_kv_heads, head_dim, page_size, dtype, num_workers, &s);
-    if (st == PKV_OK) st = check_workspace(workspace, ws_bytes, s);
+    if (st == PKV_OK) st = check_kv8_workspace(c, s);
     if (st != PKV_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if ((st = do_plan(context_lens, page_table, batch, page_size, table_stride, num_workers,
-                      workspace, s, nullptr, cs)) != PKV_OK)
+    uint32_t* flags = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + s.ws.total) +
+                      (kv8_flag_words(s, batch) - pkv::kv8_append_ctas(batch));
+    if ((st = cuda_status(pkv::launch_kv8_append(a, head_dim, nullptr, flags, cs))) != PKV_OK)
         return st;
-    WsHeader* hdr = static_cast<WsHeader*>(workspace);
-    if ((st = cuda_status(pkv::launch_kv8_append(a, head_dim, &hdr->status, cs))) != PKV_OK)
-        return st;
-    return kv8_run(c, rope ? out : q, s, cs);
+    return kv8_run(c, rope ? out : q, s, true, cs);
 }
 
 }  // extern "C"

@@ -63,10 +63,50 @@ __device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
 }
 
 // --- decode (kv8_decode.cuh) ------------------------------------------------
+// Batches up to this size: every CTA of the decode kernel works the ranges out
+// for itself; larger ones: the plan kernel does, once.
+constexpr int kKv8SelfPlan = 256;
+// A unit's start (its queries, its result) counts as this many chunks when the
+// ranges are cut.
+constexpr int kKv8UnitCost = 4;
+// Automatic worker count: at least this many positions each.
+constexpr int kKv8MinPositions = 4;
+
+// Workers and the split of `total` positions over them: sw each, one more for
+// the first r.
+__host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, int workers_auto,
+                                                    int* nw, int* sw, int* r) {
+    int n;
+    if (workers_req > 0) {
+        n = workers_req < total ? workers_req : total;
+    } else {
+        n = total / kKv8MinPositions + (total % kKv8MinPositions ? 1 : 0);
+        if (n > workers_auto) n = workers_auto;
+    }
+    *nw = n;
+    *sw = n > 0 ? total / n : 0;
+    *r = n > 0 ? total - *sw * n : 0;
+}
+
 struct Kv8DecodeParams {
-    DecodeParams d;          // q, out 16-bit; pools e4m3
+    const void* q;        // [B][n_queries][Hq][D]
+    void* out;
+    const int32_t* table;   // [B][table_stride]
+    const int32_t* lens;    // [B], the caller's
     const uint16_t* scales;  // one word a block: the K scale's byte, then the V scale's
-    int gs;                  // rows of a full unit (the partial states' layout)
+    WsHeader* hdr;          // ranges: written by this kernel (self_plan) or the plan kernel
+    int32_t* prefix;        // [B + 1] first position of every sequence: likewise
+    uint32_t* flags;        // [workers rounded up to whole CTAs] PKV_DEV_* bits of every worker
+    float* partials;        // [slots][partial_slot_floats(gs, D)]
+    RowShape rows;
+    int gs;                 // rows of a full unit (the partial states' layout)
+    int self_plan;
+    int unit_cost;          // positions a unit has beside its chunks
+    int workers_req, workers_auto;
+    int batch, n_kv_heads, sub_groups, units_per_b, num_pages, table_stride;
+    int chunks_per_page;
+    long long cap;          // tokens of a table row
+    float scale_log2;       // scale * log2(e)
 };
 
 // Launch configuration of one instantiation (the kernel also takes the K and V
@@ -81,6 +121,23 @@ struct Kv8DecodeInfo {
 // rows: query rows of a unit, 1 .. 32.
 Kv8DecodeInfo kv8_decode_info_bf16(int head_dim, int rows);
 Kv8DecodeInfo kv8_decode_info_f16(int head_dim, int rows);
+
+// Merges the units that several workers share, and sets the workspace's status
+// to the OR of n_flags words (and of the plan kernel's, when it ran).
+struct Kv8CombineArgs {
+    const float* partials;
+    const int32_t* prefix;
+    WsHeader* hdr;
+    const uint32_t* flags;
+    int n_flags;
+    int self_plan, unit_cost;
+    void* out;
+    int units, units_per_b, sub_groups, gs;
+    RowShape rows;
+};
+
+cudaError_t launch_kv8_combine(bool bf16, int head_dim, const Kv8CombineArgs& a, int workers,
+                               cudaStream_t stream);
 
 // --- append (kv8_append.cu) -------------------------------------------------
 struct Kv8AppendArgs {
@@ -103,7 +160,10 @@ struct Kv8AppendArgs {
     uint64_t turns[64];  // theta^(-2i/D) / 2 pi, its fraction times 2^64
 };
 
+// PKV_DEV_* bits of skipped runs: ORed into *status (nullable), or, with
+// flags, written to flags[CTA] for every CTA (kv8_append_ctas of them).
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* status,
-                              cudaStream_t stream);
+                              uint32_t* flags, cudaStream_t stream);
+int kv8_append_ctas(int n_tokens);
 
 }  // namespace pkv

@@ -197,7 +197,8 @@ __device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status) {
+kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status,
+                  uint32_t* flags) {
     constexpr int HALF = D / 2, HV = D / 16;
     __shared__ float ctab[kMaxSpan * HALF], stab[kMaxSpan * HALF];
     __shared__ float wq[D], wk[D];
@@ -207,6 +208,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int base = blockIdx.x * span;  // the CTA's leaders: tokens base .. base + span - 1
 
+    pdl_wait();
     if (a.q_norm_w || a.k_norm_w) {
         for (int x = tid; x < D; x += kThreads) {
             const T* q = static_cast<const T*>(a.q_norm_w);
@@ -215,7 +217,6 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
             wk[x] = k ? (float)k[x] : 1.f;
         }
     }
-    pdl_wait();
     if (warp == 0) {
         // token base + lane and the one before it; the last one a CTA can own
         // is base + span + 14, so lane 31 sees the next CTA's first leader
@@ -238,6 +239,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         const bool mine = first >= 0 && lane >= first && lane < end;
         // runs of the CTA: leaders among its tokens that are appended
         bool use = false;
+        uint32_t skipped = 0;
         Run r = {0, 0, 0, 0};
         if (mine && !cont && pos >= 0) {
             const unsigned next = lead & ~((2u << lane) - 1u);
@@ -256,10 +258,15 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
                 page = a.table[(long long)seq * a.table_stride + col];
                 if (page < 0 || page >= a.num_pages) bits = PKV_DEV_BAD_PAGE;
             }
-            if (bits) set_status(status, bits);
             use = bits == 0;
+            skipped = bits;
             r.blk = (long long)page * a.n_kv_heads * (a.page_size / kChunk) +
                     (pos % a.page_size) / kChunk;
+        }
+        skipped = __reduce_or_sync(kFull, skipped);
+        if (lane == 0) {
+            if (flags) flags[blockIdx.x] = skipped;
+            else if (skipped) set_status(status, skipped);
         }
         const unsigned used = __ballot_sync(kFull, use);
         if (use) s_runs[__popc(used & ((1u << lane) - 1u))] = r;
@@ -322,13 +329,21 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
 
 }  // namespace
 
+static int append_span(int n_tokens) { return n_tokens <= 2048 ? 1 : 16; }
+
+int kv8_append_ctas(int n_tokens) {
+    const int span = append_span(n_tokens);
+    return n_tokens / span + (n_tokens % span ? 1 : 0);
+}
+
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* status,
-                              cudaStream_t stream) {
+                              uint32_t* flags, cudaStream_t stream) {
     if (a.n_tokens <= 0) return cudaSuccess;
-    const int span = a.n_tokens <= 2048 ? 1 : 16;
-    const dim3 grid((unsigned)(((long long)a.n_tokens + span - 1) / span));
+    const int span = append_span(a.n_tokens);
+    const dim3 grid((unsigned)kv8_append_ctas(a.n_tokens));
 #define PKV_KV8_APPEND(T, D) \
-    return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), 0, stream, a, span, status)
+    return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), 0, stream, a, span, status, \
+                      flags)
     if (a.bf16) {
         if (head_dim == 128) PKV_KV8_APPEND(__nv_bfloat16, 128);
         PKV_KV8_APPEND(__nv_bfloat16, 64);

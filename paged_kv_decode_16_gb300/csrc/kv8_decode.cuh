@@ -1,10 +1,15 @@
 // kv8_decode.cuh -- decode attention over the 8-bit paged cache.
 //
-// Work split, chunk pipeline and partial states are those of the 16-bit kernel
-// (schedule.cuh, decode_mma.cuh): a warp per balanced range of 16-token
-// chunks, a ring of chunk buffers per warp filled by tensor copies, fp32
-// partial states merged by the combine kernel.  A chunk is exactly one block of
-// the cache, so it has one K scale 2^ek and one V scale 2^ev.
+// As in the 16-bit kernel (schedule.cuh, decode_mma.cuh) a warp takes a
+// balanced range of 16-token chunks through a ring of chunk buffers filled by
+// tensor copies, and units spread over several warps leave fp32 partial states
+// for a combine kernel.  A chunk is exactly one block of the cache, so it has
+// one K scale 2^ek and one V scale 2^ev.  What differs: half the bytes a chunk
+// leave half the time for everything beside them, so the ranges are worked out
+// by every CTA for itself (no plan kernel before this one, for batches of up to
+// kKv8SelfPlan sequences), they count a unit's start as kKv8UnitCost chunks
+// more, a unit's queries are fetched while the unit before it is at work, and
+// what is the same for a whole unit stays out of the loop over its chunks.
 //
 // Mathematics.  With x_t = (scale * log2 e) q.k8_t 2^ek(t) + ev(t), a running
 // reference m and p_t = 2^(x_t - m):
@@ -42,13 +47,79 @@
 
 namespace pkv {
 
-// The scales of a lane's chunk.
-struct Kv8Extra {
-    const uint16_t* scales;
-    uint32_t v;  // bytes: K, V
-    __device__ __forceinline__ void load(const ChunkDesc& d) {
-        v = d.off >= 0 ? (uint32_t)__ldg(scales + (d.off >> 4)) : 0u;
+// Positions.  Every unit (sequence, KV head, sub-group) with nch chunks has
+// cost + nch positions, its chunks the last nch; all units' positions are laid
+// end to end in unit order and cut into one range per worker, as in
+// schedule.cuh.  prefix[b]: the first position of sequence b.
+//
+// Lane x holds the description of position 32 n + x of its worker's range, for
+// the tile n that the consumer is in (a) and the next one (b), loaded a tile
+// ahead so that no wait for it is in the loop.
+struct Kv8Desc {
+    int row;        // first pool row of the chunk; -1: nothing to copy
+    uint32_t sc;    // its scales' bytes (K, V); bit 16 set: no tokens
+    int u, k, len;  // unit, chunk of the unit (< 0: a cost position), tokens of the sequence
+};
+
+struct Kv8Stream {
+    Kv8Desc a, b;
+    int tile;  // tile of a
+    int n;     // positions
+    int f0, b_lo, b_hi, lane;
+    uint32_t flags;  // PKV_DEV_* bits this lane has seen
+
+    __device__ __forceinline__ Kv8Desc describe(const Kv8DecodeParams& p, const int32_t* prefix,
+                                                int i) {
+        Kv8Desc d = {-1, 1u << 16, 0, 0, 0};
+        if (i >= n) return d;
+        const int f = f0 + i;
+        int lo = b_lo, hi = b_hi;  // the last sequence with prefix <= f: empty ones are passed over
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= f) lo = mid; else hi = mid;
+        }
+        const int first = prefix[lo];
+        const int per_unit = (prefix[lo + 1] - first) / p.units_per_b;
+        const int rem = f - first;
+        const int uidx = rem / per_unit;
+        d.u = lo * p.units_per_b + uidx;
+        d.k = rem - uidx * per_unit - p.unit_cost;
+        d.len = (int)min((long long)p.lens[lo], p.cap);
+        if (d.k < 0) return d;
+        const int col = d.k / p.chunks_per_page;
+        const int page = __ldg(p.table + (long long)lo * p.table_stride + col);
+        if (page >= 0 && page < p.num_pages) {
+            const int blk = (page * p.n_kv_heads + uidx / p.sub_groups) * p.chunks_per_page +
+                            (d.k - col * p.chunks_per_page);
+            d.row = blk * kChunk;  // below 2^31: checked on the host
+            d.sc = (uint32_t)__ldg(p.scales + blk);
+        } else {
+            flags |= PKV_DEV_BAD_PAGE;
+        }
+        return d;
     }
+    __device__ __forceinline__ void next(const Kv8DecodeParams& p, const int32_t* prefix) {
+        b = describe(p, prefix, (tile + 1) * 32 + lane);
+    }
+    // The consumer has come to position i; true: into a new tile.
+    __device__ __forceinline__ bool advance(const Kv8DecodeParams& p, const int32_t* prefix,
+                                            int i) {
+        if ((i >> 5) == tile) return false;
+        a = b;
+        ++tile;
+        next(p, prefix);
+        return true;
+    }
+    // Row, unit of position i (in tile a or b); the scales of one in tile a.
+    __device__ __forceinline__ int row(int i) const {
+        const int v = (i >> 5) == tile ? a.row : b.row;
+        return __shfl_sync(kFull, v, i & 31);
+    }
+    __device__ __forceinline__ int unit(int i) const {
+        const int v = (i >> 5) == tile ? a.u : b.u;
+        return __shfl_sync(kFull, v, i & 31);
+    }
+    __device__ __forceinline__ uint32_t sc(int i) const { return __shfl_sync(kFull, a.sc, i & 31); }
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -85,24 +156,89 @@ __device__ __forceinline__ uint32_t e4m3_nan_mask(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Shared memory of one CTA: every warp's ring of K/V stages, then (units of
-// more than 16 rows) every warp's query fragments, then the mbarriers.
+// Shared memory of one CTA: every warp's ring of chunks (K then V), its next
+// unit's query rows as they come (units of up to 16 rows), the query fragments
+// (larger units), the mbarriers, and the plan's prefix sums.
 template <int D, int NT, int STAGES, int WARPS>
 struct Kv8Layout {
-    static constexpr int kSide = kChunk * D;            // K or V bytes of a chunk
+    static constexpr int kSide = kChunk * D;  // K or V bytes of a chunk
     static constexpr int kStageBytes = 2 * kSide;
     static constexpr int kWarpKV = STAGES * kStageBytes;
     static constexpr bool kQShared = NT > 2;
-    static constexpr int kWarpQ = kQShared ? NT * 8 * D * 2 : 0;
+    static constexpr int kWarpQ = NT * 8 * D * 2;
     static constexpr int kOffQ = WARPS * kWarpKV;
     static constexpr int kOffBar = kOffQ + WARPS * kWarpQ;
-    static constexpr int kBytes = kOffBar + WARPS * STAGES * 8 + 1024;  // + alignment slack
+    static constexpr int kOffPlan = kOffBar + WARPS * STAGES * 8;
+    static constexpr int kBytes = kOffPlan + (kKv8SelfPlan + 1) * 4 + 1024;  // + alignment slack
 };
+
+// The ranges of the whole batch by one CTA: prefix sums into s_prefix, and the
+// positions' total.  CTA 0 leaves them in the workspace for the combine kernel.
+template <int THREADS>
+__device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* s_prefix,
+                                             uint32_t* flags) {
+    static_assert(kKv8SelfPlan % THREADS == 0, "whole sequences per thread");
+    constexpr int PER = kKv8SelfPlan / THREADS, NWARPS = THREADS / 32;
+    __shared__ long long s_tot[NWARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int cnt[PER];
+    long long sum = 0;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+        const int b = tid * PER + x;
+        long long len = b < p.batch ? p.lens[b] : 0;
+        if (len < 0 || len > p.cap) {
+            if (blockIdx.x == 0) *flags |= PKV_DEV_BAD_LEN;
+            len = len < 0 ? 0 : p.cap;
+        }
+        const int nch = (int)((len + kChunk - 1) / kChunk);
+        // a sequence of more positions than an int: over the limit in any case
+        const long long c = nch ? (long long)(nch + p.unit_cost) * p.units_per_b : 0;
+        cnt[x] = (int)min(c, 0x7fffffffLL);
+        sum += cnt[x];
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_tot[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) {
+        if (w < warp) before += s_tot[w];
+        total += s_tot[w];
+    }
+    if (total > 0x7fffffffLL) {  // beyond the 32-bit positions: refuse the work
+        if (blockIdx.x == 0) *flags |= PKV_DEV_BAD_LEN;
+        total = 0;
+    }
+    long long at = before + incl - sum;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+        const int b = tid * PER + x;
+        const int v = total ? (int)at : 0;
+        if (b <= p.batch) {
+            s_prefix[b] = v;
+            if (blockIdx.x == 0) p.prefix[b] = v;
+        }
+        at += cnt[x];
+    }
+    if (tid == THREADS - 1 && p.batch == kKv8SelfPlan) {
+        s_prefix[kKv8SelfPlan] = (int)total;
+        if (blockIdx.x == 0) p.prefix[kKv8SelfPlan] = (int)total;
+    }
+    __syncthreads();
+    return (int)total;
+}
 
 // NT tiles of 8 query rows; a unit has at most 8 NT rows.
 template <typename T, int D, int NT, int WARPS, int STAGES>
 __global__ void __launch_bounds__(WARPS * 32)
-kv8_decode_kernel(const Kv8DecodeParams kp, const __grid_constant__ CUtensorMap kmap,
+kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
+                  const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
     using Lay = Kv8Layout<D, NT, STAGES, WARPS>;
     constexpr int KSTEPS = D / 16;  // k-steps of S^T
@@ -113,7 +249,6 @@ kv8_decode_kernel(const Kv8DecodeParams kp, const __grid_constant__ CUtensorMap 
     // p stays below 2^8, far inside fp16, and after a range's first chunk the
     // accumulators are hardly ever rescaled
     constexpr float kSlack = 8.f;
-    const DecodeParams& p = kp.d;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -123,10 +258,10 @@ kv8_decode_kernel(const Kv8DecodeParams kp, const __grid_constant__ CUtensorMap 
     uint8_t* base = smem_raw + pad;
     uint8_t* wsm = base + warp * Lay::kWarpKV;
     const uint32_t wsm_u32 = raw + pad + warp * Lay::kWarpKV;
-    // query fragments in shared memory: 16-byte vector x of tile n at
-    // (n * KSTEPS / 2 + x) * 512 + lane * 16
+    // query rows: 16-byte vector x of tile n at (n * KSTEPS / 2 + x) * 512 + lane * 16
     const uint32_t sq = raw + pad + Lay::kOffQ + warp * Lay::kWarpQ + lane * 16;
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar) + warp * STAGES;
+    int32_t* s_prefix = reinterpret_cast<int32_t*>(base + Lay::kOffPlan);
 
     if (lane == 0) {
 #pragma unroll
@@ -140,218 +275,278 @@ kv8_decode_kernel(const Kv8DecodeParams kp, const __grid_constant__ CUtensorMap 
     __syncwarp();
     pdl_wait();
 
-    const int nw = p.hdr->num_workers;
     const int gw = blockIdx.x * WARPS + warp;
-    const int all_warps = gridDim.x * WARPS;
-    if (gw >= nw) {
-        zero_empty_sequences(p, D, gw, all_warps, lane);
-        return;
+    Kv8Stream ws;
+    ws.flags = 0;
+    ws.lane = lane;
+    ws.tile = 0;
+    ws.b_lo = 0;
+    ws.b_hi = p.batch;
+    const int32_t* prefix;
+    int nw, sw, r;
+    if (p.self_plan) {
+        const int total = kv8_self_plan<WARPS * 32>(p, s_prefix, &ws.flags);
+        prefix = s_prefix;
+        kv8_ranges(total, p.workers_req, p.workers_auto, &nw, &sw, &r);
+        if (gw == 0 && lane == 0) {
+            p.hdr->num_workers = nw;
+            p.hdr->chunks_per_worker = sw;
+            p.hdr->extra_chunks = r;
+        }
+    } else {
+        prefix = p.prefix;
+        nw = p.hdr->num_workers;
+        sw = p.hdr->chunks_per_worker;
+        r = p.hdr->extra_chunks;
     }
-    WorkStreamT<Kv8Extra> ws;
-    ws.xa.scales = ws.xb.scales = kp.scales;
-    ws.xa.v = ws.xb.v = 0u;
-    ws.init(p, lane, gw);
-    if (ws.stream_end == 0) {
-        zero_empty_sequences(p, D, gw, all_warps, lane);
-        return;
-    }
+    ws.f0 = range_begin(gw, sw, r);
+    ws.n = gw < nw ? sw + (gw < r ? 1 : 0) : 0;
+    ws.a = ws.describe(p, prefix, lane);
 
-    const int units_per_b = ws.units_per_b;
     const uint64_t kv_policy = l2_evict_first_policy();
     const int j = lane >> 2, t = lane & 3;
 
-    // Issue the copies of stream position i into stage i % STAGES; false past
-    // the end of the stream.
-    auto issue = [&](int i) -> bool {
-        if (!ws.covered(p, i)) return false;
-        const bool second = i >= ws.a_end();
-        const int src = i - (second ? ws.b_start : ws.a_start);
-        const long long off = __shfl_sync(kFull, second ? ws.wb.off : ws.wa.off, src);
+    // Copy the chunk of position i into stage st.
+    auto issue = [&](int i, int st) {
+        const int row = ws.row(i);
         if (lane == 0) {
-            const int st = i % STAGES;
+            uint64_t* bp = &bar[st];
+            uint8_t* dst = wsm + st * Lay::kStageBytes;
             fence_proxy_async_smem();
-            mbar_arrive_expect_tx(&bar[st], off >= 0 ? (uint32_t)Lay::kStageBytes : 0u);
-            if (off >= 0) {
-                uint8_t* stage = wsm + st * Lay::kStageBytes;
-                tma_load_2d_hint(stage, &kmap, 0, (int)off, &bar[st], kv_policy);
-                tma_load_2d_hint(stage + Lay::kSide, &vmap, 0, (int)off, &bar[st], kv_policy);
+            mbar_arrive_expect_tx(bp, row >= 0 ? (uint32_t)Lay::kStageBytes : 0u);
+            if (row >= 0) {
+                tma_load_2d_hint(dst, &kmap, 0, row, bp, kv_policy);
+                tma_load_2d_hint(dst + Lay::kSide, &vmap, 0, row, bp, kv_policy);
             }
         }
-        return true;
+    };
+    // Fetch this lane's part of the query rows of the unit of position i (its
+    // own 16-byte vectors only, so only this lane waits for them).
+    auto fetch_q = [&](int i) {
+        const int u = ws.unit(i);
+        const int b = u / p.units_per_b;
+        const int uidx = u - b * p.units_per_b;
+        const int h = uidx / p.sub_groups;
+        const int sg = uidx - h * p.sub_groups;
+        const int rows = p.rows.rows(sg);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            // lane (j, t) takes elements D/4 t .. of row 8n + j
+            const int rr = 8 * n + j;
+            const bool ok = rr < rows;
+            const T* src = static_cast<const T*>(p.q) +
+                           (ok ? p.rows.row(b, h, sg, rr) * D : 0) + t * (D / 4);
+#pragma unroll
+            for (int x = 0; x < KSTEPS / 2; ++x)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 sq + (n * (KSTEPS / 2) + x) * 512),
+                             "l"(src + x * 8), "r"(ok ? 16 : 0)
+                             : "memory");
+        }
     };
 
-    int issued = 0;
-    while (issued < STAGES && issue(issued)) ++issued;
-    zero_empty_sequences(p, D, gw, all_warps, lane);  // while the first copies are in flight
+    if (ws.n > 0) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+            if (s < ws.n) issue(s, s);
+        fetch_q(0);
+        ws.next(p, prefix);  // the second tile, behind the first copies
+    }
+    // rows of sequences with no tokens are zeros: no worker visits them
+    for (int b = gw; b < p.batch; b += gridDim.x * WARPS) {
+        if (prefix[b] != prefix[b + 1]) continue;
+        const long long vecs = (long long)p.rows.n_queries * p.rows.n_q_heads * D / 8;
+        uint4* dst = reinterpret_cast<uint4*>(p.out) + b * vecs;
+        for (long long x = lane; x < vecs; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+    }
 
-    uint32_t qf[Lay::kQShared ? 1 : NT][KSTEPS][2];  // B fragments of Q^T
-    float fs[NT][2];   // score factors of rows 2t, 2t+1 of a tile: scale log2(e) / row scale
-    float o[NT][MT][4];  // O^T: elements DPL j + 2i (c0, c1) and + 1 (c2, c3) of rows 2t, 2t+1
-    float m[NT][2], mr[NT][2];  // reference of rows 2t, 2t+1; the same with 0 for -inf
-    float l[NT][2];             // this lane's part of the rows' sums
-    int lim[NT][2];             // last token that rows 2t, 2t+1 see
-    int lim_min = 0;            // the smallest of the unit's
-    int seg_rows = 0, seg_slot = 0;
-    bool seg_whole_start = false;
-
-    auto give_up = [&](int from) {
-        if (lane == 0) set_status(p.status, PKV_DEV_TIMEOUT);
-        for (int i = from; i < issued; ++i)
-            mbar_wait_bounded(&bar[i % STAGES], (uint32_t)((i / STAGES) & 1));
+    int st = 0;          // stage of the position at hand
+    uint32_t phase = 0;  // its barrier's phase
+    int i = 0;           // position
+    bool q_coming = true;  // the next unit's query rows are on the way
+    // a position is done with: its stage takes the one STAGES further on
+    auto release = [&](int pos) {
+        __syncwarp();
+        if (pos + STAGES < ws.n) issue(pos + STAGES, st);
+        if (++st == STAGES) {
+            st = 0;
+            phase ^= 1u;
+        }
     };
+    while (i < ws.n) {
+        // ---- a segment: the positions of one unit in this range ----
+        ws.advance(p, prefix, i);
+        const int u = __shfl_sync(kFull, ws.a.u, i & 31);
+        int k0 = __shfl_sync(kFull, ws.a.k, i & 31);
+        const int len = __shfl_sync(kFull, ws.a.len, i & 31);
+        const int nch = (len + kChunk - 1) / kChunk;
+        if (!q_coming) fetch_q(i);
+        const int end = i + min(nch - k0, ws.n - i);
+        for (; k0 < 0 && i < end; ++i, ++k0) release(i);  // cost positions hold nothing
+        const int b = u / p.units_per_b;
+        const int uidx = u - b * p.units_per_b;
+        const int h = uidx / p.sub_groups;
+        const int sg = uidx - h * p.sub_groups;
+        const int rows = p.rows.rows(sg);
+        const int last = len - p.rows.n_queries;            // last token that query 0 sees
+        const int lim_min = last + p.rows.first_query(sg);  // the unit's first row's
 
-    for (int i = 0; i < ws.stream_end; ++i) {
-        ws.consumer_at(p, i, STAGES + 1);
-        const ChunkDesc d = ws.fetch(i);
-        const bool in_b = i >= ws.a_end();
-        const uint32_t sc = __shfl_sync(kFull, in_b ? ws.xb.v : ws.xa.v,
-                                        i - (in_b ? ws.b_start : ws.a_start));
-        const int st = i % STAGES;
-        if (ws.seg_start(i, d)) {
-            const int b = d.u / units_per_b;
-            const int uidx = d.u - b * units_per_b;
-            const int h = uidx / p.sub_groups;
-            const int sg = uidx - h * p.sub_groups;
-            seg_rows = p.rows.rows(sg);
-            seg_slot = ws.slot_base + d.u;
-            seg_whole_start = d.k == 0;
-            const int last = d.len - p.rows.n_queries;
-            lim_min = last + p.rows.first_query(sg);
+        uint32_t qf[Lay::kQShared ? 1 : NT][KSTEPS][2];  // B fragments of Q^T
+        float fs[NT][2];  // score factors of rows 2t, 2t+1 of a tile: scale log2(e) / row scale
+        float o[NT][MT][4];  // O^T: elements DPL j + 2i (c0, c1), + 1 (c2, c3) of rows 2t, 2t+1
+        float m[NT][2], mr[NT][2];  // reference of rows 2t, 2t+1; the same with 0 for -inf
+        float l[NT][2];             // this lane's part of the rows' sums
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                // lane (j, t) takes elements D/4 t .. of row 8n + j
-                uint32_t u[KSTEPS * 2];
-                const int r = 8 * n + j;
-                const bool ok = r < seg_rows;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const T*>(p.q) + (ok ? p.rows.row(b, h, sg, r) * D : 0) + t * (D / 4));
+        for (int n = 0; n < NT; ++n) {
+            uint32_t x4[KSTEPS * 2];
 #pragma unroll
-                for (int x = 0; x < KSTEPS / 2; ++x) {
-                    const uint4 v = ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-                    u[4 * x] = v.x;
-                    u[4 * x + 1] = v.y;
-                    u[4 * x + 2] = v.z;
-                    u[4 * x + 3] = v.w;
-                }
-                int shift = 0;  // the row is multiplied by 2^shift
+            for (int x = 0; x < KSTEPS / 2; ++x) {
+                const uint4 v = lds128(sq + (n * (KSTEPS / 2) + x) * 512);
+                x4[4 * x] = v.x;
+                x4[4 * x + 1] = v.y;
+                x4[4 * x + 2] = v.z;
+                x4[4 * x + 3] = v.w;
+            }
+            int shift = 0;  // the row is multiplied by 2^shift
+            if constexpr (kBf16) {
+                uint32_t mx = 0u;
+#pragma unroll
+                for (int x = 0; x < KSTEPS * 2; ++x) mx = __vmaxu2(mx, x4[x] & 0x7fff7fffu);
+                mx = max(mx & 0xffffu, mx >> 16);
+                mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
+                mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
+                shift = mx == 0u ? 0 : min(141 - (int)(mx >> 7), 126);
+                const float f = exp2i(shift);
+#pragma unroll
+                for (int x = 0; x < KSTEPS * 2; ++x)
+                    x4[x] = Cvt<__half>::pack2(__uint_as_float(x4[x] << 16) * f,
+                                               __uint_as_float(x4[x] & 0xffff0000u) * f);
+            }
+            if constexpr (Lay::kQShared) {
                 if constexpr (kBf16) {
-                    uint32_t mx = 0u;
-#pragma unroll
-                    for (int x = 0; x < KSTEPS * 2; ++x) mx = __vmaxu2(mx, u[x] & 0x7fff7fffu);
-                    mx = max(mx & 0xffffu, mx >> 16);
-                    mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
-                    mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
-                    shift = mx == 0u ? 0 : min(141 - (int)(mx >> 7), 126);
-                    const float f = exp2i(shift);
-#pragma unroll
-                    for (int x = 0; x < KSTEPS * 2; ++x)
-                        u[x] = Cvt<__half>::pack2(__uint_as_float(u[x] << 16) * f,
-                                                  __uint_as_float(u[x] & 0xffff0000u) * f);
-                }
-                if constexpr (Lay::kQShared) {
 #pragma unroll
                     for (int x = 0; x < KSTEPS / 2; ++x)
                         sts128(sq + (n * (KSTEPS / 2) + x) * 512,
-                               make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]));
-                } else {
-#pragma unroll
-                    for (int kk = 0; kk < KSTEPS; ++kk) {
-                        qf[n][kk][0] = u[2 * kk];
-                        qf[n][kk][1] = u[2 * kk + 1];
-                    }
+                               make_uint4(x4[4 * x], x4[4 * x + 1], x4[4 * x + 2], x4[4 * x + 3]));
                 }
-                // factors and limits of the rows this lane's accumulators hold
+            } else {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int sh = __shfl_sync(kFull, shift, 4 * (2 * t + c));
-                    fs[n][c] = p.scale_log2 * exp2i(-sh);
-                    lim[n][c] = last + p.rows.query(sg, 8 * n + 2 * t + c);
-                    m[n][c] = -INFINITY;
-                    mr[n][c] = 0.f;
-                    l[n][c] = 0.f;
+                for (int kk = 0; kk < KSTEPS; ++kk) {
+                    qf[n][kk][0] = x4[2 * kk];
+                    qf[n][kk][1] = x4[2 * kk + 1];
                 }
-#pragma unroll
-                for (int x = 0; x < MT; ++x) o[n][x][0] = o[n][x][1] = o[n][x][2] = o[n][x][3] = 0.f;
             }
+            // factors of the rows this lane's accumulators hold
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int sh = __shfl_sync(kFull, shift, 4 * (2 * t + c));
+                fs[n][c] = p.scale_log2 * exp2i(-sh);
+                m[n][c] = -INFINITY;
+                mr[n][c] = 0.f;
+                l[n][c] = 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < MT; ++x) o[n][x][0] = o[n][x][1] = o[n][x][2] = o[n][x][3] = 0.f;
         }
-        if (!mbar_wait_bounded(&bar[st], (uint32_t)((i / STAGES) & 1))) {
-            give_up(i + 1);
-            return;
-        }
+        // the buffer is free again (larger units keep their fragments in it)
+        q_coming = !Lay::kQShared && end < ws.n && (end >> 5) <= ws.tile + 1;
+        if (q_coming) fetch_q(end);
 
-        if (d.off >= 0) {
+        for (int pos = i; pos < end; ++pos) {
+            if (ws.advance(p, prefix, pos) && !Lay::kQShared && !q_coming && end < ws.n &&
+                (end >> 5) <= ws.tile + 1) {
+                fetch_q(end);
+                q_coming = true;
+            }
+            if (!mbar_wait_bounded(&bar[st], phase)) {
+                ws.flags |= PKV_DEV_TIMEOUT;
+                // wait (bounded) for the copies still in flight into this warp's buffers
+                for (int s = 1; s < STAGES; ++s) {
+                    const int s2 = (st + s) % STAGES;
+                    if (pos + s < ws.n) mbar_wait_bounded(&bar[s2], s2 > st ? phase : phase ^ 1u);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                ws.n = 0;
+                break;
+            }
+            const int tok0 = (k0 + pos - i) * kChunk;  // the chunk's first token
+            const uint32_t sc = ws.sc(pos);
+            const float fk = __uint_as_float((sc & 0xffu) << 23);  // 2^ek (byte 0: 0)
+            const int evi = kv8_clamp_exp((int)((sc >> 8) & 0xffu) - 127);
+            const float ev = (float)evi, inv_v = exp2i(-evi);
+            const int nv = (sc >> 16) ? 0 : min(kChunk, len - tok0);  // tokens that count
+            // rows see every token of the chunk, or masks apply
+            const bool masked = nv < kChunk || tok0 + kChunk - 1 > lim_min;
             const uint32_t kst = wsm_u32 + st * Lay::kStageBytes;
             const uint32_t vst = kst + Lay::kSide;
-            const int tok0 = d.k * kChunk;
-            const float fk = __uint_as_float((sc & 0xffu) << 23);  // 2^ek (byte 0: 0)
-            const int evi = kv8_clamp_exp((int)(sc >> 8) - 127);
-            const float ev = (float)evi, inv_v = exp2i(-evi);
             // ---- S^T = K Q^T ----
-            uint32_t kw[2][KSTEPS];  // rows j and j + 8: D/4 bytes each
+            float s[NT][4];
+            {
+                uint32_t kw[2][KSTEPS];  // token rows j and j + 8: D/4 bytes each
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int row = j + 8 * hf;
-                if constexpr (D == 128) {
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int row = j + 8 * hf;
+                    if constexpr (D == 128) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint4 v =
+                                lds128(kst + row * 128 + (((2 * t + x) ^ (row & 7)) << 4));
+                            kw[hf][4 * x] = v.x;
+                            kw[hf][4 * x + 1] = v.y;
+                            kw[hf][4 * x + 2] = v.z;
+                            kw[hf][4 * x + 3] = v.w;
+                        }
+                    } else {
+                        const uint4 v = lds128(kst + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
+                        kw[hf][0] = v.x;
+                        kw[hf][1] = v.y;
+                        kw[hf][2] = v.z;
+                        kw[hf][3] = v.w;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KSTEPS; kk += 2) {
+                    uint32_t a[2][4];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint4 v = lds128(kst + row * 128 + (((2 * t + x) ^ (row & 7)) << 4));
-                        kw[hf][4 * x] = v.x;
-                        kw[hf][4 * x + 1] = v.y;
-                        kw[hf][4 * x + 2] = v.z;
-                        kw[hf][4 * x + 3] = v.w;
+                        e4m3x4_to_h2(kw[0][kk + x], a[x][0], a[x][2]);
+                        e4m3x4_to_h2(kw[1][kk + x], a[x][1], a[x][3]);
                     }
-                } else {
-                    const uint4 v = lds128(kst + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
-                    kw[hf][0] = v.x;
-                    kw[hf][1] = v.y;
-                    kw[hf][2] = v.z;
-                    kw[hf][3] = v.w;
-                }
-            }
-            float s[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KSTEPS; kk += 2) {
-                uint32_t a[2][4];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    e4m3x4_to_h2(kw[0][kk + x], a[x][0], a[x][2]);
-                    e4m3x4_to_h2(kw[1][kk + x], a[x][1], a[x][3]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (Lay::kQShared) {
-                        const uint4 q4 = lds128(sq + (n * (KSTEPS / 2) + kk / 2) * 512);
-                        mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                        mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
-                    } else {
-                        mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], qf[n][kk][0],
-                                qf[n][kk][1]);
-                        mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3], qf[n][kk + 1][0],
-                                qf[n][kk + 1][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (Lay::kQShared) {
+                            const uint4 q4 = lds128(sq + (n * (KSTEPS / 2) + kk / 2) * 512);
+                            mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                            mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                        } else {
+                            mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], qf[n][kk][0],
+                                    qf[n][kk][1]);
+                            mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3],
+                                    qf[n][kk + 1][0], qf[n][kk + 1][1]);
+                        }
                     }
                 }
             }
-            // ---- exponents; masks only where the chunk passes a row's last token ----
-            const bool masked = tok0 + kChunk - 1 > min(lim_min, d.len - 1);
+            // ---- exponents ----
             bool above = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float f0 = fs[n][0] * fk, f1 = fs[n][1] * fk;
-                s[n][0] = fmaf(s[n][0], f0, ev);
-                s[n][1] = fmaf(s[n][1], f1, ev);
-                s[n][2] = fmaf(s[n][2], f0, ev);
-                s[n][3] = fmaf(s[n][3], f1, ev);
-                if (masked) {
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int tok = j + 8 * (c >> 1);
-                        if (tok >= d.nvalid || tok0 + tok > lim[n][c & 1]) s[n][c] = -INFINITY;
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] = fmaf(s[n][e], fs[n][e & 1] * fk, ev);
+                    if (masked) {
+                        const int tok = j + 8 * (e >> 1);
+                        const int lim = last + p.rows.query(sg, 8 * n + 2 * t + (e & 1));
+                        if (tok >= nv || tok0 + tok > lim) s[n][e] = -INFINITY;
                     }
+                    top[e & 1] = fmaxf(top[e & 1], s[n][e]);
                 }
-                above |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kSlack ||
-                         fmaxf(s[n][1], s[n][3]) > m[n][1] + kSlack;
+                above |= top[0] > m[n][0] + kSlack || top[1] > m[n][1] + kSlack;
             }
             if (__any_sync(kFull, above)) {
 #pragma unroll
@@ -375,138 +570,146 @@ kv8_decode_kernel(const Kv8DecodeParams kp, const __grid_constant__ CUtensorMap 
                         }
                     }
             }
-            uint32_t pb[NT][2];  // B fragments of P^T: tokens 2t, 2t+1 (+ 8) of row j
+            {
+                uint32_t pb[NT][2];  // B fragments of P^T: tokens 2t, 2t+1 (+ 8) of row j
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float p0 = fast_exp2(s[n][0] - mr[n][0]), p1 = fast_exp2(s[n][1] - mr[n][1]);
-                const float p2 = fast_exp2(s[n][2] - mr[n][0]), p3 = fast_exp2(s[n][3] - mr[n][1]);
-                l[n][0] = fmaf(p0 + p2, inv_v, l[n][0]);
-                l[n][1] = fmaf(p1 + p3, inv_v, l[n][1]);
-                pb[n][0] = transpose8x8(Cvt<__half>::pack2(p0, p1));
-                pb[n][1] = transpose8x8(Cvt<__half>::pack2(p2, p3));
-            }
-            // ---- O^T += V^T P^T ----
-            uint32_t vw[4][DPL / 4];  // tokens 2t, 2t+1, 2t+8, 2t+9: elements DPL j ..
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int row = 2 * t + (x & 1) + 8 * (x >> 1);
-                if constexpr (D == 128) {
-                    const uint4 v = lds128(vst + row * 128 + ((j ^ (row & 7)) << 4));
-                    vw[x][0] = v.x;
-                    vw[x][1] = v.y;
-                    vw[x][2] = v.z;
-                    vw[x][3] = v.w;
-                } else {
-                    const uint32_t addr =
-                        vst + row * 64 + (((j >> 1) ^ ((row >> 1) & 3)) << 4) + (j & 1) * 8;
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(vw[x][0]), "=r"(vw[x][1])
-                                 : "r"(addr));
+                for (int n = 0; n < NT; ++n) {
+                    const float p0 = fast_exp2(s[n][0] - mr[n][0]);
+                    const float p1 = fast_exp2(s[n][1] - mr[n][1]);
+                    const float p2 = fast_exp2(s[n][2] - mr[n][0]);
+                    const float p3 = fast_exp2(s[n][3] - mr[n][1]);
+                    l[n][0] = fmaf(p0 + p2, inv_v, l[n][0]);
+                    l[n][1] = fmaf(p1 + p3, inv_v, l[n][1]);
+                    pb[n][0] = transpose8x8(Cvt<__half>::pack2(p0, p1));
+                    pb[n][1] = transpose8x8(Cvt<__half>::pack2(p2, p3));
                 }
-            }
-            // A NaN in V at a token that some row does not see must not reach
-            // that row through its weight 0: such a chunk (a block behind the
-            // sequence's end may hold anything) multiplies with the NaNs taken
-            // out and adds them back for the rows that see them.
-            bool fix = false;
-            if (masked) {
-                uint32_t any = 0u;
+                // ---- O^T += V^T P^T ----
+                uint32_t vw[4][DPL / 4];  // tokens 2t, 2t+1, 2t+8, 2t+9: elements DPL j ..
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int w = 0; w < DPL / 4; ++w) any |= e4m3_nan_mask(vw[x][w]);
-                fix = __any_sync(kFull, any != 0u);
-            }
-#pragma unroll
-            for (int w = 0; w < DPL / 4; ++w) {
-                uint32_t nan[4] = {0u, 0u, 0u, 0u};
-                if (fix) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        nan[x] = e4m3_nan_mask(vw[x][w]) >> 7;  // 1 in each NaN's byte
-                        vw[x][w] &= ~(nan[x] * 0xffu);
-                        nan[x] *= 0x38u;  // 1.0
-                    }
-                }
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t sel = hf == 0 ? 0x5140u : 0x7362u;
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_h2(__byte_perm(vw[0][w], vw[1][w], sel), a0, a1);
-                    e4m3x4_to_h2(__byte_perm(vw[2][w], vw[3][w], sel), a2, a3);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    if (fix) {
-                        e4m3x4_to_h2(__byte_perm(nan[0], nan[1], sel), a0, a1);
-                        e4m3x4_to_h2(__byte_perm(nan[2], nan[3], sel), a2, a3);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            // which of this lane's four tokens row 8n + j sees
-                            const int lj = __shfl_sync(kFull, lim[n][0], j >> 1);
-                            const int lk = __shfl_sync(kFull, lim[n][1], j >> 1);
-                            const int lr = min((j & 1) ? lk : lj, d.len - 1) - tok0;
-                            const uint32_t v0 = (2 * t <= lr ? 0x3c00u : 0u) |
-                                                (2 * t + 1 <= lr ? 0x3c000000u : 0u);
-                            const uint32_t v1 = (2 * t + 8 <= lr ? 0x3c00u : 0u) |
-                                                (2 * t + 9 <= lr ? 0x3c000000u : 0u);
-                            float c4[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(c4, a0, a1, a2, a3, v0, v1);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (c4[c] > 0.f) o[n][2 * w + hf][c] = __uint_as_float(0x7fc00000u);
-                        }
-                    }
-                }
-            }
-        }
-
-        if (ws.seg_end(i, d)) {
-            const bool whole = seg_whole_start && (d.k == d.nch - 1);
-            const int b = d.u / units_per_b;
-            const int uidx = d.u - b * units_per_b;
-            const int h = uidx / p.sub_groups;
-            const int sg = uidx - h * p.sub_groups;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float lr = l[n][c];
-                    lr += __shfl_xor_sync(kFull, lr, 4);
-                    lr += __shfl_xor_sync(kFull, lr, 8);
-                    lr += __shfl_xor_sync(kFull, lr, 16);
-                    const int r = 8 * n + 2 * t + c;
-                    if (r >= seg_rows) continue;
-                    if (whole) {
-                        const float inv = lr == 0.f ? 0.f : 1.0f / lr;  // no token seen: zeros
-                        uint4* dst = reinterpret_cast<uint4*>(
-                            static_cast<T*>(p.out) + p.rows.row(b, h, sg, r) * D + DPL * j);
-#pragma unroll
-                        for (int x = 0; x < MT / 4; ++x)
-                            dst[x] = make_uint4(
-                                Cvt<T>::pack2(o[n][4 * x][c] * inv, o[n][4 * x][c + 2] * inv),
-                                Cvt<T>::pack2(o[n][4 * x + 1][c] * inv, o[n][4 * x + 1][c + 2] * inv),
-                                Cvt<T>::pack2(o[n][4 * x + 2][c] * inv, o[n][4 * x + 2][c + 2] * inv),
-                                Cvt<T>::pack2(o[n][4 * x + 3][c] * inv, o[n][4 * x + 3][c + 2] * inv));
+                for (int x = 0; x < 4; ++x) {
+                    const int row = 2 * t + (x & 1) + 8 * (x >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 v = lds128(vst + row * 128 + ((j ^ (row & 7)) << 4));
+                        vw[x][0] = v.x;
+                        vw[x][1] = v.y;
+                        vw[x][2] = v.z;
+                        vw[x][3] = v.w;
                     } else {
-                        float* slot = p.partials +
-                                      (long long)seg_slot * partial_slot_floats(kp.gs, D);
-                        float4* dst = reinterpret_cast<float4*>(slot + r * D + DPL * j);
+                        const uint32_t addr =
+                            vst + row * 64 + (((j >> 1) ^ ((row >> 1) & 3)) << 4) + (j & 1) * 8;
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(vw[x][0]), "=r"(vw[x][1])
+                                     : "r"(addr));
+                    }
+                }
+                // A NaN in V at a token that some row does not see must not
+                // reach that row through its weight 0: such a chunk (a block
+                // behind the sequence's end may hold anything) multiplies with
+                // the NaNs taken out and adds them back for the rows that see
+                // them.
+                if (masked) {
+                    uint32_t any = 0u;
 #pragma unroll
-                        for (int x = 0; x < MT / 2; ++x)
-                            dst[x] = make_float4(o[n][2 * x][c], o[n][2 * x][c + 2],
-                                                 o[n][2 * x + 1][c], o[n][2 * x + 1][c + 2]);
-                        if (j == 0) {
-                            slot[kp.gs * D + r] = m[n][c];
-                            slot[kp.gs * D + kp.gs + r] = lr;
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int w = 0; w < DPL / 4; ++w) any |= e4m3_nan_mask(vw[x][w]);
+                    if (__any_sync(kFull, any != 0u)) {
+#pragma unroll
+                        for (int w = 0; w < DPL / 4; ++w) {
+                            uint32_t nan[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                nan[x] = e4m3_nan_mask(vw[x][w]) >> 7;  // 1 in each NaN's byte
+                                vw[x][w] &= ~(nan[x] * 0xffu);
+                                nan[x] *= 0x38u;  // 1.0
+                            }
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t sel = hf == 0 ? 0x5140u : 0x7362u;
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_h2(__byte_perm(nan[0], nan[1], sel), a0, a1);
+                                e4m3x4_to_h2(__byte_perm(nan[2], nan[3], sel), a2, a3);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    // the last token of the chunk that row 8n + j sees
+                                    const int lr =
+                                        min(last + p.rows.query(sg, 8 * n + j) - tok0,
+                                            nv - 1);
+                                    const uint32_t v0 = (2 * t <= lr ? 0x3c00u : 0u) |
+                                                        (2 * t + 1 <= lr ? 0x3c000000u : 0u);
+                                    const uint32_t v1 = (2 * t + 8 <= lr ? 0x3c00u : 0u) |
+                                                        (2 * t + 9 <= lr ? 0x3c000000u : 0u);
+                                    float c4[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16(c4, a0, a1, a2, a3, v0, v1);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (c4[e] > 0.f)
+                                            o[n][2 * w + hf][e] = __uint_as_float(0x7fc00000u);
+                                }
+                            }
                         }
                     }
                 }
+#pragma unroll
+                for (int w = 0; w < DPL / 4; ++w) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t sel = hf == 0 ? 0x5140u : 0x7362u;
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_h2(__byte_perm(vw[0][w], vw[1][w], sel), a0, a1);
+                        e4m3x4_to_h2(__byte_perm(vw[2][w], vw[3][w], sel), a2, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    }
+                }
+            }
+            release(pos);
         }
-        __syncwarp();
-        // refill: positions up to i + STAGES (stage i % STAGES is free again)
-        while (issued <= i + STAGES && issue(issued)) ++issued;
+        if (ws.n == 0) break;  // gave up
+
+        // ---- the segment's result ----
+        const bool whole = k0 == 0 && end - i == nch;
+        float* slot =
+            p.partials + (long long)(gw + u) * partial_slot_floats(p.gs, D);  // slot u + w
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (i == end) continue;  // cost positions only
+                float lr = l[n][c];
+                lr += __shfl_xor_sync(kFull, lr, 4);
+                lr += __shfl_xor_sync(kFull, lr, 8);
+                lr += __shfl_xor_sync(kFull, lr, 16);
+                const int r = 8 * n + 2 * t + c;
+                if (r >= rows) continue;
+                if (whole) {
+                    const float inv = lr == 0.f ? 0.f : 1.0f / lr;  // no token seen: zeros
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        static_cast<T*>(p.out) + p.rows.row(b, h, sg, r) * D + DPL * j);
+#pragma unroll
+                    for (int x = 0; x < MT / 4; ++x)
+                        dst[x] = make_uint4(
+                            Cvt<T>::pack2(o[n][4 * x][c] * inv, o[n][4 * x][c + 2] * inv),
+                            Cvt<T>::pack2(o[n][4 * x + 1][c] * inv, o[n][4 * x + 1][c + 2] * inv),
+                            Cvt<T>::pack2(o[n][4 * x + 2][c] * inv, o[n][4 * x + 2][c + 2] * inv),
+                            Cvt<T>::pack2(o[n][4 * x + 3][c] * inv, o[n][4 * x + 3][c + 2] * inv));
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(slot + r * D + DPL * j);
+#pragma unroll
+                    for (int x = 0; x < MT / 2; ++x)
+                        dst[x] = make_float4(o[n][2 * x][c], o[n][2 * x][c + 2],
+                                             o[n][2 * x + 1][c], o[n][2 * x + 1][c + 2]);
+                    if (j == 0) {
+                        slot[p.gs * D + r] = m[n][c];
+                        slot[p.gs * D + p.gs + r] = lr;
+                    }
+                }
+            }
+        i = end;
     }
+    const uint32_t flags = __reduce_or_sync(kFull, ws.flags);
+    if (lane == 0) p.flags[gw] = flags;
     pdl_trigger();
 }
 
@@ -526,9 +729,11 @@ Kv8DecodeInfo pick_kv8_decode_info(int head_dim, int rows) {
     if (head_dim == 128)
         return rows <= 8    ? make_kv8_decode_info<T, 128, 1>()
                : rows <= 16 ? make_kv8_decode_info<T, 128, 2>()
+               : rows <= 24 ? make_kv8_decode_info<T, 128, 3>()
                             : make_kv8_decode_info<T, 128, 4>();
     return rows <= 8    ? make_kv8_decode_info<T, 64, 1>()
            : rows <= 16 ? make_kv8_decode_info<T, 64, 2>()
+           : rows <= 24 ? make_kv8_decode_info<T, 64, 3>()
                         : make_kv8_decode_info<T, 64, 4>();
 }
 

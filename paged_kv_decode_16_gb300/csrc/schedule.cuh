@@ -88,22 +88,14 @@ __device__ __forceinline__ ChunkDesc sel_desc(bool second, const ChunkDesc& a,
     return d;
 }
 
-// What a lane keeps of its chunk of a tile beside the description: nothing.
-struct NoExtra {
-    __device__ __forceinline__ void load(const ChunkDesc&) {}
-};
-
 // The chunk stream of one worker.  All members are warp-uniform except the
-// lane-held descriptors wa / wb and extras xa / xb (Extra::load, called by the
-// lane that owns the chunk, sets one up).  Every method must be called by all
-// 32 lanes (they shuffle).
-template <class Extra = NoExtra>
-struct WorkStreamT {
+// lane-held descriptors wa / wb.  Every method must be called by all 32
+// lanes (they shuffle).
+struct WorkStream {
     // the live tiles: a = the consumer's, b = the next one (len 0: none yet)
     int a_start, a_len;
     int b_start, b_len;
     ChunkDesc wa, wb;
-    Extra xa, xb;
     int stream_end;   // chunks in this worker's range
     // the rest of the range: next chunk, tiles left, base tile length, longer tiles
     int next_f, tiles_left, piece, extra;
@@ -127,10 +119,7 @@ struct WorkStreamT {
         wb.off = -1;
         wb.u = wb.k = wb.nvalid = wb.len = 0;
         wb.nch = 1;
-        if (lane < len) {
-            wb = describe_chunk(p, f + lane, units_per_b, b_lo, b_hi);
-            xb.load(wb);
-        }
+        if (lane < len) wb = describe_chunk(p, f + lane, units_per_b, b_lo, b_hi);
     }
 
     // Set up the worker's stream; afterwards tile a is its first tile (if any).
@@ -160,7 +149,6 @@ struct WorkStreamT {
         a_start = b_start;
         a_len = b_len;
         wa = wb;
-        xa = xb;
         b_len = 0;
         b_start = a_start + a_len;
     }
@@ -199,7 +187,5 @@ struct WorkStreamT {
         return d.k == d.nch - 1 || i + 1 >= stream_end;
     }
 };
-
-using WorkStream = WorkStreamT<>;
 
 }  // namespace pkv
