@@ -68,7 +68,10 @@ __device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
 constexpr int kKv8SelfPlan = 256;
 // A unit's start (its queries, its result) counts as this many chunks when the
 // ranges are cut.
-constexpr int kKv8UnitCost = 4;
+#ifndef KV8_COST
+#define KV8_COST 4
+#endif
+constexpr int kKv8UnitCost = KV8_COST;
 // Automatic worker count: at least this many positions each.
 constexpr int kKv8MinPositions = 4;
 

@@ -235,8 +235,14 @@ __device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* 
 }
 
 // NT tiles of 8 query rows; a unit has at most 8 NT rows.
+#ifndef KV8_MB
+#define KV8_MB 1
+#endif
+#ifndef KV8_KC
+#define KV8_KC 2
+#endif
 template <typename T, int D, int NT, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32)
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? KV8_MB : 1)
 kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                   const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -360,6 +366,9 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         for (long long x = lane; x < vecs; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
     }
 
+#ifdef KV8_TRIG
+    pdl_trigger();
+#endif
     int st = 0;          // stage of the position at hand
     uint32_t phase = 0;  // its barrier's phase
     int i = 0;           // position
@@ -505,9 +514,14 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                         kw[hf][3] = v.w;
                     }
                 }
+                // one unit tile: two chains of products, added at the end
+                constexpr int KC = NT == 1 ? KV8_KC : 1;
+                float sk[NT][KC][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < KC; ++c)
+                        sk[n][c][0] = sk[n][c][1] = sk[n][c][2] = sk[n][c][3] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KSTEPS; kk += 2) {
                     uint32_t a[2][4];
@@ -520,16 +534,21 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                     for (int n = 0; n < NT; ++n) {
                         if constexpr (Lay::kQShared) {
                             const uint4 q4 = lds128(sq + (n * (KSTEPS / 2) + kk / 2) * 512);
-                            mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                            mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                            mma_f16(sk[n][0], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                            mma_f16(sk[n][KC - 1], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
                         } else {
-                            mma_f16(s[n], a[0][0], a[0][1], a[0][2], a[0][3], qf[n][kk][0],
+                            mma_f16(sk[n][0], a[0][0], a[0][1], a[0][2], a[0][3], qf[n][kk][0],
                                     qf[n][kk][1]);
-                            mma_f16(s[n], a[1][0], a[1][1], a[1][2], a[1][3],
+                            mma_f16(sk[n][KC - 1], a[1][0], a[1][1], a[1][2], a[1][3],
                                     qf[n][kk + 1][0], qf[n][kk + 1][1]);
                         }
                     }
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[n][e] = KC == 1 ? sk[n][0][e] : sk[n][0][e] + sk[n][KC - 1][e];
             }
             // ---- exponents ----
             bool above = false;
@@ -715,7 +734,12 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
 
 template <typename T, int D, int NT>
 Kv8DecodeInfo make_kv8_decode_info() {
-    constexpr int W = 4, S = 4;
+#ifndef KV8_W
+#define KV8_W 4
+#define KV8_S 4
+#define KV8_MB 1
+#endif
+    constexpr int W = NT == 1 ? KV8_W : 4, S = NT == 1 ? KV8_S : 4;
     Kv8DecodeInfo info;
     info.fn = kv8_decode_kernel<T, D, NT, W, S>;
     info.warps = W;
