@@ -1576,6 +1576,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.n_kv_heads = c.n_kv_heads;
     p.sub_groups = s.sub_groups;
     p.units_per_b = s.units_per_b;
+    p.units = (int)s.units;
     p.num_pages = c.num_pages;
     p.table_stride = c.table_stride;
     p.chunks_per_page = c.page_size / pkv::kChunk;

@@ -68,12 +68,11 @@ __device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
 constexpr int kKv8SelfPlan = 256;
 // A unit's start (its queries, its result) counts as this many chunks when the
 // ranges are cut.
-#ifndef KV8_COST
-#define KV8_COST 4
-#endif
-constexpr int kKv8UnitCost = KV8_COST;
+constexpr int kKv8UnitCost = 4;
 // Automatic worker count: at least this many positions each.
 constexpr int kKv8MinPositions = 4;
+
+constexpr int kKv8Warps = 4;  // workers (warps) of a CTA of the decode kernel
 
 // Workers and the split of `total` positions over them: sw each, one more for
 // the first r.
@@ -91,6 +90,16 @@ __host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, 
     *r = n > 0 ? total - *sw * n : 0;
 }
 
+// Workers whose parts of one unit are merged by their CTA before they leave it: a
+// CTA's, when units are few beside the workers (nw); else 1: none are.  Merging
+// costs the decode kernel 1.5 us at its end (32 sequences of 512 to 4096 tokens, 7
+// workers a unit: 23.6 against 22.1 us); one sequence of 32768 tokens (228 a unit)
+// gains more in the combine (23.4 us both together against 24.4, and 15.2 against
+// 18.7 with one KV head).
+__host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw) {
+    return nw / 32 > units ? kKv8Warps : 1;
+}
+
 struct Kv8DecodeParams {
     const void* q;        // [B][n_queries][Hq][D]
     void* out;
@@ -106,7 +115,7 @@ struct Kv8DecodeParams {
     int self_plan;
     int unit_cost;          // positions a unit has beside its chunks
     int workers_req, workers_auto;
-    int batch, n_kv_heads, sub_groups, units_per_b, num_pages, table_stride;
+    int batch, n_kv_heads, sub_groups, units_per_b, units, num_pages, table_stride;
     int chunks_per_page;
     long long cap;          // tokens of a table row
     float scale_log2;       // scale * log2(e)

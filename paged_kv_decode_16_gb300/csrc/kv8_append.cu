@@ -46,20 +46,23 @@ __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t turns, float* c, 
     sincospif(x, s, c);
 }
 
-// Norm (w non-null: weights of the 8 low and 8 high elements) and rotation of
-// a lane's elements lo[e] and their partners hi[e]; hv lanes hold a row.
+// 1 / rms of the row whose elements HV neighbouring lanes hold.
 template <int D>
+__device__ __forceinline__ float inv_rms(const float (&lo)[8], const float (&hi)[8], float eps) {
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], sum));
+#pragma unroll
+    for (int o = D / 32; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    return 1.0f / sqrtf(sum / (float)D + eps);
+}
+
+// Norm (wlo non-null: weights of the 8 low and 8 high elements; inv: 1 / rms)
+// and rotation (c non-null) of a lane's elements lo[e] and their partners hi[e].
 __device__ __forceinline__ void norm_rotate(float (&lo)[8], float (&hi)[8], const float* wlo,
-                                            const float* whi, float eps, const float* c,
+                                            const float* whi, float inv, const float* c,
                                             const float* s) {
-    constexpr int HV = D / 16;
     if (wlo) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], sum));
-#pragma unroll
-        for (int o = HV / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        const float inv = 1.0f / sqrtf(sum / (float)D + eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             lo[e] = lo[e] * inv * wlo[e];
@@ -96,7 +99,10 @@ struct Run {
     long long blk;  // block of the pool at head 0: page * Hkv * (P / 16) + block of the page
 };
 
-// One (run, head, side) by a warp.
+// One (run, head, side) by a warp.  The rows stay packed in registers; what is
+// computed from them (the norm, the rotation) is computed twice, for the largest
+// element and for the bytes, which costs less than the registers for it would in
+// warps at work (64 more a thread).
 template <typename T, int D, bool kK>
 __device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& r, int h,
                                              int tok0, const float* ctab, const float* stab,
@@ -106,58 +112,47 @@ __device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& 
     constexpr int PASSES = kChunk / RPP;
     const int jl = lane % HV, rl = lane / HV;
     const uint4* src = static_cast<const uint4*>(kK ? a.k_new : a.v_new);
-    float lo[PASSES][8], hi[PASSES][8];
-    uint32_t mx = 0u;
+    uint4 vl[PASSES], vh[PASSES];
+    float inv[PASSES];
 #pragma unroll
     for (int ps = 0; ps < PASSES; ++ps) {
         const int x = ps * RPP + rl;  // token of the run
-        const bool ok = x < r.n;
-        uint4 vl = make_uint4(0u, 0u, 0u, 0u), vh = vl;
-        if (ok) {
+        vl[ps] = vh[ps] = make_uint4(0u, 0u, 0u, 0u);
+        if (x < r.n) {
             const uint4* row = src + ((long long)(r.tok + x) * a.n_kv_heads + h) * (D / 8);
-            vl = row[jl];
-            vh = row[HV + jl];
-        }
-        unpack<T>(vl, lo[ps]);
-        unpack<T>(vh, hi[ps]);
-    }
-    if constexpr (kK) {
-#pragma unroll
-        for (int ps = 0; ps < PASSES; ++ps) {
-            if (ps * RPP >= r.n) break;  // warp-uniform
-            const int x = min(ps * RPP + rl, r.n - 1);
-            const int at = (r.tok - tok0 + x) * (D / 2) + 8 * jl;
-            norm_rotate<D>(lo[ps], hi[ps], a.k_norm_w ? wk + 8 * jl : nullptr,
-                           wk + D / 2 + 8 * jl, a.norm_eps, a.rope ? ctab + at : nullptr,
-                           stab + at);
+            vl[ps] = row[jl];
+            vh[ps] = row[HV + jl];
         }
     }
+    auto values = [&](int ps, float (&lo)[8], float (&hi)[8], bool first) {
+        unpack<T>(vl[ps], lo);
+        unpack<T>(vh[ps], hi);
+        if constexpr (kK) {
+            if (first) inv[ps] = a.k_norm_w ? inv_rms<D>(lo, hi, a.norm_eps) : 1.f;
+            const int at = (r.tok - tok0 + min(ps * RPP + rl, r.n - 1)) * (D / 2) + 8 * jl;
+            norm_rotate(lo, hi, a.k_norm_w ? wk + 8 * jl : nullptr, wk + D / 2 + 8 * jl, inv[ps],
+                        a.rope ? ctab + at : nullptr, stab + at);
+        }
+    };
+    uint32_t mx = 0u, fin = 0u;  // largest |element|, and the largest finite one, as bits
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps)
+    for (int ps = 0; ps < PASSES; ++ps) {
+        if (ps * RPP >= r.n) break;  // warp-uniform
+        float lo[8], hi[8];
+        values(ps, lo, hi, true);
         if (ps * RPP + rl < r.n) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                mx = max(mx, __float_as_uint(lo[ps][e]) & 0x7fffffffu);
-                mx = max(mx, __float_as_uint(hi[ps][e]) & 0x7fffffffu);
+                const uint32_t x = __float_as_uint(lo[e]) & 0x7fffffffu;
+                const uint32_t y = __float_as_uint(hi[e]) & 0x7fffffffu;
+                mx = max(mx, max(x, y));
+                if (x < 0x7f800000u) fin = max(fin, x);
+                if (y < 0x7f800000u) fin = max(fin, y);
             }
         }
-    mx = __reduce_max_sync(kFull, mx);
-    const bool bad = mx >= 0x7f800000u;  // an infinity or NaN: it does not set the scale
-    if (bad) {
-        mx = 0u;
-#pragma unroll
-        for (int ps = 0; ps < PASSES; ++ps)
-            if (ps * RPP + rl < r.n) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = __float_as_uint(lo[ps][e]) & 0x7fffffffu;
-                    const uint32_t v = __float_as_uint(hi[ps][e]) & 0x7fffffffu;
-                    if (u < 0x7f800000u) mx = max(mx, u);
-                    if (v < 0x7f800000u) mx = max(mx, v);
-                }
-            }
-        mx = __reduce_max_sync(kFull, mx);
     }
+    const bool bad = __any_sync(kFull, mx >= 0x7f800000u);  // it does not set the scale
+    mx = __reduce_max_sync(kFull, fin);
     const int bpp = a.page_size / kChunk;
     const long long blk = r.blk + (long long)h * bpp;  // [page][head][block]
     uint8_t* pool = (kK ? a.k_pool : a.v_pool) + blk * (kChunk * D);
@@ -183,20 +178,22 @@ __device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& 
     }
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = (uint8_t)(e + 127);
-    const float inv = exp2i(-e);
+    const float up = exp2i(-e);
 #pragma unroll
     for (int ps = 0; ps < PASSES; ++ps) {
         const int x = ps * RPP + rl;
         if (x < r.n) {
+            float lo[8], hi[8];
+            values(ps, lo, hi, false);
             uint2* row = reinterpret_cast<uint2*>(pool + (r.lo + x) * D);
-            row[jl] = quantise8(lo[ps], inv, bad);
-            row[HV + jl] = quantise8(hi[ps], inv, bad);
+            row[jl] = quantise8(lo, up, bad);
+            row[HV + jl] = quantise8(hi, up, bad);
         }
     }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status,
                   uint32_t* flags) {
     constexpr int HALF = D / 2, HV = D / 16;
@@ -303,24 +300,35 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         uint4* qo = static_cast<uint4*>(a.q_out);
         const long long row0 = (long long)tok0 * a.n_q_heads;
         const int rows = ntok * a.n_q_heads;
-        const int jl = tid % HV;
-        // every lane of a warp takes part in the norm's exchange
-        for (int r0 = warp * (32 / HV); r0 < rows; r0 += kThreads / HV) {
-            const int r = r0 + lane / HV;
-            const bool ok = r < rows;
-            const int rc = ok ? r : rows - 1;
-            const int tk = rc / a.n_q_heads;
-            const long long at = (row0 + rc) * (D / 8);
-            const uint4 vl = q[at + jl], vh = q[at + HV + jl];
-            float lo[8], hi[8];
-            unpack<T>(vl, lo);
-            unpack<T>(vh, hi);
-            const int c = tk * HALF + 8 * jl;
-            norm_rotate<D>(lo, hi, a.q_norm_w ? wq + 8 * jl : nullptr, wq + HALF + 8 * jl,
-                           a.norm_eps, a.rope ? ctab + c : nullptr, stab + c);
-            if (ok) {
-                qo[at + jl] = pack<T>(lo);
-                qo[at + HV + jl] = pack<T>(hi);
+        const int jl = lane % HV;
+        constexpr int STEP = kThreads / HV, U = 4;  // rows a pass of the CTA; passes in flight
+        for (int r0 = warp * (32 / HV) + lane / HV; r0 - lane / HV < rows; r0 += U * STEP) {
+            uint4 vl[U], vh[U];
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                vl[x] = vh[x] = make_uint4(0u, 0u, 0u, 0u);
+                const int r = r0 + x * STEP;
+                if (r < rows) {
+                    const uint4* row = q + (row0 + r) * (D / 8);
+                    vl[x] = row[jl];
+                    vh[x] = row[HV + jl];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int r = r0 + x * STEP;
+                if (r - lane / HV >= rows) break;  // warp-uniform
+                float lo[8], hi[8];
+                unpack<T>(vl[x], lo);
+                unpack<T>(vh[x], hi);
+                const float inv = a.q_norm_w ? inv_rms<D>(lo, hi, a.norm_eps) : 1.f;
+                if (r >= rows) continue;
+                const int c = r / a.n_q_heads * HALF + 8 * jl;
+                norm_rotate(lo, hi, a.q_norm_w ? wq + 8 * jl : nullptr, wq + HALF + 8 * jl, inv,
+                            a.rope ? ctab + c : nullptr, stab + c);
+                uint4* row = qo + (row0 + r) * (D / 8);
+                row[jl] = pack<T>(lo);
+                row[HV + jl] = pack<T>(hi);
             }
         }
     }

@@ -1,14 +1,16 @@
 // kv8_combine.cu -- merging the partial states of the 8-bit cache's decode.
 //
-// A warp per row of a unit; when units are few beside the workers (their rows
-// have many segments then), a CTA per row, whose warps share the segments
-// (merge.cuh).  Rows that one worker finished end at once.  A warp's loads --
-// every segment's maximum and sum, and the weighted sums of the first eight
-// segments -- go out together, before the first of them is used: one round of
-// loads behind the one for the ranges is what the kernel takes.  CTA 0 collects
-// the workers' status bits.  (A CTA of 8 warps per unit took 5.3 us of a
-// decode over 32 sequences of 512 to 4096 tokens and 13 us of one over 256
-// uneven ones, whose 1024 CTAs came in three waves.)
+// A warp per row of a unit; when units are few beside the decode's CTAs (their
+// rows have many segments then), a CTA per row, whose warps take every eighth
+// segment each and meet in shared memory.  Rows that the decode kernel finished
+// end at once.  A warp's loads -- its segments' maxima and sums, and the weighted
+// sums of its first eight segments -- go out together, before the first of them
+// is used: one round of loads behind the one for the ranges is what the kernel
+// takes.  CTA 0 collects the workers' status bits.
+//
+// Segments of a unit (kv8_decode.cuh): one for each of its workers, in slot
+// u + w; with merge_warps, the workers of one CTA whose ranges end within the
+// unit, or with it, have merged theirs into one, in the slot of the first.
 #include "kv8.cuh"
 #include "merge.cuh"
 
@@ -16,67 +18,99 @@ namespace pkv {
 
 namespace {
 
+struct Segs {
+    int u, w0;    // unit, its first worker
+    int chains;   // merged segments
+    int count;    // segments: the chains, and the last worker's own if it has one
+    int w_last;
+    int per;      // workers merged into one (those of a CTA), 1: none are
+    __device__ __forceinline__ long long slot(int s) const {
+        return (long long)u + (s == 0         ? w0
+                               : s < chains   ? (w0 / per + s) * per
+                                              : w_last);
+    }
+};
+
+// The segments of unit u, whose chunks are positions a .. e.
+__device__ __forceinline__ Segs kv8_segments(int sw, int r, int u, int a, int e, int per) {
+    Segs s;
+    s.u = u;
+    s.w0 = worker_of(a, sw, r);
+    s.w_last = worker_of(e, sw, r);
+    const bool own = s.w_last > s.w0 && e + 1 < range_begin(s.w_last + 1, sw, r);
+    const int wt = own ? s.w_last - 1 : s.w_last;
+    s.per = per;
+    s.chains = wt / per - s.w0 / per + 1;
+    s.count = s.chains + (own ? 1 : 0);
+    return s;
+}
+
+constexpr int kWarps = 8;
 constexpr int kBlock = 8;  // segments whose sums are in flight together
 
-// The row's segments by one warp: lane x takes elements 4x .. 4x + 3.
-template <typename T, int D>
-__device__ __forceinline__ void merge_row_warp(const SlotSegs& sg, int ns, int g, int lane,
-                                               T* out) {
+// Segments 0 .. n - 1 of a row by one warp, relative to their own largest
+// maximum M: lane x has elements 4x .. 4x + 3 of the weighted sum.  at(s): the
+// segment's slot; o, m, l: the row's places in a slot.
+template <int D, class At>
+__device__ __forceinline__ float4 merge_some(const At& at, int n, int o, int m, int l, int lane,
+                                             float& M, float& den) {
     const bool act = lane < D / 4;
     float4 v[kBlock];
 #pragma unroll
     for (int x = 0; x < kBlock; ++x)
-        if (act && x < ns) v[x] = __ldcg(sg.o4(x, g, lane));
-    float M = -INFINITY;
+        if (act && x < n) v[x] = __ldcg(reinterpret_cast<const float4*>(at(x) + o) + lane);
     float m0 = -INFINITY, l0 = 0.f;  // segment `lane`
-    if (lane < ns) {
-        m0 = __ldcg(sg.m(lane, g));
-        l0 = __ldcg(sg.l(lane, g));
+    if (lane < n) {
+        m0 = __ldcg(at(lane) + m);
+        l0 = __ldcg(at(lane) + l);
     }
     M = m0;
-    for (int s = 32 + lane; s < ns; s += 32) M = fmaxf(M, __ldcg(sg.m(s, g)));
+    for (int x = 32 + lane; x < n; x += 32) M = fmaxf(M, __ldcg(at(x) + m));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
     float w = merge_weight(m0, M);
-    float den = w * l0;
-    for (int s = 32 + lane; s < ns; s += 32)
-        den = fmaf(merge_weight(__ldcg(sg.m(s, g)), M), __ldcg(sg.l(s, g)), den);
+    den = w * l0;
+    for (int x = 32 + lane; x < n; x += 32)
+        den = fmaf(merge_weight(__ldcg(at(x) + m), M), __ldcg(at(x) + l), den);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+    for (int k = 16; k > 0; k >>= 1) den += __shfl_xor_sync(kFull, den, k);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < ns; s0 += kBlock) {
-        if (s0 > 0) {
+    for (int x0 = 0; x0 < n; x0 += kBlock) {
+        if (x0 > 0) {
 #pragma unroll
             for (int x = 0; x < kBlock; ++x)
-                if (act && s0 + x < ns) v[x] = __ldcg(sg.o4(s0 + x, g, lane));
-            // weights of the next 32 segments
-            if ((s0 & 31) == 0)
-                w = s0 + lane < ns ? merge_weight(__ldcg(sg.m(s0 + lane, g)), M) : 0.f;
+                if (act && x0 + x < n)
+                    v[x] = __ldcg(reinterpret_cast<const float4*>(at(x0 + x) + o) + lane);
+            if ((x0 & 31) == 0)  // weights of the next 32
+                w = x0 + lane < n ? merge_weight(__ldcg(at(x0 + lane) + m), M) : 0.f;
         }
 #pragma unroll
         for (int x = 0; x < kBlock; ++x) {
-            const float ws = __shfl_sync(kFull, w, (s0 + x) & 31);
-            if (act && s0 + x < ns) {
-                acc.x = fmaf(ws, v[x].x, acc.x);
-                acc.y = fmaf(ws, v[x].y, acc.y);
-                acc.z = fmaf(ws, v[x].z, acc.z);
-                acc.w = fmaf(ws, v[x].w, acc.w);
+            const float wt = __shfl_sync(kFull, w, (x0 + x) & 31);
+            if (act && x0 + x < n) {
+                acc.x = fmaf(wt, v[x].x, acc.x);
+                acc.y = fmaf(wt, v[x].y, acc.y);
+                acc.z = fmaf(wt, v[x].z, acc.z);
+                acc.w = fmaf(wt, v[x].w, acc.w);
             }
         }
     }
-    if (act) {
-        // a sum of 0: no token seen.  (Sums may be as small as 2^-40 and NaN
-        // stays NaN, so it is compared with 0.)
-        const float inv = den == 0.f ? 0.f : 1.0f / den;
-        *reinterpret_cast<uint2*>(out + lane * 4) =
-            make_uint2(Cvt<T>::pack2(acc.x * inv, acc.y * inv),
-                       Cvt<T>::pack2(acc.z * inv, acc.w * inv));
-    }
+    return acc;
+}
+
+// A sum of 0: no token seen, zeros.  (Sums may be as small as 2^-40, and NaN
+// stays NaN.)
+template <typename T>
+__device__ __forceinline__ void store_row(const float4& acc, float den, int lane, T* out) {
+    const float inv = den == 0.f ? 0.f : 1.0f / den;
+    *reinterpret_cast<uint2*>(out + lane * 4) =
+        make_uint2(Cvt<T>::pack2(acc.x * inv, acc.y * inv),
+                   Cvt<T>::pack2(acc.z * inv, acc.w * inv));
 }
 
 // kRowCta: a CTA per row, else a warp.
 template <typename T, int D, bool kRowCta>
-__global__ void __launch_bounds__(kMergeSlots * 32)
+__global__ void __launch_bounds__(kWarps * 32, kRowCta ? 1 : 3)
 kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();  // everything read below, the ranges too, is the decode kernel's
@@ -97,7 +131,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
         return;
     }
     const long long item = kRowCta ? (long long)blockIdx.x - 1
-                                   : ((long long)blockIdx.x - 1) * kMergeSlots + warp;
+                                   : ((long long)blockIdx.x - 1) * kWarps + warp;
     const int u = (int)(item / a.gs), g = (int)(item - (long long)u * a.gs);
     if (u >= a.units) return;
     const int b = u / a.units_per_b;
@@ -105,21 +139,55 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     const int h = uidx / a.sub_groups;
     const int sg = uidx - h * a.sub_groups;
     const int first = a.prefix[b], next = a.prefix[b + 1];
-    const int sw = a.hdr->chunks_per_worker, r = a.hdr->extra_chunks;
+    const int nw = a.hdr->num_workers, sw = a.hdr->chunks_per_worker, r = a.hdr->extra_chunks;
     if (g >= a.rows.rows(sg)) return;
     const int per_unit = (next - first) / a.units_per_b;
     if (per_unit == 0) return;  // no tokens: the decode kernel wrote zeros
-    const UnitSegments segs = unit_segments(sw, r, u, first + uidx * per_unit + a.unit_cost,
-                                            per_unit - a.unit_cost);
-    const int ns = segs.count();
-    if (ns <= 1) return;  // finished in place by its worker
-    const SlotSegs slots{a.partials, segs.base, partial_slot_floats(a.gs, D), a.gs, D};
+    const int at = first + uidx * per_unit;
+    const Segs segs = kv8_segments(sw, r, u, at + a.unit_cost, at + per_unit - 1,
+                                   kv8_merge_warps(a.units, nw));
+    if (segs.count <= 1) return;  // finished in the decode kernel
+    const int stride = partial_slot_floats(a.gs, D);
     T* out = static_cast<T*>(a.out) + a.rows.row(b, h, sg, g) * D;
     if constexpr (kRowCta) {
-        const RowShift<SlotSegs> one{slots, g};
-        merge_rows_cta<T, D>(one, ns, 1, warp, lane, [&](int) { return out; });
+        __shared__ float4 s_acc[kWarps][D / 4];
+        __shared__ float s_m[kWarps], s_den[kWarps];
+        float M, den;
+        const int n = segs.count > warp ? (segs.count - warp + kWarps - 1) / kWarps : 0;
+        const float4 acc = merge_some<D>(
+            [&](int s) { return a.partials + segs.slot(warp + s * kWarps) * stride; }, n, g * D,
+            a.gs * D + g, a.gs * D + a.gs + g, lane, M, den);
+        if (lane < D / 4) s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_den[warp] = den;
+        }
+        __syncthreads();
+        if (warp > 0 || lane >= D / 4) return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float wt = merge_weight(s_m[w], top);
+            const float4 y = s_acc[w][lane];
+            total = fmaf(wt, s_den[w], total);
+            sum.x = fmaf(wt, y.x, sum.x);
+            sum.y = fmaf(wt, y.y, sum.y);
+            sum.z = fmaf(wt, y.z, sum.z);
+            sum.w = fmaf(wt, y.w, sum.w);
+        }
+        store_row<T>(sum, total, lane, out);
     } else {
-        merge_row_warp<T, D>(slots, ns, g, lane, out);
+        float M, den;
+        // (merged warps come with few units, so with kRowCta: here the slots are
+        // next to each other)
+        const float* slots = a.partials + (segs.u + segs.w0) * (long long)stride;
+        const float4 acc = merge_some<D>([&](int s) { return slots + s * stride; }, segs.count,
+                                         g * D, a.gs * D + g, a.gs * D + a.gs + g, lane, M, den);
+        if (lane < D / 4) store_row<T>(acc, den, lane, out);
     }
 }
 
@@ -128,14 +196,15 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
 cudaError_t launch_kv8_combine(bool bf16, int head_dim, const Kv8CombineArgs& a, int workers,
                                cudaStream_t stream) {
     const long long rows = (long long)a.units * a.gs;
-    const bool row_cta = (long long)a.units * 32 < workers;
-    const long long ctas = 1 + (row_cta ? rows : (rows + kMergeSlots - 1) / kMergeSlots);
+    // more than about eight segments a unit, if every worker has work
+    const bool row_cta = (long long)a.units * 8 < workers;
+    const long long ctas = 1 + (row_cta ? rows : (rows + kWarps - 1) / kWarps);
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)ctas);
 #define PKV_KV8_COMBINE(T, D)                                                                  \
-    return row_cta ? launch_pdl(kv8_combine_kernel<T, D, true>, grid, dim3(kMergeSlots * 32), 0, \
+    return row_cta ? launch_pdl(kv8_combine_kernel<T, D, true>, grid, dim3(kWarps * 32), 0, \
                                 stream, a)                                                      \
-                   : launch_pdl(kv8_combine_kernel<T, D, false>, grid, dim3(kMergeSlots * 32),  \
+                   : launch_pdl(kv8_combine_kernel<T, D, false>, grid, dim3(kWarps * 32),  \
                                 0, stream, a)
     if (bf16) {
         if (head_dim == 128) PKV_KV8_COMBINE(__nv_bfloat16, 128);

@@ -235,14 +235,8 @@ __device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* 
 }
 
 // NT tiles of 8 query rows; a unit has at most 8 NT rows.
-#ifndef KV8_MB
-#define KV8_MB 1
-#endif
-#ifndef KV8_KC
-#define KV8_KC 2
-#endif
 template <typename T, int D, int NT, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? KV8_MB : 1)
+__global__ void __launch_bounds__(WARPS * 32)
 kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                   const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -269,7 +263,19 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar) + warp * STAGES;
     int32_t* s_prefix = reinterpret_cast<int32_t*>(base + Lay::kOffPlan);
 
+    // every warp's last segment, when it holds a part of a unit: the unit (-1:
+    // none), whether it has the unit's first (1) and last (2) chunk, and its
+    // rows' maxima and sums (its weighted sums take the place of the ring)
+    struct Tail {
+        int u, ends, b, h, sg, rows;
+    };
+    __shared__ Tail s_tail[WARPS];
+    __shared__ float s_ml[WARPS][2 * 8 * NT];
+    static_assert(WARPS == kKv8Warps, "the combine kernel counts on it");
+    static_assert(NT * 8 * D * 4 <= Lay::kWarpKV, "a segment's sums fit its ring");
+
     if (lane == 0) {
+        s_tail[warp].u = -1;
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) mbar_init(&bar[s], 1);
         fence_barrier_init();
@@ -305,6 +311,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         sw = p.hdr->chunks_per_worker;
         r = p.hdr->extra_chunks;
     }
+    const int merge_warps = kv8_merge_warps(p.units, nw);
     ws.f0 = range_begin(gw, sw, r);
     ws.n = gw < nw ? sw + (gw < r ? 1 : 0) : 0;
     ws.a = ws.describe(p, prefix, lane);
@@ -366,9 +373,6 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         for (long long x = lane; x < vecs; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
     }
 
-#ifdef KV8_TRIG
-    pdl_trigger();
-#endif
     int st = 0;          // stage of the position at hand
     uint32_t phase = 0;  // its barrier's phase
     int i = 0;           // position
@@ -515,7 +519,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                     }
                 }
                 // one unit tile: two chains of products, added at the end
-                constexpr int KC = NT == 1 ? KV8_KC : 1;
+                constexpr int KC = NT == 1 ? 2 : 1;
                 float sk[NT][KC][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -688,9 +692,16 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         if (ws.n == 0) break;  // gave up
 
         // ---- the segment's result ----
+        // the whole unit: its output; a part: a partial state -- except, with
+        // merge_warps, where the range ends within the unit or with it: to
+        // shared memory, merged below with the other warps' of the CTA
         const bool whole = k0 == 0 && end - i == nch;
-        float* slot =
-            p.partials + (long long)(gw + u) * partial_slot_floats(p.gs, D);  // slot u + w
+        const bool to_tail = !whole && end == ws.n && merge_warps > 1;
+        if (to_tail && i < end && lane == 0) {
+            s_tail[warp] = {u, (k0 == 0 ? 1 : 0) | (k0 + end - i == nch ? 2 : 0), b, h, sg, rows};
+        }
+        float* slot = p.partials + (long long)(u + gw) * partial_slot_floats(p.gs, D);
+        float* sm_o = reinterpret_cast<float*>(wsm);  // the ring: its copies are all used up
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -714,14 +725,16 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                             Cvt<T>::pack2(o[n][4 * x + 2][c] * inv, o[n][4 * x + 2][c + 2] * inv),
                             Cvt<T>::pack2(o[n][4 * x + 3][c] * inv, o[n][4 * x + 3][c + 2] * inv));
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(slot + r * D + DPL * j);
+                    float4* dst =
+                        reinterpret_cast<float4*>((to_tail ? sm_o : slot) + r * D + DPL * j);
 #pragma unroll
                     for (int x = 0; x < MT / 2; ++x)
                         dst[x] = make_float4(o[n][2 * x][c], o[n][2 * x][c + 2],
                                              o[n][2 * x + 1][c], o[n][2 * x + 1][c + 2]);
                     if (j == 0) {
-                        slot[p.gs * D + r] = m[n][c];
-                        slot[p.gs * D + p.gs + r] = lr;
+                        float* ml = to_tail ? s_ml[warp] : slot + p.gs * D;
+                        ml[r] = m[n][c];
+                        ml[(to_tail ? 8 * NT : p.gs) + r] = lr;
                     }
                 }
             }
@@ -729,17 +742,66 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
     }
     const uint32_t flags = __reduce_or_sync(kFull, ws.flags);
     if (lane == 0) p.flags[gw] = flags;
+    if (merge_warps == 1) {
+        pdl_trigger();
+        return;
+    }
+    __syncthreads();
+
+    // ---- the warps' last segments: neighbours of one unit become one state ----
+    int tail_u[WARPS];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) tail_u[w] = s_tail[w].u;
+#pragma unroll
+    for (int w0 = 0; w0 < WARPS; ++w0) {
+        const int u = tail_u[w0];
+        if (u < 0 || (w0 > 0 && tail_u[w0 > 0 ? w0 - 1 : 0] == u)) continue;
+        int w1 = w0 + 1;
+#pragma unroll
+        for (int w = w0 + 1; w < WARPS; ++w)
+            if (w1 == w && tail_u[w] == u) w1 = w + 1;
+        const bool whole = (s_tail[w0].ends & 1) && (s_tail[w1 - 1].ends & 2);
+        const int b = s_tail[w0].b, h = s_tail[w0].h, sg = s_tail[w0].sg;
+        const int rows = s_tail[w0].rows;
+        float* slot = p.partials + (long long)(u + blockIdx.x * WARPS + w0) *
+                                       partial_slot_floats(p.gs, D);
+        for (int x = threadIdx.x; x < rows * (D / 4); x += WARPS * 32) {
+            const int r = x / (D / 4), v = x - r * (D / 4);
+            float M = -INFINITY;
+            for (int w = w0; w < w1; ++w) M = fmaxf(M, s_ml[w][r]);
+            float den = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = w0; w < w1; ++w) {
+                const float wt = merge_weight(s_ml[w][r], M);
+                const float4 y =
+                    reinterpret_cast<const float4*>(base + w * Lay::kWarpKV)[r * (D / 4) + v];
+                den = fmaf(wt, s_ml[w][8 * NT + r], den);
+                acc.x = fmaf(wt, y.x, acc.x);
+                acc.y = fmaf(wt, y.y, acc.y);
+                acc.z = fmaf(wt, y.z, acc.z);
+                acc.w = fmaf(wt, y.w, acc.w);
+            }
+            if (whole) {
+                const float inv = den == 0.f ? 0.f : 1.0f / den;
+                *reinterpret_cast<uint2*>(static_cast<T*>(p.out) +
+                                          p.rows.row(b, h, sg, r) * D + 4 * v) =
+                    make_uint2(Cvt<T>::pack2(acc.x * inv, acc.y * inv),
+                               Cvt<T>::pack2(acc.z * inv, acc.w * inv));
+            } else {
+                reinterpret_cast<float4*>(slot + r * D)[v] = acc;
+                if (v == 0) {
+                    slot[p.gs * D + r] = M;
+                    slot[p.gs * D + p.gs + r] = den;
+                }
+            }
+        }
+    }
     pdl_trigger();
 }
 
 template <typename T, int D, int NT>
 Kv8DecodeInfo make_kv8_decode_info() {
-#ifndef KV8_W
-#define KV8_W 4
-#define KV8_S 4
-#define KV8_MB 1
-#endif
-    constexpr int W = NT == 1 ? KV8_W : 4, S = NT == 1 ? KV8_S : 4;
+    constexpr int W = kKv8Warps, S = NT == 1 ? 2 : 4;
     Kv8DecodeInfo info;
     info.fn = kv8_decode_kernel<T, D, NT, W, S>;
     info.warps = W;
