@@ -1533,11 +1533,11 @@ pkv_status validate_kv8(const Kv8Call& c) {
     return PKV_OK;
 }
 
-// Words of the workspace's flags: the workers' (whole CTAs), then the CTAs' of
+// Words of the workspace's flags: the workers' (whole CTAs), then the tokens' of
 // a step's append.
 int kv8_flag_words(const DecodeSetup& s, int batch) {
     const int warps = s.kernel.warps();
-    return (s.workers + warps - 1) / warps * warps + pkv::kv8_append_ctas(batch);
+    return (s.workers + warps - 1) / warps * warps + batch;
 }
 
 size_t kv8_ws_bytes(const DecodeSetup& s, int batch) {
@@ -1598,7 +1598,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     a.prefix = p.prefix;
     a.hdr = p.hdr;
     a.flags = p.flags;
-    a.n_flags = ctas * warps + (append_flags ? pkv::kv8_append_ctas(c.batch) : 0);
+    a.n_flags = ctas * warps + (append_flags ? c.batch : 0);
     a.self_plan = p.self_plan;
     a.unit_cost = p.unit_cost;
     a.out = c.out;
@@ -1821,7 +1821,7 @@ pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int
     if (st != PKV_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     uint32_t* flags = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + s.ws.total) +
-                      (kv8_flag_words(s, batch) - pkv::kv8_append_ctas(batch));
+                      (kv8_flag_words(s, batch) - batch);
     if ((st = cuda_status(pkv::launch_kv8_append(a, head_dim, nullptr, flags, cs))) != PKV_OK)
         return st;
     return kv8_run(c, rope ? out : q, s, true, cs);

@@ -172,10 +172,9 @@ struct Kv8AppendArgs {
     uint64_t turns[64];  // theta^(-2i/D) / 2 pi, its fraction times 2^64
 };
 
-// PKV_DEV_* bits of skipped runs: ORed into *status (nullable), or, with
-// flags, written to flags[CTA] for every CTA (kv8_append_ctas of them).
+// PKV_DEV_* bits of skipped runs: ORed into *status (nullable), or, without
+// seq_ids and with flags, written to flags[i] for every token i.
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* status,
                               uint32_t* flags, cudaStream_t stream);
-int kv8_append_ctas(int n_tokens);
 
 }  // namespace pkv

@@ -22,17 +22,72 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kDepth = 2;   // tasks of a warp whose rows are on the way
+constexpr int kVecs = 8;    // 16-byte vectors a lane holds of a task's rows
 constexpr int kMaxSpan = 16 + kChunk - 1;  // tokens a CTA may own (S <= 16)
 
+// Pairs of floats: the packed multiply and fused multiply-add of this part (each
+// half rounds as the scalar one does) halve the arithmetic's instructions.
+using f2 = unsigned long long;
+
+__device__ __forceinline__ f2 make_f2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split_f2(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 neg2(f2 a) { return a ^ 0x8000000080000000ull; }
+
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
-    Cvt<T>::unpack8(v, f);
+__device__ __forceinline__ void unpack(const uint4& v, f2 (&f)[4]) {
+    float x[8];
+    Cvt<T>::unpack8(v, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = make_f2(x[2 * e], x[2 * e + 1]);
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(Cvt<T>::pack2(f[0], f[1]), Cvt<T>::pack2(f[2], f[3]),
-                      Cvt<T>::pack2(f[4], f[5]), Cvt<T>::pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack(const f2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a, b;
+        split_f2(f[e], a, b);
+        w[e] = Cvt<T>::pack2(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Tables of N floats in shared memory, eight to a lane, are laid out as two halves
+// of four floats a lane: a lane's two 16-byte reads then sit next to its
+// neighbours'.  Place of float x:
+template <int N>
+__device__ __forceinline__ int place(int x) {
+    return (x & 4) * (N / 8) + (x >> 3) * 4 + (x & 3);
+}
+
+// Floats 8 jl .. 8 jl + 7 of such a table.
+template <int N>
+__device__ __forceinline__ void load8(const float* p, int jl, f2 (&f)[4]) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p + 4 * jl);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(p + N / 2 + 4 * jl);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
 }
 
 // cos and sin of position * theta^(-2i/D), from the frequency in turns as a
@@ -46,50 +101,75 @@ __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t turns, float* c, 
     sincospif(x, s, c);
 }
 
-// 1 / rms of the row whose elements HV neighbouring lanes hold.
+// 1 / rms of the row whose elements D / 16 neighbouring lanes hold.
 template <int D>
-__device__ __forceinline__ float inv_rms(const float (&lo)[8], const float (&hi)[8], float eps) {
-    float sum = 0.f;
+__device__ __forceinline__ float inv_rms(const f2 (&lo)[4], const f2 (&hi)[4], float eps) {
+    f2 sum = mul2(lo[0], lo[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], sum));
+    for (int e = 1; e < 4; ++e) sum = fma2(lo[e], lo[e], sum);
 #pragma unroll
-    for (int o = D / 32; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    return 1.0f / sqrtf(sum / (float)D + eps);
+    for (int e = 0; e < 4; ++e) sum = fma2(hi[e], hi[e], sum);
+    float a, b;
+    split_f2(sum, a, b);
+    a += b;
+#pragma unroll
+    for (int o = D / 32; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+    return 1.0f / sqrtf(a / (float)D + eps);
 }
 
-// Norm (wlo non-null: weights of the 8 low and 8 high elements; inv: 1 / rms)
-// and rotation (c non-null) of a lane's elements lo[e] and their partners hi[e].
-__device__ __forceinline__ void norm_rotate(float (&lo)[8], float (&hi)[8], const float* wlo,
-                                            const float* whi, float inv, const float* c,
-                                            const float* s) {
-    if (wlo) {
+// Norm: a lane's elements lo and their partners hi times 1 / rms and the weights
+// wlo, whi.
+__device__ __forceinline__ void scale_row(f2 (&lo)[4], f2 (&hi)[4], float inv, const f2 (&wlo)[4],
+                                          const f2 (&whi)[4]) {
+    const f2 i2 = make_f2(inv, inv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            lo[e] = lo[e] * inv * wlo[e];
-            hi[e] = hi[e] * inv * whi[e];
-        }
-    }
-    if (c) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = lo[e], b = hi[e];
-            lo[e] = fmaf(a, c[e], -b * s[e]);
-            hi[e] = fmaf(b, c[e], a * s[e]);
-        }
+    for (int e = 0; e < 4; ++e) {
+        lo[e] = mul2(mul2(lo[e], i2), wlo[e]);
+        hi[e] = mul2(mul2(hi[e], i2), whi[e]);
     }
 }
 
-// Eight elements times inv (2^-e) as e4m3 bytes; bad: some element is not
-// finite (stored as NaN).
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv, bool bad) {
-    float y[8];
+__device__ __forceinline__ void rotate_row(f2 (&lo)[4], f2 (&hi)[4], const f2 (&c)[4],
+                                           const f2 (&s)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        y[e] = x[e] * inv;
-        if (bad && !(fabsf(x[e]) <= 3.402823466e38f)) y[e] = __uint_as_float(0x7fc00000u);
+    for (int e = 0; e < 4; ++e) {
+        const f2 a = lo[e], b = hi[e];
+        lo[e] = fma2(a, c[e], mul2(b, neg2(s[e])));
+        hi[e] = fma2(b, c[e], mul2(a, s[e]));
     }
-    return make_uint2(f2_to_e4m3x2(y[0], y[1]) | f2_to_e4m3x2(y[2], y[3]) << 16,
-                      f2_to_e4m3x2(y[4], y[5]) | f2_to_e4m3x2(y[6], y[7]) << 16);
+}
+
+// Eight elements times up (2^-e) as e4m3 bytes.
+__device__ __forceinline__ uint2 quantise8(const f2 (&x)[4], float up) {
+    const f2 u2 = make_f2(up, up);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a, b;
+        split_f2(mul2(x[e], u2), a, b);
+        w[e] = f2_to_e4m3x2(a, b);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+__device__ __forceinline__ float max_abs8(const f2 (&x)[4], float m) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a, b;
+        split_f2(x[e], a, b);
+        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));  // a NaN is passed over
+    }
+    return m;
+}
+
+// A lane's vectors of a task come through shared memory by asynchronous copies
+// (its own vectors only: no other lane waits for them), two tasks ahead: in
+// registers the loads in flight would have to wait for the arithmetic of the task
+// before (96 us against ... of the prompts below).
+__device__ __forceinline__ void copy_vec(uint32_t dst, const uint4* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
 }
 
 struct Run {
@@ -99,73 +179,29 @@ struct Run {
     long long blk;  // block of the pool at head 0: page * Hkv * (P / 16) + block of the page
 };
 
-// One (run, head, side) by a warp.  The rows stay packed in registers; what is
-// computed from them (the norm, the rotation) is computed twice, for the largest
-// element and for the bytes, which costs less than the registers for it would in
-// warps at work (64 more a thread).
-template <typename T, int D, bool kK>
-__device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& r, int h,
-                                             int tok0, const float* ctab, const float* stab,
-                                             const float* wk, int lane) {
-    constexpr int HV = D / 16;        // lanes a row
-    constexpr int RPP = 32 / HV;      // rows a pass
-    constexpr int PASSES = kChunk / RPP;
-    const int jl = lane % HV, rl = lane / HV;
-    const uint4* src = static_cast<const uint4*>(kK ? a.k_new : a.v_new);
-    uint4 vl[PASSES], vh[PASSES];
-    float inv[PASSES];
-#pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-        const int x = ps * RPP + rl;  // token of the run
-        vl[ps] = vh[ps] = make_uint4(0u, 0u, 0u, 0u);
-        if (x < r.n) {
-            const uint4* row = src + ((long long)(r.tok + x) * a.n_kv_heads + h) * (D / 8);
-            vl[ps] = row[jl];
-            vh[ps] = row[HV + jl];
-        }
-    }
-    auto values = [&](int ps, float (&lo)[8], float (&hi)[8], bool first) {
-        unpack<T>(vl[ps], lo);
-        unpack<T>(vh[ps], hi);
-        if constexpr (kK) {
-            if (first) inv[ps] = a.k_norm_w ? inv_rms<D>(lo, hi, a.norm_eps) : 1.f;
-            const int at = (r.tok - tok0 + min(ps * RPP + rl, r.n - 1)) * (D / 2) + 8 * jl;
-            norm_rotate(lo, hi, a.k_norm_w ? wk + 8 * jl : nullptr, wk + D / 2 + 8 * jl, inv[ps],
-                        a.rope ? ctab + at : nullptr, stab + at);
-        }
-    };
-    uint32_t mx = 0u, fin = 0u;  // largest |element|, and the largest finite one, as bits
-#pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-        if (ps * RPP >= r.n) break;  // warp-uniform
-        float lo[8], hi[8];
-        values(ps, lo, hi, true);
-        if (ps * RPP + rl < r.n) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t x = __float_as_uint(lo[e]) & 0x7fffffffu;
-                const uint32_t y = __float_as_uint(hi[e]) & 0x7fffffffu;
-                mx = max(mx, max(x, y));
-                if (x < 0x7f800000u) fin = max(fin, x);
-                if (y < 0x7f800000u) fin = max(fin, y);
-            }
-        }
-    }
-    const bool bad = __any_sync(kFull, mx >= 0x7f800000u);  // it does not set the scale
-    mx = __reduce_max_sync(kFull, fin);
-    const int bpp = a.page_size / kChunk;
-    const long long blk = r.blk + (long long)h * bpp;  // [page][head][block]
-    uint8_t* pool = (kK ? a.k_pool : a.v_pool) + blk * (kChunk * D);
-    uint8_t* scale = a.scales + blk * 2 + (kK ? 0 : 1);
-    int e = kv8_need_exp(__uint_as_float(mx));
-    if (r.lo > 0) {
-        const int old = kv8_clamp_exp((int)*scale - 127);
+// What a warp needs of the block that it appends to.
+struct Target {
+    uint8_t* rows;   // the block's rows
+    uint8_t* scale;
+    const uint4* src;        // the run's first row
+    long long src_stride;    // 16-byte vectors from one token's row to the next's
+    const float* ctab;       // of the run's first token (null: no rotation)
+    const float* stab;
+    const float* w;          // norm weights (null: none)
+};
+
+// The block's exponent after a run of largest element `top`; moves the rows below
+// the run to it when it grows, and stores it.  Warp-collective.
+template <int D>
+__device__ __forceinline__ int settle_scale(const Target& t, int lo, float top, int lane) {
+    int e = kv8_need_exp(top);
+    if (lo > 0) {
+        const int old = kv8_clamp_exp((int)*t.scale - 127);
         if (e > old) {
-            // earlier rows of the block to the larger scale (exact above e4m3's
-            // smallest normal value)
+            // exact above e4m3's smallest normal value
             const float f = exp2i(old - e);
-            uint32_t* w = reinterpret_cast<uint32_t*>(pool);
-            for (int x = lane; x < r.lo * D / 4; x += 32) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(t.rows);
+            for (int x = lane; x < lo * D / 4; x += 32) {
                 uint32_t h0, h1;
                 e4m3x4_to_h2(w[x], h0, h1);
                 const float2 p = __half22float2(*reinterpret_cast<__half2*>(&h0));
@@ -177,28 +213,150 @@ __device__ __forceinline__ void append_block(const Kv8AppendArgs& a, const Run& 
         }
     }
     __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = (uint8_t)(e + 127);
-    const float up = exp2i(-e);
+    if (lane == 0) *t.scale = (uint8_t)(e + 127);
+    return e;
+}
+
+// A lane's elements of row x of the run.
+template <typename T, int D>
+__device__ __forceinline__ void row_values(const Target& t, int x, int jl, float eps, f2 (&lo)[4],
+                                           f2 (&hi)[4]) {
+    constexpr int HALF = D / 2;
+    if (t.w) {
+        f2 wlo[4], whi[4];
+        load8<HALF>(t.w, jl, wlo);
+        load8<HALF>(t.w + HALF, jl, whi);
+        scale_row(lo, hi, inv_rms<D>(lo, hi, eps), wlo, whi);
+    }
+    if (t.ctab) {
+        f2 c[4], s[4];
+        load8<HALF>(t.ctab + x * HALF, jl, c);
+        load8<HALF>(t.stab + x * HALF, jl, s);
+        rotate_row(lo, hi, c, s);
+    }
+}
+
+// A run with an infinity among its values: it is stored as NaN and does not set
+// the scale.  A row at a time, apart from the path below.
+template <typename T, int D>
+__device__ __noinline__ void append_block_with_inf(const Target& t, int n, int lo_slot, float eps,
+                                                   int lane) {
+    constexpr int HV = D / 16;
+    const int jl = lane % HV, rl = lane / HV;
+    float top = 0.f, up = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int x0 = 0; x0 < n; x0 += 32 / HV) {
+            const int x = x0 + rl;
+            const uint4* row = t.src + min(x, n - 1) * t.src_stride;
+            f2 v[2][4];
+            unpack<T>(row[jl], v[0]);
+            unpack<T>(row[HV + jl], v[1]);
+            row_values<T, D>(t, min(x, n - 1), jl, eps, v[0], v[1]);
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-        const int x = ps * RPP + rl;
-        if (x < r.n) {
-            float lo[8], hi[8];
-            values(ps, lo, hi, false);
-            uint2* row = reinterpret_cast<uint2*>(pool + (r.lo + x) * D);
-            row[jl] = quantise8(lo, up, bad);
-            row[HV + jl] = quantise8(hi, up, bad);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float p[2];
+                    split_f2(v[k][e], p[0], p[1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const bool fin = fabsf(p[c]) <= 3.402823466e38f;
+                        if (pass == 0 && fin) top = fmaxf(top, fabsf(p[c]));
+                        if (!fin) p[c] = __uint_as_float(0x7fc00000u);
+                    }
+                    v[k][e] = make_f2(p[0], p[1]);
+                }
+            if (pass == 1 && x < n) {
+                uint2* dst = reinterpret_cast<uint2*>(t.rows + (lo_slot + x) * D);
+                dst[jl] = quantise8(v[0], up);
+                dst[HV + jl] = quantise8(v[1], up);
+            }
+        }
+        if (pass == 0) {
+            top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+            up = exp2i(-settle_scale<D>(t, lo_slot, top, lane));
         }
     }
 }
 
+template <int D>
+__device__ __forceinline__ Target block_target(const Kv8AppendArgs& a, const Run& r, int h, bool k,
+                                               int tok0, const float* ctab, const float* stab,
+                                               const float* wk) {
+    const long long blk = r.blk + (long long)h * (a.page_size / kChunk);  // [page][head][block]
+    Target t;
+    t.rows = (k ? a.k_pool : a.v_pool) + blk * (kChunk * D);
+    t.scale = a.scales + blk * 2 + (k ? 0 : 1);
+    t.src_stride = (long long)a.n_kv_heads * (D / 8);
+    t.src = static_cast<const uint4*>(k ? a.k_new : a.v_new) +
+            ((long long)r.tok * a.n_kv_heads + h) * (D / 8);
+    t.ctab = k && a.rope ? ctab + (r.tok - tok0) * (D / 2) : nullptr;
+    t.stab = stab + (r.tok - tok0) * (D / 2);
+    t.w = k && a.k_norm_w ? wk : nullptr;
+    return t;
+}
+
+// One (run, head, side) by a warp; v: its rows, two vectors a lane and pass (the
+// elements of a row's lower half, their partners).  They stay packed: what is
+// computed from them (the norm, the rotation) is computed twice, for the largest
+// element and for the bytes, which costs less than the registers for it would in
+// warps at work (64 more a thread).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3)
-kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status,
-                  uint32_t* flags) {
+__device__ __forceinline__ void append_block(const Target& t, const uint4 (&v)[kVecs], int n,
+                                             int slot, float eps, int lane) {
+    constexpr int HV = D / 16;        // lanes a row
+    constexpr int RPP = 32 / HV;      // rows a pass
+    constexpr int PASSES = kChunk / RPP;
+    static_assert(2 * PASSES <= kVecs, "a block's rows fit a task");
+    const int jl = lane % HV, rl = lane / HV;
+    float top = 0.f;
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+        if (ps * RPP >= n) break;  // warp-uniform
+        f2 lo[4], hi[4];
+        unpack<T>(v[2 * ps], lo);
+        unpack<T>(v[2 * ps + 1], hi);
+        row_values<T, D>(t, min(ps * RPP + rl, n - 1), jl, eps, lo, hi);
+        if (ps * RPP + rl < n) top = max_abs8(hi, max_abs8(lo, top));
+    }
+    top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+    if (top > 3.402823466e38f) {
+        append_block_with_inf<T, D>(t, n, slot, eps, lane);
+        return;
+    }
+    const float up = exp2i(-settle_scale<D>(t, slot, top, lane));
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+        if (ps * RPP >= n) break;  // warp-uniform
+        const int x = ps * RPP + rl;
+        f2 lo[4], hi[4];
+        unpack<T>(v[2 * ps], lo);
+        unpack<T>(v[2 * ps + 1], hi);
+        row_values<T, D>(t, min(x, n - 1), jl, eps, lo, hi);
+        if (x < n) {
+            uint2* row = reinterpret_cast<uint2*>(t.rows + (slot + x) * D);
+            row[jl] = quantise8(lo, up);
+            row[HV + jl] = quantise8(hi, up);
+        }
+    }
+}
+
+// cos / sin tables, weights, and the warps' rings.
+template <int D>
+constexpr int kSmemBytes = 2 * kMaxSpan * (D / 2) * 4 + 2 * D * 4 + kWarps * kDepth * kVecs * 512;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status) {
     constexpr int HALF = D / 2, HV = D / 16;
-    __shared__ float ctab[kMaxSpan * HALF], stab[kMaxSpan * HALF];
-    __shared__ float wq[D], wk[D];
+    extern __shared__ __align__(16) uint8_t smem[];  // kSmemBytes<D>
+    float* ctab = reinterpret_cast<float*>(smem);
+    float* stab = ctab + kMaxSpan * HALF;
+    float* wq = stab + kMaxSpan * HALF;
+    float* wk = wq + D;
+    const uint32_t ring = smem_u32(wk + D) + (threadIdx.x >> 5) * (kDepth * kVecs * 512) +
+                          (threadIdx.x & 31) * 16;  // this lane's first vector
     __shared__ int s_pos[kMaxSpan];
     __shared__ Run s_runs[kMaxSpan];
     __shared__ int s_first, s_end, s_nruns;
@@ -210,8 +368,9 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         for (int x = tid; x < D; x += kThreads) {
             const T* q = static_cast<const T*>(a.q_norm_w);
             const T* k = static_cast<const T*>(a.k_norm_w);
-            wq[x] = q ? (float)q[x] : 1.f;
-            wk[x] = k ? (float)k[x] : 1.f;
+            const int at = x / HALF * HALF + place<HALF>(x % HALF);
+            wq[at] = q ? (float)q[x] : 1.f;
+            wk[at] = k ? (float)k[x] : 1.f;
         }
     }
     if (warp == 0) {
@@ -220,11 +379,11 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         const int i = base + lane;
         const bool in = i < a.n_tokens;
         const int pos = in ? a.positions[i] : -1;
-        const int seq = in ? (a.seq_ids ? a.seq_ids[i] : i) : -1;
+        const int seq = in ? a.seq_ids[i] : -1;
         int ppos = __shfl_up_sync(kFull, pos, 1), pseq = __shfl_up_sync(kFull, seq, 1);
         if (lane == 0) {
             ppos = base > 0 ? a.positions[base - 1] : -1;
-            pseq = base > 0 ? (a.seq_ids ? a.seq_ids[base - 1] : base - 1) : -1;
+            pseq = base > 0 ? a.seq_ids[base - 1] : -1;
         }
         const bool cont = in && pos > 0 && ppos >= 0 && pseq == seq && pos - 1 == ppos &&
                           (pos & (kChunk - 1)) != 0;
@@ -261,10 +420,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
                     (pos % a.page_size) / kChunk;
         }
         skipped = __reduce_or_sync(kFull, skipped);
-        if (lane == 0) {
-            if (flags) flags[blockIdx.x] = skipped;
-            else if (skipped) set_status(status, skipped);
-        }
+        if (lane == 0 && skipped) set_status(status, skipped);
         const unsigned used = __ballot_sync(kFull, use);
         if (use) s_runs[__popc(used & ((1u << lane) - 1u))] = r;
         if (mine) s_pos[lane - first] = pos;
@@ -278,57 +434,253 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
     if (s_first < 0 || s_end <= s_first) return;  // all its tokens belong to the CTA before
     const int tok0 = base + s_first;
     const int ntok = s_end - s_first;
-    if (a.rope) {
+    // a warp's tasks: K and V blocks, then stretches of one token's q rows (which
+    // share the token's cos / sin, and the weights, in registers)
+    constexpr int RPP = 32 / HV, PASSES = kChunk / RPP, U = kVecs / 2;
+    const int per_run = a.n_kv_heads * 2;
+    const int blocks = s_nruns * per_run;
+    const int stretches = a.q ? (a.n_q_heads + U * RPP - 1) / (U * RPP) : 0;
+    const int tasks = blocks + ntok * stretches;
+    const int jl = lane % HV, rl = lane / HV;
+    auto fetch = [&](int x, int buf) {
+        const uint32_t dst = ring + buf * (kVecs * 512);
+        if (x < blocks) {
+            const int ri = x / per_run, y = x - ri * per_run;
+            const Run& r = s_runs[ri];
+            const uint4* src = static_cast<const uint4*>(y & 1 ? a.v_new : a.k_new) +
+                               ((long long)r.tok * a.n_kv_heads + (y >> 1)) * (D / 8) + jl;
+            const long long stride = (long long)a.n_kv_heads * (D / 8);
+#pragma unroll
+            for (int ps = 0; ps < PASSES; ++ps) {
+                const int k = ps * RPP + rl;  // token of the run
+                const uint4* row = src + (k < r.n ? k * stride : 0);
+                copy_vec(dst + (2 * ps) * 512, row, k < r.n);
+                copy_vec(dst + (2 * ps + 1) * 512, row + HV, k < r.n);
+            }
+        } else if (x < tasks) {
+            const int tk = (x - blocks) / stretches;
+            const int h0 = (x - blocks - tk * stretches) * (U * RPP) + rl;
+            const uint4* src = static_cast<const uint4*>(a.q) +
+                               (long long)(tok0 + tk) * a.n_q_heads * (D / 8) + jl;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int h = h0 + k * RPP;
+                const uint4* row = src + (h < a.n_q_heads ? h * (D / 8) : 0);
+                copy_vec(dst + (2 * k) * 512, row, h < a.n_q_heads);
+                copy_vec(dst + (2 * k + 1) * 512, row + HV, h < a.n_q_heads);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) fetch(warp + k * kWarps, k);
+    if (a.rope) {  // while the first rows come
         for (int x = tid; x < ntok * HALF; x += kThreads) {
-            const int tk = x / HALF;
-            turn_cos_sin(s_pos[tk], a.turns[x - tk * HALF], &ctab[x], &stab[x]);
+            const int tk = x / HALF, i = x - tk * HALF;
+            const int at = tk * HALF + place<HALF>(i);
+            turn_cos_sin(s_pos[tk], a.turns[i], &ctab[at], &stab[at]);
         }
         __syncthreads();
     }
-    // K and V blocks
-    const int nruns = s_nruns;
-    const int per_run = a.n_kv_heads * 2;
-    for (int x = warp; x < nruns * per_run; x += kThreads / 32) {
-        const int ri = x / per_run, y = x - ri * per_run;
-        const Run r = s_runs[ri];
-        if (y & 1) append_block<T, D, false>(a, r, y >> 1, tok0, ctab, stab, wk, lane);
-        else append_block<T, D, true>(a, r, y >> 1, tok0, ctab, stab, wk, lane);
-    }
-    // q rows: HV lanes each
-    if (a.q) {
-        const uint4* q = static_cast<const uint4*>(a.q);
-        uint4* qo = static_cast<uint4*>(a.q_out);
-        const long long row0 = (long long)tok0 * a.n_q_heads;
-        const int rows = ntok * a.n_q_heads;
-        const int jl = lane % HV;
-        constexpr int STEP = kThreads / HV, U = 4;  // rows a pass of the CTA; passes in flight
-        for (int r0 = warp * (32 / HV) + lane / HV; r0 - lane / HV < rows; r0 += U * STEP) {
-            uint4 vl[U], vh[U];
+    int buf = 0;
+    for (int x = warp; x < tasks; x += kWarps) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        uint4 v[kVecs];
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-                vl[x] = vh[x] = make_uint4(0u, 0u, 0u, 0u);
-                const int r = r0 + x * STEP;
-                if (r < rows) {
-                    const uint4* row = q + (row0 + r) * (D / 8);
-                    vl[x] = row[jl];
-                    vh[x] = row[HV + jl];
+        for (int k = 0; k < kVecs; ++k)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                         : "r"(ring + (buf * kVecs + k) * 512));
+        fetch(x + kDepth * kWarps, buf);
+        buf = buf + 1 == kDepth ? 0 : buf + 1;
+        if (x < blocks) {
+            const int ri = x / per_run, y = x - ri * per_run;
+            const Run r = s_runs[ri];
+            append_block<T, D>(block_target<D>(a, r, y >> 1, !(y & 1), tok0, ctab, stab, wk), v,
+                               r.n, r.lo, a.norm_eps, lane);
+            continue;
+        }
+        const int tk = (x - blocks) / stretches;
+        const int h0 = (x - blocks - tk * stretches) * (U * RPP) + rl;
+        uint4* qo = static_cast<uint4*>(a.q_out) +
+                    (long long)(tok0 + tk) * a.n_q_heads * (D / 8) + jl;
+        f2 c[4], sn[4], wlo[4], whi[4];
+        if (a.q_norm_w) {
+            load8<HALF>(wq, jl, wlo);
+            load8<HALF>(wq + HALF, jl, whi);
+        }
+        if (a.rope) {
+            load8<HALF>(ctab + tk * HALF, jl, c);
+            load8<HALF>(stab + tk * HALF, jl, sn);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = h0 + k * RPP;
+            if (h - rl >= a.n_q_heads) break;  // warp-uniform
+            f2 lo[4], hi[4];
+            unpack<T>(v[2 * k], lo);
+            unpack<T>(v[2 * k + 1], hi);
+            if (a.q_norm_w) scale_row(lo, hi, inv_rms<D>(lo, hi, a.norm_eps), wlo, whi);
+            if (a.rope) rotate_row(lo, hi, c, sn);
+            if (h < a.n_q_heads) {
+                qo[h * (D / 8)] = pack<T>(lo);
+                qo[h * (D / 8) + HV] = pack<T>(hi);
+            }
+        }
+    }
+    pdl_trigger();
+}
+
+// One token of every sequence (no seq_ids): every token is a run of its own, so
+// nothing has to be found out before its rows are fetched, and D / 16 lanes take a
+// row each -- of q, K or V -- instead of a warp a block.  A CTA per token.  What
+// bounds it: latency (the position, the page, the block's scale, one after the
+// other, with the rows on the way beside them).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+kv8_append_single_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* status,
+                         uint32_t* flags) {
+    constexpr int HALF = D / 2, HV = D / 16, GROUPS = kThreads / HV, U = 2;
+    __shared__ __align__(16) float ctab[HALF], stab[HALF];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int jl = lane % HV, grp = tid / HV;
+    const int tok = blockIdx.x;
+    pdl_wait();
+    const int pos = a.positions[tok];
+    const int nq = a.q ? a.n_q_heads : 0, rows = nq + 2 * a.n_kv_heads;
+    // row r: q heads, then K heads, then V heads
+    auto source = [&](int r) -> const uint4* {
+        if (r < nq)
+            return static_cast<const uint4*>(a.q) + ((long long)tok * nq + r) * (D / 8) + jl;
+        const int h = r - nq;
+        const bool k = h < a.n_kv_heads;
+        return static_cast<const uint4*>(k ? a.k_new : a.v_new) +
+               ((long long)tok * a.n_kv_heads + (k ? h : h - a.n_kv_heads)) * (D / 8) + jl;
+    };
+    uint4 vl[U], vh[U];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = r0 + k * GROUPS;
+            vl[k] = vh[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+                const uint4* src = source(r);
+                vl[k] = src[0];
+                vh[k] = src[HV];
+            }
+        }
+    };
+    fetch(grp);
+    uint32_t bits = 0;
+    long long blk0 = -1;  // the block at head 0; -1: nothing is appended
+    if (pos >= 0) {
+        const int col = pos / a.page_size;
+        int page = -1;
+        if (col < a.table_stride) page = a.table[(long long)tok * a.table_stride + col];
+        else bits = PKV_DEV_BAD_LEN;
+        if (page >= 0 && page < a.num_pages)
+            blk0 = (long long)page * a.n_kv_heads * (a.page_size / kChunk) +
+                   pos % a.page_size / kChunk;
+        else if (!bits) bits = PKV_DEV_BAD_PAGE;
+    }
+    if (tid == 0) {
+        if (flags) flags[blockIdx.x] = bits;
+        else if (bits) set_status(status, bits);
+    }
+    if (a.rope) {
+        for (int i = tid; i < HALF; i += kThreads)
+            turn_cos_sin(pos, a.turns[i], &ctab[place<HALF>(i)], &stab[place<HALF>(i)]);
+        __syncthreads();
+    }
+    const int slot = pos & (kChunk - 1);
+    for (int r0 = grp; r0 - lane / HV < rows; r0 += U * GROUPS) {
+        if (r0 != grp) fetch(r0);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = r0 + k * GROUPS;
+            if (r - lane / HV >= rows) break;  // warp-uniform
+            f2 lo[4], hi[4];
+            unpack<T>(vl[k], lo);
+            unpack<T>(vh[k], hi);
+            const bool is_q = r < nq, is_k = !is_q && r < nq + a.n_kv_heads;
+            const void* w = is_q ? a.q_norm_w : is_k ? a.k_norm_w : nullptr;
+            if (a.q_norm_w || a.k_norm_w) {
+                const float inv = inv_rms<D>(lo, hi, a.norm_eps);  // every lane takes part
+                if (w) {
+                    const T* wt = static_cast<const T*>(w);
+                    f2 wlo[4], whi[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        wlo[e] = make_f2((float)wt[8 * jl + 2 * e], (float)wt[8 * jl + 2 * e + 1]);
+                        whi[e] = make_f2((float)wt[HALF + 8 * jl + 2 * e],
+                                         (float)wt[HALF + 8 * jl + 2 * e + 1]);
+                    }
+                    scale_row(lo, hi, inv, wlo, whi);
                 }
             }
+            if (a.rope && (is_q || is_k)) {
+                f2 c[4], s[4];
+                load8<HALF>(ctab, jl, c);
+                load8<HALF>(stab, jl, s);
+                rotate_row(lo, hi, c, s);
+            }
+            float top = max_abs8(hi, max_abs8(lo, 0.f));
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int r = r0 + x * STEP;
-                if (r - lane / HV >= rows) break;  // warp-uniform
-                float lo[8], hi[8];
-                unpack<T>(vl[x], lo);
-                unpack<T>(vh[x], hi);
-                const float inv = a.q_norm_w ? inv_rms<D>(lo, hi, a.norm_eps) : 1.f;
-                if (r >= rows) continue;
-                const int c = r / a.n_q_heads * HALF + 8 * jl;
-                norm_rotate(lo, hi, a.q_norm_w ? wq + 8 * jl : nullptr, wq + HALF + 8 * jl, inv,
-                            a.rope ? ctab + c : nullptr, stab + c);
-                uint4* row = qo + (row0 + r) * (D / 8);
-                row[jl] = pack<T>(lo);
-                row[HV + jl] = pack<T>(hi);
+            for (int o = HV / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            if (__any_sync(kFull, top > 3.402823466e38f && !is_q && r < rows)) {
+                // an infinity: stored as NaN, and it does not set the scale
+                top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    f2& x = e < 4 ? lo[e & 3] : hi[e & 3];
+                    float p[2];
+                    split_f2(x, p[0], p[1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (fabsf(p[c]) <= 3.402823466e38f) top = fmaxf(top, fabsf(p[c]));
+                        else if (!is_q) p[c] = __uint_as_float(0x7fc00000u);
+                    }
+                    x = make_f2(p[0], p[1]);
+                }
+#pragma unroll
+                for (int o = HV / 2; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            }
+            if (is_q) {
+                uint4* dst = static_cast<uint4*>(a.q_out) +
+                             ((long long)tok * nq + r) * (D / 8) + jl;
+                dst[0] = pack<T>(lo);
+                dst[HV] = pack<T>(hi);
+            }
+            const bool put = !is_q && r < rows && blk0 >= 0;
+            const int h = is_k ? r - nq : r - nq - a.n_kv_heads;
+            const long long blk = blk0 + (long long)h * (a.page_size / kChunk);
+            uint8_t* block = (is_k ? a.k_pool : a.v_pool) + (put ? blk * (kChunk * D) : 0);
+            uint8_t* scale = a.scales + (put ? blk * 2 + (is_k ? 0 : 1) : 0);
+            int e = kv8_need_exp(top);
+            if (put && slot > 0) {
+                const int old = kv8_clamp_exp((int)*scale - 127);
+                if (e > old) {  // as settle_scale
+                    const float f = exp2i(old - e);
+                    uint32_t* p = reinterpret_cast<uint32_t*>(block);
+                    for (int x = jl; x < slot * D / 4; x += HV) {
+                        uint32_t h0, h1;
+                        e4m3x4_to_h2(p[x], h0, h1);
+                        const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h0));
+                        const float2 z = __half22float2(*reinterpret_cast<__half2*>(&h1));
+                        p[x] = f2_to_e4m3x2(y.x * f, y.y * f) | f2_to_e4m3x2(z.x * f, z.y * f) << 16;
+                    }
+                } else {
+                    e = old;
+                }
+            }
+            __syncwarp();  // a row's lanes have read the old scale
+            if (put) {
+                if (jl == 0) *scale = (uint8_t)(e + 127);
+                uint2* row = reinterpret_cast<uint2*>(block + slot * D);
+                const float up = exp2i(-e);
+                row[jl] = quantise8(lo, up);
+                row[HV + jl] = quantise8(hi, up);
             }
         }
     }
@@ -337,21 +689,37 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
 
 }  // namespace
 
-static int append_span(int n_tokens) { return n_tokens <= 2048 ? 1 : 16; }
-
-int kv8_append_ctas(int n_tokens) {
-    const int span = append_span(n_tokens);
-    return n_tokens / span + (n_tokens % span ? 1 : 0);
-}
-
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* status,
                               uint32_t* flags, cudaStream_t stream) {
     if (a.n_tokens <= 0) return cudaSuccess;
-    const int span = append_span(a.n_tokens);
-    const dim3 grid((unsigned)kv8_append_ctas(a.n_tokens));
-#define PKV_KV8_APPEND(T, D) \
-    return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), 0, stream, a, span, status, \
-                      flags)
+    if (!a.seq_ids) {
+#define PKV_KV8_SINGLE(T, D)                                                                  \
+    return launch_pdl(kv8_append_single_kernel<T, D>, dim3((unsigned)a.n_tokens), dim3(kThreads), \
+                      0, stream, a, status, flags)
+        if (a.bf16) {
+            if (head_dim == 128) PKV_KV8_SINGLE(__nv_bfloat16, 128);
+            PKV_KV8_SINGLE(__nv_bfloat16, 64);
+        }
+        if (head_dim == 128) PKV_KV8_SINGLE(__half, 128);
+        PKV_KV8_SINGLE(__half, 64);
+#undef PKV_KV8_SINGLE
+    }
+    // leaders a CTA looks for among so many tokens: few tokens, a CTA for every
+    // block; many, one for about every block of a prompt, so that its angles serve
+    // a whole one
+    const int span = a.n_tokens <= 2048 ? 1 : 16;
+    const dim3 grid((unsigned)(a.n_tokens / span + (a.n_tokens % span ? 1 : 0)));
+    // more shared memory than a kernel has unasked (cheap, and per device: asked
+    // for with every launch)
+#define PKV_KV8_APPEND(T, D)                                                                     \
+    do {                                                                                         \
+        const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T, D>,                      \
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,  \
+                                                   kSmemBytes<D>);                               \
+        if (e != cudaSuccess) return e;                                                          \
+        return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), kSmemBytes<D>, stream,  \
+                          a, span, status);                                                      \
+    } while (0)
     if (a.bf16) {
         if (head_dim == 128) PKV_KV8_APPEND(__nv_bfloat16, 128);
         PKV_KV8_APPEND(__nv_bfloat16, 64);
