@@ -779,15 +779,39 @@ def paged_decode_combine(out: torch.Tensor, n_kv_heads: int, workspace: torch.Te
 # 8-bit cache: e4m3 pools with a power-of-two scale (E8M0) for each block of 16
 # tokens, KV head and side
 # ---------------------------------------------------------------------------
+# These calls are short beside a decode of a few sequences, so their checks are one
+# expression of cheap tensor queries; only when it is false does _kv8_explain look
+# for what is wrong (and raises the usual error).
 _SCALE_DTYPES = (torch.float8_e8m0fnu, torch.uint8)
+_E4M3 = torch.float8_e4m3fn
+_I32 = torch.int32
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _current(stream, dev):
+    """The raw stream of a call on the current device `dev`."""
+    if stream is not None or _raw_stream is None:
+        return _stream(stream)
+    return _raw_stream(dev)
+
+
+def _kv8_explain(*checks):
+    """Raise for the first (tensor, name, dtype, ndim) that _dev refuses."""
+    for c in checks:
+        _dev(*c)
+    raise ValueError("arguments disagree")
+
+
+def _kv8_scales(scales):
+    if scales.dtype not in _SCALE_DTYPES:
+        raise ValueError(f"scales must be float8_e8m0fnu (or its bytes), got {scales.dtype}")
 
 
 def _kv8_pools(k_pool, v_pool, scales):
-    _dev(k_pool, "k_pool", torch.float8_e4m3fn, 4)
-    _dev(v_pool, "v_pool", torch.float8_e4m3fn, 4)
+    _dev(k_pool, "k_pool", _E4M3, 4)
+    _dev(v_pool, "v_pool", _E4M3, 4)
     _dev(scales, "scales", None, 4)
-    if scales.dtype not in _SCALE_DTYPES:
-        raise ValueError(f"scales must be float8_e8m0fnu (or its bytes), got {scales.dtype}")
+    _kv8_scales(scales)
     NP, Hkv, P, D = k_pool.shape
     if v_pool.shape != k_pool.shape or scales.shape != (NP, Hkv, P // 16, 2):
         raise ValueError("k_pool/v_pool must be [NP, Hkv, P, D] and scales [NP, Hkv, P / 16, 2]")
@@ -818,25 +842,36 @@ def kv8_pool_create(num_pages: int, page_size: int, n_kv_heads: int, head_dim: i
 
 
 def _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status):
-    if pool.dtype != torch.float8_e4m3fn:
+    """(current device, tokens, dtype code) of an append's checked arguments."""
+    if pool.dtype is not _E4M3:
         raise ValueError("pool must be an 8-bit pool (kv8_pool_create)")
-    _dev(k_new, "k_new", None, 3)
+    dev = _get_device()
+    try:
+        ok = (k_new.get_device() == dev and v_new.get_device() == dev
+              and page_table.get_device() == dev and positions.get_device() == dev
+              and v_new.dtype is k_new.dtype and page_table.dtype is _I32
+              and positions.dtype is _I32 and k_new.dim() == 3 and page_table.dim() == 2
+              and positions.dim() == 1 and k_new.is_contiguous() and v_new.is_contiguous()
+              and page_table.is_contiguous() and positions.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _dev(k_new, "k_new", None, 3)
+        _kv8_explain((v_new, "v_new", k_new.dtype, 3), (page_table, "page_table", _I32, 2),
+                     (positions, "positions", _I32, 1))
     dt = _dtype_code(k_new)
-    _dev(v_new, "v_new", k_new.dtype, 3)
-    _dev(page_table, "page_table", torch.int32, 2)
-    _dev(positions, "positions", torch.int32, 1)
     N = positions.shape[0]
     if k_new.shape != (N, pool.n_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
         raise ValueError("k_new/v_new must be [tokens, Hkv, D] matching the pool and positions")
     if seq_ids is not None:
-        _dev(seq_ids, "seq_ids", torch.int32, 1)
+        _dev(seq_ids, "seq_ids", _I32, 1)
         if seq_ids.shape[0] != N:
             raise ValueError("seq_ids must have one entry per token")
     elif page_table.shape[0] < N:
         raise ValueError("page_table has fewer rows than tokens (give seq_ids)")
     if dev_status is not None:
-        _dev(dev_status, "dev_status", torch.int32)
-    return N, dt
+        _dev(dev_status, "dev_status", _I32)
+    return dev, N, dt
 
 
 def kv8_append(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor,
@@ -845,10 +880,11 @@ def kv8_append(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, page_table:
     """Append k_new/v_new [tokens, Hkv, D] (float16 or bfloat16) at positions[i]
     of sequence seq_ids[i] (default: token i's is row i of page_table): single
     tokens of a step, or prompts laid end to end."""
-    N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
-    _check(load_library().kv8_append(pool.handle, _ptr(k_new), _ptr(v_new), dt, _ptr(page_table),
-                                     page_table.shape[1], page_table.shape[0], _ptr(positions),
-                                     _ptr(seq_ids), N, _ptr(dev_status), _stream(stream)),
+    dev, N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
+    rows, cols = page_table.shape
+    _check(load_library().kv8_append(pool.handle, k_new.data_ptr(), v_new.data_ptr(), dt,
+                                     page_table.data_ptr(), cols, rows, positions.data_ptr(),
+                                     _ptr(seq_ids), N, _ptr(dev_status), _current(stream, dev)),
            "kv8_append")
 
 
@@ -861,17 +897,26 @@ def kv8_append_rope(pool: Pool, q: torch.Tensor, k_new: torch.Tensor, v_new: tor
                     norm_eps: float = 1e-6) -> torch.Tensor:
     """kv8_append with the rotary embedding of q [tokens, Hq, D] (into q_out) and
     of k_new; with a norm weight [D], the per-head RMS norm of that side first."""
-    N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
-    _dev(q, "q", k_new.dtype, 3)
-    _dev(q_out, "q_out", k_new.dtype, 3)
-    if q.shape[0] != N or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
+    dev, N, dt = _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status)
+    try:
+        ok = (q.get_device() == dev and q_out.get_device() == dev and q.dtype is k_new.dtype
+              and q_out.dtype is k_new.dtype and q.dim() == 3 and q.is_contiguous()
+              and q_out.is_contiguous() and q_out.dim() == 3)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _kv8_explain((q, "q", k_new.dtype, 3), (q_out, "q_out", k_new.dtype, 3))
+    nq, Hq, D = q.shape
+    if nq != N or D != pool.head_dim or q_out.shape != q.shape:
         raise ValueError("q/q_out must be [tokens, Hq, D] matching the pool and positions")
-    _norm_weights(q_norm_weight, k_norm_weight, q.dtype, pool.head_dim)
+    if q_norm_weight is not None or k_norm_weight is not None:
+        _norm_weights(q_norm_weight, k_norm_weight, q.dtype, D)
+    rows, cols = page_table.shape
     _check(load_library().kv8_append_rope(
-        pool.handle, _ptr(q), _ptr(k_new), _ptr(v_new), dt, _ptr(page_table),
-        page_table.shape[1], page_table.shape[0], _ptr(positions), _ptr(seq_ids), N, q.shape[1],
-        float(rope_theta), _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps),
-        _ptr(q_out), _ptr(dev_status), _stream(stream)), "kv8_append_rope")
+        pool.handle, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), dt, page_table.data_ptr(),
+        cols, rows, positions.data_ptr(), _ptr(seq_ids), N, Hq, rope_theta, _ptr(q_norm_weight),
+        _ptr(k_norm_weight), norm_eps, q_out.data_ptr(), _ptr(dev_status),
+        _current(stream, dev)), "kv8_append_rope")
     return q_out
 
 
@@ -893,19 +938,39 @@ def alloc_kv8_workspace(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: i
 
 
 def _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out, workspace, ndim):
-    _dev(q, "q", None, ndim)
+    """(current device, Hkv, D, P, NP, dtype code) of an attention call's checked arguments."""
+    dev = _get_device()
+    try:
+        ok = (q.get_device() == dev and out.get_device() == dev and k_pool.get_device() == dev
+              and v_pool.get_device() == dev and scales.get_device() == dev
+              and page_table.get_device() == dev and context_lens.get_device() == dev
+              and workspace.get_device() == dev and out.dtype is q.dtype
+              and k_pool.dtype is _E4M3 and v_pool.dtype is _E4M3 and page_table.dtype is _I32
+              and context_lens.dtype is _I32 and workspace.dtype is torch.uint8
+              and q.dim() == ndim and k_pool.dim() == 4 and scales.dim() == 4
+              and page_table.dim() == 2 and context_lens.dim() == 1 and q.is_contiguous()
+              and out.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
+              and scales.is_contiguous() and page_table.is_contiguous()
+              and context_lens.is_contiguous() and workspace.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _dev(q, "q", None, ndim)
+        _kv8_explain((out, "out", q.dtype, ndim), (k_pool, "k_pool", _E4M3, 4),
+                     (v_pool, "v_pool", _E4M3, 4), (scales, "scales", None, 4),
+                     (page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
+                     (workspace, "workspace", torch.uint8))
     dt = _dtype_code(q)
-    _dev(out, "out", q.dtype, ndim)
-    NP, Hkv, P, D = _kv8_pools(k_pool, v_pool, scales)
-    _dev(page_table, "page_table", torch.int32, 2)
-    _dev(context_lens, "context_lens", torch.int32, 1)
-    _dev(workspace, "workspace", torch.uint8)
+    _kv8_scales(scales)
+    NP, Hkv, P, D = k_pool.shape
     B = q.shape[0]
+    if v_pool.shape != k_pool.shape or scales.shape != (NP, Hkv, P // 16, 2):
+        raise ValueError("k_pool/v_pool must be [NP, Hkv, P, D] and scales [NP, Hkv, P / 16, 2]")
     if q.shape[-1] != D or out.shape != q.shape:
         raise ValueError("q/out [..., Hq, D] and pools [NP, Hkv, P, D] disagree")
     if page_table.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("page_table rows or context_lens != batch")
-    return B, Hkv, D, P, NP, dt
+    return dev, Hkv, D, P, NP, dt
 
 
 def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -915,13 +980,14 @@ def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: to
                                stream=None) -> torch.Tensor:
     """paged_decode_attention over an 8-bit cache: q, out [B, Hq, D] in float16
     or bfloat16, pools float8_e4m3fn, scales float8_e8m0fnu."""
-    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                     workspace, 3)
+    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                       workspace, 3)
+    B, Hq, _ = q.shape
     _check(load_library().paged_decode_attention_kv8(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(scales), _ptr(page_table), page_table.shape[1],
-        _ptr(context_lens), B, q.shape[1], Hkv, D, P, NP, dt, float(scale), _ptr(out),
-        _ptr(workspace), workspace.numel(), int(num_workers), _stream(stream)),
-        "paged_decode_attention_kv8")
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
+        page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP,
+        dt, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(), num_workers,
+        _current(stream, dev)), "paged_decode_attention_kv8")
     return out
 
 
@@ -932,13 +998,14 @@ def paged_decode_attention_multi_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_po
                                      stream=None) -> torch.Tensor:
     """paged_decode_attention_multi over an 8-bit cache: q, out [B, Qn, Hq, D],
     query j of sequence b attends causally to tokens 0 .. context_lens[b] - Qn + j."""
-    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                     workspace, 4)
+    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                       workspace, 4)
+    B, Qn, Hq, _ = q.shape
     _check(load_library().paged_decode_attention_multi_kv8(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(scales), _ptr(page_table), page_table.shape[1],
-        _ptr(context_lens), B, q.shape[1], q.shape[2], Hkv, D, P, NP, dt, float(scale),
-        _ptr(out), _ptr(workspace), workspace.numel(), int(num_workers), _stream(stream)),
-        "paged_decode_attention_multi_kv8")
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
+        page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Qn, Hq, Hkv, D, P,
+        NP, dt, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(), num_workers,
+        _current(stream, dev)), "paged_decode_attention_multi_kv8")
     return out
 
 
@@ -953,20 +1020,29 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
     """One decode step over an 8-bit cache: append k_new/v_new [B, Hkv, D] at
     positions[b], then decode attention into out; with rope_theta > 0 the rotary
     embedding of q and k_new (after the optional per-head RMS norm) comes first."""
-    B, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                     workspace, 3)
-    _dev(k_new, "k_new", q.dtype, 3)
-    _dev(v_new, "v_new", q.dtype, 3)
-    _dev(positions, "positions", torch.int32, 1)
-    if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D) or positions.shape[0] != B:
+    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
+                                       workspace, 3)
+    B, Hq, _ = q.shape
+    try:
+        ok = (k_new.get_device() == dev and v_new.get_device() == dev
+              and positions.get_device() == dev and k_new.dtype is q.dtype
+              and v_new.dtype is q.dtype and positions.dtype is _I32 and k_new.is_contiguous()
+              and v_new.is_contiguous() and positions.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _kv8_explain((k_new, "k_new", q.dtype, 3), (v_new, "v_new", q.dtype, 3),
+                     (positions, "positions", _I32, 1))
+    if k_new.shape != (B, Hkv, D) or v_new.shape != k_new.shape or positions.shape != (B,):
         raise ValueError("k_new/v_new must be [B, Hkv, D] and positions [B]")
-    _norm_weights(q_norm_weight, k_norm_weight, q.dtype, D)
+    if q_norm_weight is not None or k_norm_weight is not None:
+        _norm_weights(q_norm_weight, k_norm_weight, q.dtype, D)
     _check(load_library().paged_decode_step_kv8(
-        _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-        _ptr(scales), _ptr(page_table), page_table.shape[1], _ptr(context_lens), B, q.shape[1],
-        Hkv, D, P, NP, dt, float(scale), float(rope_theta), _ptr(q_norm_weight),
-        _ptr(k_norm_weight), float(norm_eps), _ptr(out), _ptr(workspace), workspace.numel(),
-        int(num_workers), _stream(stream)), "paged_decode_step_kv8")
+        k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), q.data_ptr(),
+        k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(),
+        page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP, dt, scale, rope_theta,
+        _ptr(q_norm_weight), _ptr(k_norm_weight), norm_eps, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), num_workers, _current(stream, dev)), "paged_decode_step_kv8")
     return out
 
 
