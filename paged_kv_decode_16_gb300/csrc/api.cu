@@ -83,13 +83,15 @@ struct KernelPick {
     DecodeUmmaInfo um{};
     pkv::Kv8DecodeInfo q8{};
     const void* fn() const {
-        if (variant == kVariantKv8) return reinterpret_cast<const void*>(q8.fn);
+        if (variant == kVariantKv8)
+            return q8.umma ? reinterpret_cast<const void*>(q8.umma)
+                           : reinterpret_cast<const void*>(q8.fn);
         return variant == PKV_VARIANT_TCGEN05     ? reinterpret_cast<const void*>(um.fn)
                : variant == PKV_VARIANT_TENSOR_CORES ? reinterpret_cast<const void*>(mma.fn)
                                                      : reinterpret_cast<const void*>(cc.fn);
     }
     int threads() const {
-        if (variant == kVariantKv8) return q8.warps * 32;
+        if (variant == kVariantKv8) return q8.threads;
         return variant == PKV_VARIANT_TCGEN05       ? um.threads
                : variant == PKV_VARIANT_TENSOR_CORES ? mma.warps * 32
                                                      : cc.warps * 32;
@@ -150,9 +152,26 @@ pkv_status prepare_kernel(const KernelPick& k, int* auto_workers) {
     if (cudaFuncSetAttribute(k.fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem()) !=
         cudaSuccess)
         return PKV_ERR_CUDA;
+    // the CTAs that fit an SM's shared memory need all of it to be that
+    if (k.variant == kVariantKv8 &&
+        cudaFuncSetAttribute(k.fn(), cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return PKV_ERR_CUDA;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn(), k.threads(),
                                                       k.smem()) != cudaSuccess)
         return PKV_ERR_CUDA;
+    if (k.variant == kVariantKv8 && k.q8.umma) {
+        // what the shared memory holds, at most two (the tensor memory): the query
+        // above answers 1 for a kernel that uses tensor memory
+        int smem = 0, reserved = 0;
+        if (cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) !=
+                cudaSuccess ||
+            cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) !=
+                cudaSuccess)
+            return PKV_ERR_CUDA;
+        per_sm = smem / (k.smem() + reserved);
+        per_sm = per_sm < 1 ? 1 : (per_sm > 2 ? 2 : per_sm);
+    }
     const int workers = sms * (per_sm > 0 ? per_sm : 1) * k.warps();
     std::lock_guard<std::mutex> lk(g_mu);
     g_auto_workers[key] = workers;
@@ -1426,9 +1445,15 @@ pkv_status paged_decode_attention_multi(const void* q, const void* k_pool, const
 // --- 8-bit cache (kv8.cuh) ---------------------------------------------------
 namespace {
 
-// Rows of a unit: at most 32 (four tiles of 8).  One query a sequence: the
-// query group, cut evenly when it is larger; several: as for the 16-bit kernel.
+// Rows of a unit: at most 32 (four tiles of 8) on the warp kernel, 128 on the
+// tcgen05 one, which takes over from kKv8UmmaMinRows rows of a KV head on.
 constexpr int kKv8UnitRows = 32;
+#ifndef UMIN
+#define UMIN 48
+#endif
+constexpr int kKv8UmmaMinRows = UMIN;
+// A unit's start on the tcgen05 kernel, in chunks.
+constexpr int kKv8UmmaUnitCost = 8;
 
 pkv_status setup_kv8(int batch, int n_queries, int n_q_heads, int n_kv_heads, int head_dim,
                      int page_size, pkv_dtype dtype, int num_workers, DecodeSetup* s) {
@@ -1438,12 +1463,20 @@ pkv_status setup_kv8(int batch, int n_queries, int n_q_heads, int n_kv_heads, in
     if (num_workers < 0 || n_queries < 1) return PKV_ERR_INVALID_ARG;
     if (n_queries > kMaxQueries) return PKV_ERR_UNSUPPORTED;
     s->group = n_q_heads / n_kv_heads;
-    const int t0 = (n_queries + kKv8UnitRows - 1) / kKv8UnitRows;
-    const int qpu = (n_queries + t0 - 1) / t0;
+    const bool umma = (long long)n_queries * s->group >= kKv8UmmaMinRows;
+    // warp kernel: the fewest equal tiles of query tokens, and as many heads as
+    // fit beside one; tcgen05: as many heads of the group as fit a tile, and then
+    // equal tiles of tokens
+    const int unit_rows = umma ? pkv::kKv8UmmaRows : kKv8UnitRows;
+    int hpu = 1, qpu = n_queries;
+    for (int d = 1; umma && d <= s->group; ++d)
+        if (s->group % d == 0 && d <= unit_rows) hpu = d;
+    const int most = unit_rows / hpu;  // tokens of a tile
+    const int t0 = (n_queries + most - 1) / most;
+    qpu = (n_queries + t0 - 1) / t0;
     const int tiles = (n_queries + qpu - 1) / qpu;
-    int hpu = 1;
-    for (int d = 1; d <= s->group; ++d)
-        if (s->group % d == 0 && qpu * d <= kKv8UnitRows) hpu = d;
+    for (int d = 1; !umma && d <= s->group; ++d)
+        if (s->group % d == 0 && qpu * d <= unit_rows) hpu = d;
     s->gs = qpu * hpu;
     s->sub_groups = (s->group / hpu) * tiles;
     s->rs = pkv::RowShape{n_queries, qpu, hpu, s->group / hpu, s->group, n_q_heads};
@@ -1452,8 +1485,9 @@ pkv_status setup_kv8(int batch, int n_queries, int n_q_heads, int n_kv_heads, in
     if (s->units > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     s->kernel = KernelPick();
     s->kernel.variant = kVariantKv8;
-    s->kernel.q8 = dtype == PKV_BF16 ? pkv::kv8_decode_info_bf16(head_dim, s->gs)
-                                     : pkv::kv8_decode_info_f16(head_dim, s->gs);
+    s->kernel.q8 = umma                ? pkv::kv8_umma_info(dtype == PKV_BF16, head_dim)
+                   : dtype == PKV_BF16 ? pkv::kv8_decode_info_bf16(head_dim, s->gs)
+                                       : pkv::kv8_decode_info_f16(head_dim, s->gs);
     st = prepare_kernel(s->kernel, &s->workers_auto);
     if (st != PKV_OK) return st;
     s->workers = num_workers > 0 ? num_workers : s->workers_auto;
@@ -1569,7 +1603,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.rows = s.rs;
     p.gs = s.gs;
     p.self_plan = c.batch <= pkv::kKv8SelfPlan;
-    p.unit_cost = p.self_plan ? pkv::kKv8UnitCost : 0;
+    p.unit_cost = !p.self_plan ? 0 : s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
     p.workers_req = c.num_workers;
     p.workers_auto = s.workers_auto;
     p.batch = c.batch;
@@ -1580,18 +1614,29 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.num_pages = c.num_pages;
     p.table_stride = c.table_stride;
     p.chunks_per_page = c.page_size / pkv::kChunk;
+    p.page_magic = pkv::kv8_page_magic(p.chunks_per_page);
     p.cap = (long long)c.table_stride * c.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
-    CUtensorMap km, vm;
-    const long long rows = (long long)c.num_pages * c.n_kv_heads * c.page_size;
-    pkv_status st = kv8_map(c.k_pool, rows, c.head_dim, &km);
-    if (st == PKV_OK) st = kv8_map(c.v_pool, rows, c.head_dim, &vm);
-    if (st == PKV_OK && !p.self_plan)
+    pkv_status st = PKV_OK;
+    if (!p.self_plan)
         st = do_plan(c.lens, nullptr, c.batch, c.page_size, c.table_stride, c.num_workers,
                      c.workspace, s, nullptr, stream);
-    if (st == PKV_OK)
-        st = cuda_status(pkv::launch_pdl(s.kernel.q8.fn, dim3(ctas), dim3(warps * 32),
-                                         s.kernel.smem(), stream, p, km, vm));
+    if (st != PKV_OK) return st;
+    if (s.kernel.q8.umma) {
+        st = cuda_status(pkv::launch_pdl(s.kernel.q8.umma, dim3(ctas), dim3(s.kernel.threads()),
+                                         s.kernel.smem(), stream, p,
+                                         static_cast<const uint8_t*>(c.k_pool),
+                                         static_cast<const uint8_t*>(c.v_pool)));
+    } else {
+        CUtensorMap km, vm;
+        const long long rows = (long long)c.num_pages * c.n_kv_heads * c.page_size;
+        st = kv8_map(c.k_pool, rows, c.head_dim, &km);
+        if (st == PKV_OK) st = kv8_map(c.v_pool, rows, c.head_dim, &vm);
+        if (st == PKV_OK)
+            st = cuda_status(pkv::launch_pdl(s.kernel.q8.fn, dim3(ctas),
+                                             dim3(s.kernel.threads()), s.kernel.smem(), stream, p,
+                                             km, vm));
+    }
     if (st != PKV_OK) return st;
     pkv::Kv8CombineArgs a = {};
     a.partials = p.partials;
@@ -1601,6 +1646,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     a.n_flags = ctas * warps + (append_flags ? c.batch : 0);
     a.self_plan = p.self_plan;
     a.unit_cost = p.unit_cost;
+    a.warps = warps;
     a.out = c.out;
     a.units = (int)s.units;
     a.units_per_b = s.units_per_b;

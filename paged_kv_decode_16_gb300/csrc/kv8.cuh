@@ -74,6 +74,16 @@ constexpr int kKv8MinPositions = 4;
 
 constexpr int kKv8Warps = 4;  // workers (warps) of a CTA of the decode kernel
 
+// k / cpp as the high word of k * magic, for cpp = 1 .. 16 (chunks of a page) and k
+// below 2^27 (chunks of a sequence): magic * cpp exceeds 2^32 by less than 16.
+// 0 stands for cpp = 1.
+inline uint32_t kv8_page_magic(int cpp) {
+    return cpp == 1 ? 0u : (uint32_t)(((1ull << 32) + cpp - 1) / cpp);
+}
+__device__ __forceinline__ int kv8_page_col(int k, uint32_t magic) {
+    return magic ? (int)__umulhi((uint32_t)k, magic) : k;
+}
+
 // Workers and the split of `total` positions over them: sw each, one more for
 // the first r.
 __host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, int workers_auto,
@@ -96,8 +106,9 @@ __host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, 
 // workers a unit: 23.6 against 22.1 us); one sequence of 32768 tokens (228 a unit)
 // gains more in the combine (23.4 us both together against 24.4, and 15.2 against
 // 18.7 with one KV head).
-__host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw) {
-    return nw / 32 > units ? kKv8Warps : 1;
+// (warps: workers of a CTA.)
+__host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw, int warps) {
+    return nw / 32 > units ? warps : 1;
 }
 
 struct Kv8DecodeParams {
@@ -117,6 +128,7 @@ struct Kv8DecodeParams {
     int workers_req, workers_auto;
     int batch, n_kv_heads, sub_groups, units_per_b, units, num_pages, table_stride;
     int chunks_per_page;
+    uint32_t page_magic;    // kv8_page_magic(chunks_per_page)
     long long cap;          // tokens of a table row
     float scale_log2;       // scale * log2(e)
 };
@@ -125,14 +137,20 @@ struct Kv8DecodeParams {
 // tensor maps).
 struct Kv8DecodeInfo {
     void (*fn)(Kv8DecodeParams, CUtensorMap, CUtensorMap) = nullptr;
-    int warps = 0;
-    int stages = 0;
+    void (*umma)(Kv8DecodeParams, const uint8_t*, const uint8_t*) = nullptr;  // instead of fn
+    int warps = 0;    // workers of a CTA
+    int threads = 0;
     int smem_bytes = 0;
 };
 
 // rows: query rows of a unit, 1 .. 32.
 Kv8DecodeInfo kv8_decode_info_bf16(int head_dim, int rows);
 Kv8DecodeInfo kv8_decode_info_f16(int head_dim, int rows);
+
+// Units of up to kKv8UmmaRows rows on the fifth-generation tensor cores
+// (kv8_umma.cu); takes the pools' addresses.
+constexpr int kKv8UmmaRows = 128;
+Kv8DecodeInfo kv8_umma_info(bool bf16, int head_dim);
 
 // Merges the units that several workers share, and sets the workspace's status
 // to the OR of n_flags words (and of the plan kernel's, when it ran).
@@ -143,6 +161,7 @@ struct Kv8CombineArgs {
     const uint32_t* flags;
     int n_flags;
     int self_plan, unit_cost;
+    int warps;  // workers of a CTA of the decode kernel
     void* out;
     int units, units_per_b, sub_groups, gs;
     RowShape rows;

@@ -145,7 +145,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     if (per_unit == 0) return;  // no tokens: the decode kernel wrote zeros
     const int at = first + uidx * per_unit;
     const Segs segs = kv8_segments(sw, r, u, at + a.unit_cost, at + per_unit - 1,
-                                   kv8_merge_warps(a.units, nw));
+                                   kv8_merge_warps(a.units, nw, a.warps));
     if (segs.count <= 1) return;  // finished in the decode kernel
     const int stride = partial_slot_floats(a.gs, D);
     T* out = static_cast<T*>(a.out) + a.rows.row(b, h, sg, g) * D;

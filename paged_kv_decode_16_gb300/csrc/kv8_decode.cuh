@@ -41,7 +41,7 @@
 #include <type_traits>
 
 #include "decode_mma.cuh"
-#include "kv8.cuh"
+#include "kv8_plan.cuh"
 #include "merge.cuh"
 #include "schedule.cuh"
 
@@ -86,7 +86,7 @@ struct Kv8Stream {
         d.k = rem - uidx * per_unit - p.unit_cost;
         d.len = (int)min((long long)p.lens[lo], p.cap);
         if (d.k < 0) return d;
-        const int col = d.k / p.chunks_per_page;
+        const int col = kv8_page_col(d.k, p.page_magic);
         const int page = __ldg(p.table + (long long)lo * p.table_stride + col);
         if (page >= 0 && page < p.num_pages) {
             const int blk = (page * p.n_kv_heads + uidx / p.sub_groups) * p.chunks_per_page +
@@ -172,68 +172,6 @@ struct Kv8Layout {
     static constexpr int kBytes = kOffPlan + (kKv8SelfPlan + 1) * 4 + 1024;  // + alignment slack
 };
 
-// The ranges of the whole batch by one CTA: prefix sums into s_prefix, and the
-// positions' total.  CTA 0 leaves them in the workspace for the combine kernel.
-template <int THREADS>
-__device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* s_prefix,
-                                             uint32_t* flags) {
-    static_assert(kKv8SelfPlan % THREADS == 0, "whole sequences per thread");
-    constexpr int PER = kKv8SelfPlan / THREADS, NWARPS = THREADS / 32;
-    __shared__ long long s_tot[NWARPS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int cnt[PER];
-    long long sum = 0;
-#pragma unroll
-    for (int x = 0; x < PER; ++x) {
-        const int b = tid * PER + x;
-        long long len = b < p.batch ? p.lens[b] : 0;
-        if (len < 0 || len > p.cap) {
-            if (blockIdx.x == 0) *flags |= PKV_DEV_BAD_LEN;
-            len = len < 0 ? 0 : p.cap;
-        }
-        const int nch = (int)((len + kChunk - 1) / kChunk);
-        // a sequence of more positions than an int: over the limit in any case
-        const long long c = nch ? (long long)(nch + p.unit_cost) * p.units_per_b : 0;
-        cnt[x] = (int)min(c, 0x7fffffffLL);
-        sum += cnt[x];
-    }
-    long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_tot[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < NWARPS; ++w) {
-        if (w < warp) before += s_tot[w];
-        total += s_tot[w];
-    }
-    if (total > 0x7fffffffLL) {  // beyond the 32-bit positions: refuse the work
-        if (blockIdx.x == 0) *flags |= PKV_DEV_BAD_LEN;
-        total = 0;
-    }
-    long long at = before + incl - sum;
-#pragma unroll
-    for (int x = 0; x < PER; ++x) {
-        const int b = tid * PER + x;
-        const int v = total ? (int)at : 0;
-        if (b <= p.batch) {
-            s_prefix[b] = v;
-            if (blockIdx.x == 0) p.prefix[b] = v;
-        }
-        at += cnt[x];
-    }
-    if (tid == THREADS - 1 && p.batch == kKv8SelfPlan) {
-        s_prefix[kKv8SelfPlan] = (int)total;
-        if (blockIdx.x == 0) p.prefix[kKv8SelfPlan] = (int)total;
-    }
-    __syncthreads();
-    return (int)total;
-}
-
 // NT tiles of 8 query rows; a unit has at most 8 NT rows.
 template <typename T, int D, int NT, int WARPS, int STAGES>
 __global__ void __launch_bounds__(WARPS * 32)
@@ -311,7 +249,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         sw = p.hdr->chunks_per_worker;
         r = p.hdr->extra_chunks;
     }
-    const int merge_warps = kv8_merge_warps(p.units, nw);
+    const int merge_warps = kv8_merge_warps(p.units, nw, WARPS);
     ws.f0 = range_begin(gw, sw, r);
     ws.n = gw < nw ? sw + (gw < r ? 1 : 0) : 0;
     ws.a = ws.describe(p, prefix, lane);
@@ -805,7 +743,7 @@ Kv8DecodeInfo make_kv8_decode_info() {
     Kv8DecodeInfo info;
     info.fn = kv8_decode_kernel<T, D, NT, W, S>;
     info.warps = W;
-    info.stages = S;
+    info.threads = W * 32;
     info.smem_bytes = Kv8Layout<D, NT, S, W>::kBytes;
     return info;
 }
