@@ -1448,10 +1448,7 @@ namespace {
 // Rows of a unit: at most 32 (four tiles of 8) on the warp kernel, 128 on the
 // tcgen05 one, which takes over from kKv8UmmaMinRows rows of a KV head on.
 constexpr int kKv8UnitRows = 32;
-#ifndef UMIN
-#define UMIN 48
-#endif
-constexpr int kKv8UmmaMinRows = UMIN;
+constexpr int kKv8UmmaMinRows = 64;
 // A unit's start on the tcgen05 kernel, in chunks.
 constexpr int kKv8UmmaUnitCost = 8;
 
@@ -1604,6 +1601,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.gs = s.gs;
     p.self_plan = c.batch <= pkv::kKv8SelfPlan;
     p.unit_cost = !p.self_plan ? 0 : s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
+    p.merge = s.units * s.gs <= pkv::kKv8RowCtas ? warps : 1;
     p.workers_req = c.num_workers;
     p.workers_auto = s.workers_auto;
     p.batch = c.batch;
@@ -1646,7 +1644,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     a.n_flags = ctas * warps + (append_flags ? c.batch : 0);
     a.self_plan = p.self_plan;
     a.unit_cost = p.unit_cost;
-    a.warps = warps;
+    a.merge = p.merge;
     a.out = c.out;
     a.units = (int)s.units;
     a.units_per_b = s.units_per_b;

@@ -100,15 +100,20 @@ __host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, 
     *r = n > 0 ? total - *sw * n : 0;
 }
 
-// Workers whose parts of one unit are merged by their CTA before they leave it: a
-// CTA's, when units are few beside the workers (nw); else 1: none are.  Merging
-// costs the decode kernel 1.5 us at its end (32 sequences of 512 to 4096 tokens, 7
-// workers a unit: 23.6 against 22.1 us); one sequence of 32768 tokens (228 a unit)
-// gains more in the combine (23.4 us both together against 24.4, and 15.2 against
-// 18.7 with one KV head).
-// (warps: workers of a CTA.)
-__host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw, int warps) {
-    return nw / 32 > units ? warps : 1;
+// Rows of all units up to which the combine kernel gives a row of many segments a
+// CTA instead of a warp (2 sequences of 8192 tokens, 16 query tokens, 1024 rows: a
+// CTA a row 33.0 us in all, a warp 28.2).
+constexpr int kKv8RowCtas = 512;
+
+// Workers whose parts of one unit are merged by their CTA before they leave it:
+// `most` (a CTA's, or 1: beyond kKv8RowCtas rows, and where a worker is a CTA)
+// when units are few beside the workers (nw); else 1, none are.  Merging costs the
+// decode kernel 1.5 us at its end (32 sequences of 512 to 4096 tokens, 7 workers a
+// unit: 23.6 against 22.1 us); one sequence of 32768 tokens (228 a unit) gains
+// more in the combine (23.4 us both together against 24.4, and 15.2 against 18.7
+// with one KV head).
+__host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw, int most) {
+    return nw / 32 > units ? most : 1;
 }
 
 struct Kv8DecodeParams {
@@ -125,6 +130,7 @@ struct Kv8DecodeParams {
     int gs;                 // rows of a full unit (the partial states' layout)
     int self_plan;
     int unit_cost;          // positions a unit has beside its chunks
+    int merge;              // workers whose parts of a unit may be merged by their CTA
     int workers_req, workers_auto;
     int batch, n_kv_heads, sub_groups, units_per_b, units, num_pages, table_stride;
     int chunks_per_page;
@@ -161,7 +167,7 @@ struct Kv8CombineArgs {
     const uint32_t* flags;
     int n_flags;
     int self_plan, unit_cost;
-    int warps;  // workers of a CTA of the decode kernel
+    int merge;  // as the decode kernel's
     void* out;
     int units, units_per_b, sub_groups, gs;
     RowShape rows;

@@ -145,7 +145,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     if (per_unit == 0) return;  // no tokens: the decode kernel wrote zeros
     const int at = first + uidx * per_unit;
     const Segs segs = kv8_segments(sw, r, u, at + a.unit_cost, at + per_unit - 1,
-                                   kv8_merge_warps(a.units, nw, a.warps));
+                                   kv8_merge_warps(a.units, nw, a.merge));
     if (segs.count <= 1) return;  // finished in the decode kernel
     const int stride = partial_slot_floats(a.gs, D);
     T* out = static_cast<T*>(a.out) + a.rows.row(b, h, sg, g) * D;
@@ -182,8 +182,8 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
         store_row<T>(sum, total, lane, out);
     } else {
         float M, den;
-        // (merged warps come with few units, so with kRowCta: here the slots are
-        // next to each other)
+        // (merged warps come with few rows, so with kRowCta: here the slots are next
+        // to each other)
         const float* slots = a.partials + (segs.u + segs.w0) * (long long)stride;
         const float4 acc = merge_some<D>([&](int s) { return slots + s * stride; }, segs.count,
                                          g * D, a.gs * D + g, a.gs * D + a.gs + g, lane, M, den);
@@ -197,7 +197,7 @@ cudaError_t launch_kv8_combine(bool bf16, int head_dim, const Kv8CombineArgs& a,
                                cudaStream_t stream) {
     const long long rows = (long long)a.units * a.gs;
     // more than about eight segments a unit, if every worker has work
-    const bool row_cta = (long long)a.units * 8 < workers;
+    const bool row_cta = (long long)a.units * 8 < workers && rows <= kKv8RowCtas;
     const long long ctas = 1 + (row_cta ? rows : (rows + kWarps - 1) / kWarps);
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)ctas);

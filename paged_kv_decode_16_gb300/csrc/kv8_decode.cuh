@@ -249,7 +249,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         sw = p.hdr->chunks_per_worker;
         r = p.hdr->extra_chunks;
     }
-    const int merge_warps = kv8_merge_warps(p.units, nw, WARPS);
+    const int merge_warps = kv8_merge_warps(p.units, nw, p.merge);
     ws.f0 = range_begin(gw, sw, r);
     ws.n = gw < nw ? sw + (gw < r ? 1 : 0) : 0;
     ws.a = ws.describe(p, prefix, lane);

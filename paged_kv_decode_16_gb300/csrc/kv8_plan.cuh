@@ -11,8 +11,7 @@ namespace pkv {
 template <int THREADS>
 __device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* s_prefix,
                                              uint32_t* flags) {
-    static_assert(kKv8SelfPlan % THREADS == 0, "whole sequences per thread");
-    constexpr int PER = kKv8SelfPlan / THREADS, NWARPS = THREADS / 32;
+    constexpr int PER = (kKv8SelfPlan + THREADS - 1) / THREADS, NWARPS = THREADS / 32;
     __shared__ long long s_tot[NWARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int cnt[PER];
@@ -60,7 +59,7 @@ __device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* 
         }
         at += cnt[x];
     }
-    if (tid == THREADS - 1 && p.batch == kKv8SelfPlan) {
+    if (PER * THREADS == kKv8SelfPlan && tid == THREADS - 1 && p.batch == kKv8SelfPlan) {
         s_prefix[kKv8SelfPlan] = (int)total;
         if (blockIdx.x == 0) p.prefix[kKv8SelfPlan] = (int)total;
     }

@@ -35,7 +35,11 @@ namespace {
 constexpr int kRows = kKv8UmmaRows;   // M: one tensor-memory lane a row
 constexpr int kBlockChunks = 8;
 constexpr int kBlockTok = kBlockChunks * kChunk;
-constexpr int kThreads = 256;  // two threads a row
+// (Four threads a row, in 64 registers each, spill: 86 against 63 us of
+// the 64 tokens of 4 sequences of 1000 to 8192 below.)
+constexpr int kThreads = 256;
+constexpr int kParts = kThreads / 128;             // threads a row: each its part of the tokens
+constexpr int kPartChunks = kBlockChunks / kParts;  // ... and of O's columns
 
 // Shared memory of one CTA from a 1 KiB aligned base: fp16 column blocks of 64
 // elements (128 bytes a row), 8-row groups of 1 KiB.
@@ -47,9 +51,10 @@ struct Layout {
     static constexpr int kOffK = kOffQ + kCols * kColBytes;  // K, then P (2 blocks of 64 tokens)
     static constexpr int kOffV = kOffK + 2 * kColBytes;
     static constexpr int kOffEnd = kOffV + kCols * kColBytes;
-    static constexpr int kOffMax = kOffEnd;                  // [2][128] floats
-    static constexpr int kOffChunk = kOffMax + 2 * 128 * 4;  // [8] ChunkInfo
-    static constexpr int kOffBar = kOffChunk + kBlockChunks * 16;
+    static constexpr int kOffMax = kOffEnd;                  // [parts][128] floats
+    static constexpr int kOffChunk = kOffMax + kParts * 128 * 4;  // [8] ChunkInfo
+    static constexpr int kOffPages = kOffChunk + kBlockChunks * 16;  // [2][8] ids, [8] scales
+    static constexpr int kOffBar = kOffPages + 3 * kBlockChunks * 4;
     static constexpr int kOffPlan = kOffBar + 32;
     static constexpr int kUsed = kOffPlan + (kKv8SelfPlan + 1) * 4 + 1024;
     // at least 80 KiB: no more CTAs on an SM than its tensor memory serves
@@ -133,12 +138,14 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     const uint32_t sb = raw + pad;
     float* s_max = reinterpret_cast<float*>(base + Lay::kOffMax);
     ChunkInfo* s_chunk = reinterpret_cast<ChunkInfo*>(base + Lay::kOffChunk);
+    int32_t* s_pages = reinterpret_cast<int32_t*>(base + Lay::kOffPages);
+    uint32_t* s_scales = reinterpret_cast<uint32_t*>(s_pages + 2 * kBlockChunks);
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
     uint32_t* s_flags = tmem_slot + 1;
     int32_t* s_prefix = reinterpret_cast<int32_t*>(base + Lay::kOffPlan);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int row = tid & 127, half = tid >> 7;
+    const int row = tid & 127, part = tid >> 7;
 
     if (warp == 0) tmem_alloc(tmem_slot, Lay::kTmemCols);
     if (tid == 32) {
@@ -228,14 +235,21 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     // This thread's part of a block's bytes: piece tid % PPR of token rows
     // tid / PPR + ROWS i, K's and V's at different times (the L1 that the shared
     // memory leaves holds the lines of about one side of two CTAs on the way; more
-    // loads wait for room).  The page ids of the block after it are asked for at
-    // the same time, so that no load waits for another one inside a segment.
+    // loads wait for room).  Threads 0 .. 7 ask for the page ids of the block after
+    // the next one at the same time, and for the next one's scales, both into
+    // shared memory, so that no load waits for another one inside a segment.
     uint4 kr[LOADS], vr[LOADS];
-    int pages[LOADS], pg[LOADS];  // of the block after the next one; of the next one
-    uint32_t info = 0u;  // threads 0 .. 7: the chunk's scale bytes, the tokens that count << 16
+    int pg[LOADS];       // page ids of this thread's rows of the next block
+    uint32_t info = 0u;  // threads 0 .. 7: tokens of the chunk that count; bit 31: its scales
+                         // are the upper half of their word
+    int turn = 0;        // which half of s_pages has the next block's ids
     const int pc = tid % PPR, r0 = tid / PPR;
     auto page_of = [&](const Block& c, int k) {
-        return __ldg(p.table + (long long)c.b * p.table_stride + kv8_page_col(k, p.page_magic));
+        return p.table + (long long)c.b * p.table_stride + kv8_page_col(k, p.page_magic);
+    };
+    auto copy4 = [&](const void* dst, const void* src) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+                     : "memory");
     };
     auto load_side = [&](const Block& c, const uint8_t* pool, uint4 (&v)[LOADS]) {
 #pragma unroll
@@ -253,30 +267,39 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         }
     };
     auto fetch_k = [&](const Block& c) {
+        if (c.first) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int ch = (r0 + ROWS * i) / kChunk;
-            pg[i] = ch >= c.cnt ? -1 : c.first ? page_of(c, c.k + ch) : pages[i];
-            if (ch < c.cnt && (pg[i] < 0 || pg[i] >= p.num_pages)) flags |= PKV_DEV_BAD_PAGE;
+            for (int i = 0; i < LOADS; ++i) {
+                const int ch = (r0 + ROWS * i) / kChunk;
+                pg[i] = ch < c.cnt ? __ldg(page_of(c, c.k + ch)) : -1;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int ch = (r0 + ROWS * i) / kChunk;
+                pg[i] = ch < c.cnt ? s_pages[turn * kBlockChunks + ch] : -1;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if ((r0 + ROWS * i) / kChunk < c.cnt && (pg[i] < 0 || pg[i] >= p.num_pages))
+                flags |= PKV_DEV_BAD_PAGE;
         load_side(c, k_pool, kr);
         info = 0u;
         if (tid < c.cnt) {
-            const int k = c.k + tid, page = page_of(c, k);
+            const int k = c.k + tid;
+            const int page = c.first ? __ldg(page_of(c, k)) : s_pages[turn * kBlockChunks + tid];
             if (page >= 0 && page < p.num_pages) {
                 const int in_page = k - kv8_page_col(k, p.page_magic) * p.chunks_per_page;
-                info = (uint32_t)__ldg(p.scales + (long long)(page * p.n_kv_heads + c.h) *
-                                                      p.chunks_per_page + in_page) |
-                       (uint32_t)min(kChunk, c.len - k * kChunk) << 16;
+                const long long blk =
+                    (long long)(page * p.n_kv_heads + c.h) * p.chunks_per_page + in_page;
+                copy4(s_scales + tid, p.scales + (blk & ~1ll));
+                info = (uint32_t)min(kChunk, c.len - k * kChunk) | (uint32_t)(blk & 1) << 31;
             }
         }
-        if (!c.last) {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int k = c.k + c.cnt + (r0 + ROWS * i) / kChunk;
-                pages[i] = k < c.nch ? page_of(c, k) : -1;
-            }
-        }
+        turn ^= 1;
+        if (!c.last && tid < kBlockChunks && c.k + c.cnt + tid < c.nch)
+            copy4(s_pages + turn * kBlockChunks + tid, page_of(c, c.k + c.cnt + tid));
     };
     auto fetch_v = [&](const Block& c) { load_side(c, v_pool, vr); };
     // 16 converted bytes into the tile at `off`: pieces 2 q, 2 q + 1 of a row (the
@@ -366,9 +389,11 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) put(Lay::kOffK, r0 + ROWS * i, kr[i]);
         if (tid < kBlockChunks) {
-            const int e = kv8_clamp_exp((int)((info >> 8) & 0xffu) - 127);
-            s_chunk[tid] = {__uint_as_float((info & 0xffu) << 23), (float)e, exp2i(-e),
-                            (int)(info >> 16)};
+            asm volatile("cp.async.wait_all;" ::: "memory");  // its scales, the page ids after
+            const uint32_t sc = s_scales[tid] >> (info >> 31 ? 16 : 0);
+            const int e = kv8_clamp_exp((int)((sc >> 8) & 0xffu) - 127);
+            s_chunk[tid] = {__uint_as_float((sc & 0xffu) << 23), (float)e, exp2i(-e),
+                            (int)(info & 0xffffu)};
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -403,17 +428,17 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         ph ^= 1u;
         tc_fence_after();
 
-        // ---- softmax: this thread's half of row `row`, columns 64 half ..
+        // ---- softmax: this thread's part of row `row`
         // (twice out of tensor memory, for the maximum and for the weights, a chunk at
         // a time: beside the next block's bytes there are no registers for more, and
         // what the compiler moves to local memory instead does not stay in the little
         // L1 that the shared memory leaves)
         float mx = -INFINITY;
-        const bool have = half * 64 < ntok;
+        const bool have = part * kPartChunks < cur.cnt;
         if (!fail && have) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int ch = half * 4 + c;
+            for (int c = 0; c < kPartChunks; ++c) {
+                const int ch = part * kPartChunks + c;
                 if (ch >= cur.cnt) break;
                 uint32_t v[16];
                 tmem_ld(lane_base + ch * kChunk, v);
@@ -432,10 +457,11 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
                 if (see > 0) mx = fmaxf(mx, fmaf(top, fs * ci.x, ci.y));
             }
         }
-        s_max[half * 128 + row] = mx;
-        // the two warps that share these 32 rows
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-        mx = fmaxf(mx, s_max[(half ^ 1) * 128 + row]);
+        s_max[part * 128 + row] = mx;
+        // the warps that share these 32 rows
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(kParts * 32) : "memory");
+#pragma unroll
+        for (int x = 0; x < kParts; ++x) mx = fmaxf(mx, s_max[x * 128 + row]);
         float alpha = 1.f;
         if (mx > m_run + kSlack) {
             mr = mx;  // finite, or +inf (then NaN, as it should be)
@@ -446,8 +472,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         // the products S = Q K^T of the block are done: K's place takes P
         if (have) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int ch = half * 4 + c;
+            for (int c = 0; c < kPartChunks; ++c) {
+                const int ch = part * kPartChunks + c;
                 if (ch >= cur.cnt) break;
                 uint32_t v[16];
                 float y[16];
@@ -470,18 +496,18 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const float* w = y + 8 * q;
-                    *reinterpret_cast<uint4*>(base + Lay::kOffK + half * Lay::kColBytes +
-                                              swz(row, 2 * c + q)) =
+                    *reinterpret_cast<uint4*>(base + Lay::kOffK + (ch >> 2) * Lay::kColBytes +
+                                              swz(row, 2 * (ch & 3) + q)) =
                         make_uint4(Cvt<__half>::pack2(w[0], w[1]), Cvt<__half>::pack2(w[2], w[3]),
                                    Cvt<__half>::pack2(w[4], w[5]), Cvt<__half>::pack2(w[6], w[7]));
                 }
             }
         }
-        // the earlier blocks' O to the new reference: half of the columns a thread
+        // the earlier blocks' O to the new reference: its part of the columns a thread
         if (!cur.first && __any_sync(kFull, alpha != 1.f)) {
 #pragma unroll
-            for (int x = 0; x < D / 2; x += 16) {
-                const uint32_t at = lane_base + Lay::kColsS + half * (D / 2) + x;
+            for (int x = 0; x < D / kParts; x += 16) {
+                const uint32_t at = lane_base + Lay::kColsS + part * (D / kParts) + x;
                 uint32_t v[16];
                 tmem_ld(at, v);
 #pragma unroll
@@ -523,15 +549,17 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) put(Lay::kOffV, r0 + ROWS * i, nan_ones(vr[i]));
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 2 * kPartChunks; ++q) {
                 uint32_t w[4];
+                const int piece = part * 2 * kPartChunks + q;  // 8 tokens
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = half * 64 + 8 * q + 2 * e;
+                    const int t = 8 * piece + 2 * e;
                     w[e] = (t <= lim ? 0x3c00u : 0u) | (t + 1 <= lim ? 0x3c000000u : 0u);
                 }
-                *reinterpret_cast<uint4*>(base + Lay::kOffK + half * Lay::kColBytes +
-                                          swz(row, q)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(base + Lay::kOffK + (piece >> 3) * Lay::kColBytes +
+                                          swz(row, piece & 7)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -542,14 +570,14 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
             tc_fence_after();
             if (__syncthreads_or(fail)) break;
 #pragma unroll 1
-            for (int x = 0; x < D / 2; x += 8) {
+            for (int x = 0; x < D / kParts; x += 8) {
                 uint32_t n[8], v[8];
-                tmem_ld(lane_base + half * (D / 2) + x, n);
-                tmem_ld(lane_base + Lay::kColsS + half * (D / 2) + x, v);
+                tmem_ld(lane_base + part * (D / kParts) + x, n);
+                tmem_ld(lane_base + Lay::kColsS + part * (D / kParts) + x, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (__uint_as_float(n[e]) > 0.f) v[e] = 0x7fc00000u;
-                tmem_st(lane_base + Lay::kColsS + half * (D / 2) + x, v);
+                tmem_st(lane_base + Lay::kColsS + part * (D / kParts) + x, v);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -558,19 +586,21 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         }
         in_flight = false;
 
-        // ---- the segment's end: half a row a thread
+        // ---- the segment's end
         if (cur.last) {
-            s_max[half * 128 + row] = l_run;
+            s_max[part * 128 + row] = l_run;
             if (__syncthreads_or(fail)) break;
-            const float l = l_run + s_max[(half ^ 1) * 128 + row];
+            float l = 0.f;
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) l += s_max[x * 128 + row];
             const Unit un(p, cur.u);
             const int rows = p.rows.rows(un.sg);
             const bool whole = cur.head && cur.k + cur.cnt == cur.nch;
             const float inv = l == 0.f ? 0.f : 1.0f / l;  // no token seen: zeros
             float* slot = p.partials + (long long)(cur.u + cta) * partial_slot_floats(p.gs, D);
 #pragma unroll
-            for (int x = 0; x < D / 2; x += 16) {
-                const int c0 = half * (D / 2) + x;
+            for (int x = 0; x < D / kParts; x += 16) {
+                const int c0 = part * (D / kParts) + x;
                 uint32_t v[16];
                 tmem_ld(lane_base + Lay::kColsS + c0, v);
                 if (row < rows) {
@@ -595,7 +625,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
                     }
                 }
             }
-            if (!whole && row < rows && half == 0) {
+            if (!whole && row < rows && part == 0) {
                 slot[p.gs * D + row] = m_run;
                 slot[p.gs * D + p.gs + row] = l;
             }

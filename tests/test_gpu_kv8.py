@@ -333,6 +333,10 @@ SHAPES = [  # lens, Hq, Hkv, D, P
     ([1000], 33, 1, 128, 16),       # a group cut into threes of eleven
     ([900, 1200, 40], 28, 4, 128, 32),
     ([50, 2000], 9, 3, 64, 128),
+    ([2500, 2490], 512, 16, 64, 16),  # few units, many rows
+    ([700], 64, 1, 128, 16),          # a group that fills half a tensor-core tile
+    ([90, 1500, 0, 17], 96, 1, 64, 32),
+    ([640, 33], 260, 2, 128, 48),     # 130 rows a KV head: two tiles
 ]
 
 
@@ -347,16 +351,50 @@ def test_decode(dtype, workers, lens, Hq, Hkv, D, P):
     assert (out[c.lens_g == 0] == 0).all()
 
 
+@pytest.mark.parametrize("Hq", [6, 20, 70])
 @pytest.mark.parametrize("dtype", DT)
-def test_decode_scales_apart(dtype):
+def test_decode_scales_apart(dtype, Hq):
     """V scales from one end of their range to the other in one sequence: fp16
     outputs need the values small, so the large ones go with small weights."""
     c = Cache(8, [400, 200], 1, 128, 16)
     c.scales[..., 1] = c.rng.integers(127 - 60, 127 + 41 if dtype == torch.bfloat16 else 127 + 4,
                                       c.scales[..., 1].shape)
     c.gpu()
-    q = torch.randn(2, 6, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    q = torch.randn(2, Hq, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
     check(c, q[:, None], decode(c, q, 0.1)[:, None], 0.1)
+
+
+@pytest.mark.parametrize("Hq", [3, 70])
+def test_decode_negative_and_zero_scale(Hq):
+    c = Cache(23, [300, 33], 1, 128, 16).gpu()
+    for dtype in DT:
+        q = torch.randn(2, Hq, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+        for scale in (-0.09, 0.0):
+            check(c, q[:, None], decode(c, q, scale)[:, None], scale)
+
+
+def test_decode_large_batches():
+    """More sequences than a CTA plans for itself (the plan kernel's path), with
+    empty ones, padded lengths and a bad length among them."""
+    B = 700
+    lens = np.random.default_rng(5).integers(0, 70, B)
+    lens[::9] = 0
+    c = Cache(24, lens, 2, 64, 16).poison().gpu()
+    for Hq in (6, 140):
+        q = torch.randn(B, Hq, 64, generator=torch.Generator().manual_seed(4)).half().cuda()
+        out = decode(c, q, 0.125)
+        sel = np.r_[0:40, B - 20:B]
+        sub = Cache.__new__(Cache)
+        sub.__dict__.update(c.__dict__)
+        sub.table, sub.lens = c.table[sel], c.lens[sel]
+        check(sub, q[sel][:, None], out[sel][:, None], 0.125)
+        bad = c.lens_g.clone()
+        bad[3] = -5
+        ws = pkv.alloc_kv8_workspace(B, Hq, 2, 64)
+        two = torch.empty_like(out)
+        pkv.paged_decode_attention_kv8(q, c.k_g, c.v_g, c.s_g, c.table_g, bad, 0.125, two, ws)
+        assert pkv.pkv_read_device_status(ws) == pkv.DEV_BAD_LEN
+        assert (two[3] == 0).all()
 
 
 def test_decode_queries_of_any_size():
@@ -406,6 +444,9 @@ def test_decode_nan_where_seen_only():
     (64, [64, 500, 10], 8, 2, 128, 16),
     (64, [128, 70], 3, 1, 64, 256),
     (3, [90, 1000], 32, 1, 128, 16),
+    (40, [41, 700, 2, 0, 129], 4, 2, 128, 16),   # 80 rows a KV head
+    (64, [2000, 1], 5, 1, 64, 64),               # 320 rows: three tiles
+    (17, [400, 18], 24, 3, 128, 48),             # 136 rows
 ])
 def test_multi(dtype, workers, Q, lens, Hq, Hkv, D, P):
     c = Cache(11, lens, Hkv, D, P).poison().gpu()
@@ -422,41 +463,51 @@ def test_multi(dtype, workers, Q, lens, Hq, Hkv, D, P):
         assert torch.equal(out[:, 0], decode(c, q[:, 0].contiguous(), D ** -0.5, workers))
 
 
-def test_multi_nan_in_a_later_token():
-    """A NaN in the value of token 20 reaches only the queries from token 20 on,
-    also through weights that vanish."""
-    Q, n = 12, 30  # queries stand at tokens 18 .. 29
-    c = Cache(12, [n], 1, 128, 16).poison()
-    c.v[c.table[0, 1], 0, 4, 5] = 0x7F
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,n", [(4, 30), (4, 200), (8, 30), (8, 150), (8, 1000)])
+def test_multi_nan_in_a_later_token(Hq, n, D):
+    """A NaN in the value of one of the queries' own tokens reaches only the
+    queries from there on, also through weights that vanish; one far before
+    them reaches all (48 rows: the warp kernel; 96: the tensor-core tile)."""
+    Q = 12  # queries stand at the last 12 tokens
+    at = n - 10
+    c = Cache(12, [n, n], 1, D, 16).poison()
+    c.v[c.table[0, at // 16], 0, at % 16, 5] = 0x7F
+    c.v[c.table[1, 0], 0, 7, D - 1] = 0xFF
     c.gpu()
-    q = torch.randn(1, Q, 4, 128).half().cuda()
-    out = torch.empty_like(q)
-    ws = pkv.alloc_kv8_workspace(1, 4, 1, 128, n_queries=Q)
-    pkv.paged_decode_attention_multi_kv8(q, c.k_g, c.v_g, c.s_g, c.table_g, c.lens_g, 0.09, out, ws)
-    want = torch.zeros_like(out, dtype=torch.bool)
-    want[0, 2:, :, 5] = True
-    assert torch.equal(out.isnan(), want)
+    q = torch.randn(2, Q, Hq, D).half().cuda()
+    for workers in (0, 1):
+        out = torch.empty_like(q)
+        ws = pkv.alloc_kv8_workspace(2, Hq, 1, D, n_queries=Q, num_workers=workers)
+        pkv.paged_decode_attention_multi_kv8(q, c.k_g, c.v_g, c.s_g, c.table_g, c.lens_g, 0.09,
+                                             out, ws, num_workers=workers)
+        want = torch.zeros_like(out, dtype=torch.bool)
+        want[0, 2:, :, 5] = True
+        want[1, :, :, D - 1] = True
+        assert torch.equal(out.isnan(), want)
 
 
-def test_attention_bad_inputs():
+@pytest.mark.parametrize("Hq", [8, 140])
+def test_attention_bad_inputs(Hq):
     """Bad page ids and lengths are flagged; the other sequences are unharmed."""
     c = Cache(13, [100, 90, 60], 2, 128, 16).gpu()
-    q = torch.randn(3, 8, 128).bfloat16().cuda()
+    q = torch.randn(3, Hq, 128).bfloat16().cuda()
     good = decode(c, q, 0.09)
     c.table_g[1, 2] = c.NP + 5
     lens = c.lens_g.clone()
     lens[2] = 1000  # beyond the table row: clamped to it, whose last entries are -1
     out = torch.empty_like(q)
-    ws = pkv.alloc_kv8_workspace(3, 8, 2, 128)
+    ws = pkv.alloc_kv8_workspace(3, Hq, 2, 128)
     pkv.paged_decode_attention_kv8(q, c.k_g, c.v_g, c.s_g, c.table_g, lens, 0.09, out, ws)
     assert pkv.pkv_read_device_status(ws) == pkv.DEV_BAD_PAGE | pkv.DEV_BAD_LEN
     assert (out[0] - good[0]).abs().max() < 0.02 * good[0].abs().max()
     assert out.isfinite().all()
 
 
-def test_page_ids_and_reruns_do_not_matter():
+@pytest.mark.parametrize("Hq", [8, 140])
+def test_page_ids_and_reruns_do_not_matter(Hq):
     c = Cache(14, [700, 30, 260], 2, 128, 32).gpu()
-    q = torch.randn(3, 8, 128).half().cuda()
+    q = torch.randn(3, Hq, 128).half().cuda()
     a, b = decode(c, q, 0.09), decode(c, q, 0.09)
     assert torch.equal(a, b)
     perm = torch.from_numpy(c.rng.permutation(c.NP)).cuda()
