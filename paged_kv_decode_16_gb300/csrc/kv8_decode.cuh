@@ -26,8 +26,10 @@
 // be half empty the other way round.  e4m3 is exact in fp16, so the cache
 // enters without rounding.  bf16 queries are scaled by a power of two per row
 // (largest element in [2^14, 2^15)) and are exact in fp16 down to 2^-31 of the
-// row's largest element.  P is rounded to fp16 (11 bits, relative error at most
-// 2^-11 a weight), as in the 16-bit kernel.
+// row's largest element.  P is rounded to fp16 (11 bits), which is far below a bf16
+// output's 8; for fp16 outputs what the rounding left enters in a second product
+// (the error against 64 bits, 256 uneven sequences: 2.7e-4 of the norm without it,
+// 2.1e-4 with it, which is the output's own rounding).
 //
 // The order of k in a product is free as long as both operands agree.  For
 // S^T lane (j = lane / 4, t = lane % 4) takes D/4 consecutive elements of token
@@ -183,6 +185,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
     constexpr int MT = D / 16;      // m16 tiles of O^T
     constexpr int DPL = D / 8;      // V elements a lane takes of a row
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kSplitP = !kBf16;  // P in two fp16 pieces
     // a row's scores may pass m by this much (in binary orders) before m moves:
     // p stays below 2^8, far inside fp16, and after a range's first chunk the
     // accumulators are hardly ever rescaled
@@ -533,6 +536,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
             }
             {
                 uint32_t pb[NT][2];  // B fragments of P^T: tokens 2t, 2t+1 (+ 8) of row j
+                uint32_t pl[NT][2];  // fp16 outputs: what P's rounding left
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float p0 = fast_exp2(s[n][0] - mr[n][0]);
@@ -541,8 +545,16 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                     const float p3 = fast_exp2(s[n][3] - mr[n][1]);
                     l[n][0] = fmaf(p0 + p2, inv_v, l[n][0]);
                     l[n][1] = fmaf(p1 + p3, inv_v, l[n][1]);
-                    pb[n][0] = transpose8x8(Cvt<__half>::pack2(p0, p1));
-                    pb[n][1] = transpose8x8(Cvt<__half>::pack2(p2, p3));
+                    const uint32_t h0 = Cvt<__half>::pack2(p0, p1);
+                    const uint32_t h1 = Cvt<__half>::pack2(p2, p3);
+                    pb[n][0] = transpose8x8(h0);
+                    pb[n][1] = transpose8x8(h1);
+                    if constexpr (kSplitP) {
+                        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                        pl[n][0] = transpose8x8(Cvt<__half>::pack2(p0 - f0.x, p1 - f0.y));
+                        pl[n][1] = transpose8x8(Cvt<__half>::pack2(p2 - f1.x, p3 - f1.y));
+                    }
                 }
                 // ---- O^T += V^T P^T ----
                 uint32_t vw[4][DPL / 4];  // tokens 2t, 2t+1, 2t+8, 2t+9: elements DPL j ..
@@ -622,6 +634,11 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                        if constexpr (kSplitP) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                        }
                     }
                 }
             }
