@@ -1600,6 +1600,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.rows = s.rs;
     p.gs = s.gs;
     p.self_plan = c.batch <= pkv::kKv8SelfPlan;
+    p.after_append = append_flags;
     p.unit_cost = !p.self_plan ? 0 : s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
     p.merge = s.units * s.gs <= pkv::kKv8RowCtas ? warps : 1;
     p.workers_req = c.num_workers;

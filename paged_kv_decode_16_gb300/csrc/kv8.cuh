@@ -129,6 +129,7 @@ struct Kv8DecodeParams {
     RowShape rows;
     int gs;                 // rows of a full unit (the partial states' layout)
     int self_plan;
+    int after_append;       // the kernel before it is the step's append (see kv8_decode.cuh)
     int unit_cost;          // positions a unit has beside its chunks
     int merge;              // workers whose parts of a unit may be merged by their CTA
     int workers_req, workers_auto;

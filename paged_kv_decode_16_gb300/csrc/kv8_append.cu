@@ -546,6 +546,7 @@ kv8_append_single_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* stat
     const int jl = lane % HV, grp = tid / HV;
     const int tok = blockIdx.x;
     pdl_wait();
+    pdl_trigger();  // a step's decode works out its ranges beside this
     const int pos = a.positions[tok];
     const int nq = a.q ? a.n_q_heads : 0, rows = nq + 2 * a.n_kv_heads;
     // row r: q heads, then K heads, then V heads
@@ -684,7 +685,6 @@ kv8_append_single_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* stat
             }
         }
     }
-    pdl_trigger();
 }
 
 }  // namespace

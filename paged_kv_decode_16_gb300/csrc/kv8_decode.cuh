@@ -226,7 +226,13 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                      : "memory");
     }
     __syncwarp();
-    pdl_wait();
+    // After a step's append the ranges are worked out beside it: that kernel lets
+    // this one start only after its own wait, so every kernel before it is
+    // complete, and it writes neither the lengths nor the ranges' place in the
+    // workspace.  (The rows, scales and rotated queries it does write: below the
+    // wait.)
+    const bool early = p.after_append && p.self_plan;
+    if (!early) pdl_wait();
 
     const int gw = blockIdx.x * WARPS + warp;
     Kv8Stream ws;
@@ -252,6 +258,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         sw = p.hdr->chunks_per_worker;
         r = p.hdr->extra_chunks;
     }
+    if (early) pdl_wait();
     const int merge_warps = kv8_merge_warps(p.units, nw, p.merge);
     ws.f0 = range_begin(gw, sw, r);
     ws.n = gw < nw ? sw + (gw < r ? 1 : 0) : 0;

@@ -158,7 +158,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    pdl_wait();
+    const bool early = p.after_append && p.self_plan;  // as in kv8_decode.cuh
+    if (!early) pdl_wait();
 
     uint32_t flags = 0;
     const int32_t* prefix;
@@ -178,6 +179,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         sw = p.hdr->chunks_per_worker;
         rr = p.hdr->extra_chunks;
     }
+    if (early) pdl_wait();
     const int cta = blockIdx.x;
     const int f0 = range_begin(cta, sw, rr);
     const int f_end = cta < nw ? f0 + sw + (cta < rr ? 1 : 0) : f0;
