@@ -845,14 +845,16 @@ def _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status
     """(current device, tokens, dtype code) of an append's checked arguments."""
     if pool.dtype is not _E4M3:
         raise ValueError("pool must be an 8-bit pool (kv8_pool_create)")
-    dev = _get_device()
+    dev = -1
     try:
-        ok = (k_new.get_device() == dev and v_new.get_device() == dev
+        dev = k_new.get_device()
+        ok = (dev >= 0 and v_new.get_device() == dev
               and page_table.get_device() == dev and positions.get_device() == dev
               and v_new.dtype is k_new.dtype and page_table.dtype is _I32
               and positions.dtype is _I32 and k_new.dim() == 3 and page_table.dim() == 2
               and positions.dim() == 1 and k_new.is_contiguous() and v_new.is_contiguous()
-              and page_table.is_contiguous() and positions.is_contiguous())
+              and page_table.is_contiguous() and positions.is_contiguous()
+              and dev == _get_device())
     except AttributeError:
         ok = False
     if not ok:
@@ -914,8 +916,8 @@ def kv8_append_rope(pool: Pool, q: torch.Tensor, k_new: torch.Tensor, v_new: tor
     rows, cols = page_table.shape
     _check(load_library().kv8_append_rope(
         pool.handle, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), dt, page_table.data_ptr(),
-        cols, rows, positions.data_ptr(), _ptr(seq_ids), N, Hq, rope_theta, _ptr(q_norm_weight),
-        _ptr(k_norm_weight), norm_eps, q_out.data_ptr(), _ptr(dev_status),
+        cols, rows, positions.data_ptr(), _ptr(seq_ids), N, Hq, float(rope_theta), _ptr(q_norm_weight),
+        _ptr(k_norm_weight), float(norm_eps), q_out.data_ptr(), _ptr(dev_status),
         _current(stream, dev)), "kv8_append_rope")
     return q_out
 
@@ -939,9 +941,10 @@ def alloc_kv8_workspace(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: i
 
 def _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out, workspace, ndim):
     """(current device, Hkv, D, P, NP, dtype code) of an attention call's checked arguments."""
-    dev = _get_device()
+    dev = -1
     try:
-        ok = (q.get_device() == dev and out.get_device() == dev and k_pool.get_device() == dev
+        dev = q.get_device()
+        ok = (dev >= 0 and out.get_device() == dev and k_pool.get_device() == dev
               and v_pool.get_device() == dev and scales.get_device() == dev
               and page_table.get_device() == dev and context_lens.get_device() == dev
               and workspace.get_device() == dev and out.dtype is q.dtype
@@ -951,7 +954,8 @@ def _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out, workspac
               and page_table.dim() == 2 and context_lens.dim() == 1 and q.is_contiguous()
               and out.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
               and scales.is_contiguous() and page_table.is_contiguous()
-              and context_lens.is_contiguous() and workspace.is_contiguous())
+              and context_lens.is_contiguous() and workspace.is_contiguous()
+              and dev == _get_device())
     except AttributeError:
         ok = False
     if not ok:
@@ -986,8 +990,8 @@ def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: to
     _check(load_library().paged_decode_attention_kv8(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
         page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP,
-        dt, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(), num_workers,
-        _current(stream, dev)), "paged_decode_attention_kv8")
+        dt, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        int(num_workers), _current(stream, dev)), "paged_decode_attention_kv8")
     return out
 
 
@@ -1004,8 +1008,8 @@ def paged_decode_attention_multi_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_po
     _check(load_library().paged_decode_attention_multi_kv8(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
         page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Qn, Hq, Hkv, D, P,
-        NP, dt, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(), num_workers,
-        _current(stream, dev)), "paged_decode_attention_multi_kv8")
+        NP, dt, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        int(num_workers), _current(stream, dev)), "paged_decode_attention_multi_kv8")
     return out
 
 
@@ -1040,9 +1044,10 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
     _check(load_library().paged_decode_step_kv8(
         k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), q.data_ptr(),
         k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(),
-        page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP, dt, scale, rope_theta,
-        _ptr(q_norm_weight), _ptr(k_norm_weight), norm_eps, out.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), num_workers, _current(stream, dev)), "paged_decode_step_kv8")
+        page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP, dt, float(scale),
+        float(rope_theta), _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps),
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(), int(num_workers),
+        _current(stream, dev)), "paged_decode_step_kv8")
     return out
 
 

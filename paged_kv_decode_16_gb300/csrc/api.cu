@@ -1601,7 +1601,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.gs = s.gs;
     p.self_plan = c.batch <= pkv::kKv8SelfPlan;
     p.after_append = append_flags;
-    p.unit_cost = !p.self_plan ? 0 : s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
+    p.unit_cost = s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
     p.merge = s.units * s.gs <= pkv::kKv8RowCtas ? warps : 1;
     p.workers_req = c.num_workers;
     p.workers_auto = s.workers_auto;
@@ -1617,9 +1617,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.cap = (long long)c.table_stride * c.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     pkv_status st = PKV_OK;
-    if (!p.self_plan)
-        st = do_plan(c.lens, nullptr, c.batch, c.page_size, c.table_stride, c.num_workers,
-                     c.workspace, s, nullptr, stream);
+    if (!p.self_plan) st = cuda_status(pkv::launch_kv8_plan(p, stream));
     if (st != PKV_OK) return st;
     if (s.kernel.q8.umma) {
         st = cuda_status(pkv::launch_pdl(s.kernel.q8.umma, dim3(ctas), dim3(s.kernel.threads()),

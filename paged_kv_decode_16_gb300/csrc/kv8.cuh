@@ -159,6 +159,9 @@ Kv8DecodeInfo kv8_decode_info_f16(int head_dim, int rows);
 constexpr int kKv8UmmaRows = 128;
 Kv8DecodeInfo kv8_umma_info(bool bf16, int head_dim);
 
+// The ranges of a batch of more than kKv8SelfPlan sequences.
+cudaError_t launch_kv8_plan(const Kv8DecodeParams& p, cudaStream_t stream);
+
 // Merges the units that several workers share, and sets the workspace's status
 // to the OR of n_flags words (and of the plan kernel's, when it ran).
 struct Kv8CombineArgs {

@@ -1,4 +1,5 @@
-// kv8_combine.cu -- merging the partial states of the 8-bit cache's decode.
+// kv8_combine.cu -- merging the partial states of the 8-bit cache's decode, and the
+// plan of batches too large for every CTA to work out its own.
 //
 // A warp per row of a unit; when units are few beside the decode's CTAs (their
 // rows have many segments then), a CTA per row, whose warps take every eighth
@@ -142,7 +143,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     const int nw = a.hdr->num_workers, sw = a.hdr->chunks_per_worker, r = a.hdr->extra_chunks;
     if (g >= a.rows.rows(sg)) return;
     const int per_unit = (next - first) / a.units_per_b;
-    if (per_unit == 0) return;  // no tokens: the decode kernel wrote zeros
+    if (per_unit == 0 || nw <= 0) return;  // no tokens: the decode kernel wrote zeros
     const int at = first + uidx * per_unit;
     const Segs segs = kv8_segments(sw, r, u, at + a.unit_cost, at + per_unit - 1,
                                    kv8_merge_warps(a.units, nw, a.merge));
@@ -191,7 +192,66 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     }
 }
 
+// kv8_plan.cuh's ranges by one CTA, for any batch.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+kv8_plan_kernel(const __grid_constant__ Kv8DecodeParams p) {
+    __shared__ long long s_tot[kPlanThreads / 32];
+    __shared__ uint32_t s_bits;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_bits = 0;
+    pdl_wait();
+    long long running = 0;
+    uint32_t bits = 0;
+    for (int base = 0; base < p.batch; base += kPlanThreads) {
+        const int b = base + tid;
+        long long len = b < p.batch ? p.lens[b] : 0;
+        if (len < 0 || len > p.cap) {
+            bits |= PKV_DEV_BAD_LEN;
+            len = len < 0 ? 0 : p.cap;
+        }
+        const long long nch = (len + kChunk - 1) / kChunk;
+        const long long c = nch ? (nch + p.unit_cost) * p.units_per_b : 0;
+        long long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_tot[warp] = incl;
+        __syncthreads();
+        long long before = running;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) before += s_tot[w];
+            running += s_tot[w];
+        }
+        if (b < p.batch) p.prefix[b] = (int)(before + incl - c);
+        __syncthreads();
+    }
+    if (running > 0x7fffffffLL) {  // beyond the 32-bit positions: refuse the work
+        bits |= PKV_DEV_BAD_LEN;
+        running = 0;
+    }
+    bits = __reduce_or_sync(kFull, bits);
+    if (lane == 0 && bits) atomicOr(&s_bits, bits);
+    __syncthreads();
+    if (tid == 0) {
+        int nw, sw, r;
+        kv8_ranges((int)running, p.workers_req, p.workers_auto, &nw, &sw, &r);
+        p.prefix[p.batch] = (int)running;
+        p.hdr->num_workers = nw;
+        p.hdr->chunks_per_worker = sw;
+        p.hdr->extra_chunks = r;
+        p.hdr->status = s_bits;
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_kv8_plan(const Kv8DecodeParams& p, cudaStream_t stream) {
+    return launch_pdl(kv8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+}
 
 cudaError_t launch_kv8_combine(bool bf16, int head_dim, const Kv8CombineArgs& a, int workers,
                                cudaStream_t stream) {

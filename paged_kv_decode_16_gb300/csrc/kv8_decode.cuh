@@ -175,8 +175,8 @@ struct Kv8Layout {
 };
 
 // NT tiles of 8 query rows; a unit has at most 8 NT rows.
-template <typename T, int D, int NT, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32)
+template <typename T, int D, int NT, int WARPS, int STAGES, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS)
 kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                   const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -212,7 +212,6 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
     };
     __shared__ Tail s_tail[WARPS];
     __shared__ float s_ml[WARPS][2 * 8 * NT];
-    static_assert(WARPS == kKv8Warps, "the combine kernel counts on it");
     static_assert(NT * 8 * D * 4 <= Lay::kWarpKV, "a segment's sums fit its ring");
 
     if (lane == 0) {
@@ -313,9 +312,10 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         fetch_q(0);
         ws.next(p, prefix);  // the second tile, behind the first copies
     }
-    // rows of sequences with no tokens are zeros: no worker visits them
+    // rows of sequences with no tokens are zeros: no worker visits them (nor, when
+    // the positions are too many and nothing is done, any)
     for (int b = gw; b < p.batch; b += gridDim.x * WARPS) {
-        if (prefix[b] != prefix[b + 1]) continue;
+        if (prefix[b] != prefix[b + 1] && nw > 0) continue;
         const long long vecs = (long long)p.rows.n_queries * p.rows.n_q_heads * D / 8;
         uint4* dst = reinterpret_cast<uint4*>(p.out) + b * vecs;
         for (long long x = lane; x < vecs; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -763,9 +763,14 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
 
 template <typename T, int D, int NT>
 Kv8DecodeInfo make_kv8_decode_info() {
-    constexpr int W = kKv8Warps, S = NT == 1 ? 2 : 4;
+    // Chunks on the way: one tile of rows, 12 warps of 2 stages (96 KiB an SM; 3
+    // stages took 93.1 us of 8 sequences of 32768 tokens, 4 took 97.0, 2 take 90.4:
+    // more copies in flight than the memory needs cost it order).  Larger units hold
+    // their accumulators in all the registers that 8 warps leave (3 CTAs of fewer
+    // registers, or 2 warps a CTA, spill: 69 us against 45 of 5 query tokens).
+    constexpr int W = kKv8Warps, S = NT == 1 ? 2 : NT == 3 ? 3 : 4, C = NT == 1 ? 3 : 2;
     Kv8DecodeInfo info;
-    info.fn = kv8_decode_kernel<T, D, NT, W, S>;
+    info.fn = kv8_decode_kernel<T, D, NT, W, S, C>;
     info.warps = W;
     info.threads = W * 32;
     info.smem_bytes = Kv8Layout<D, NT, S, W>::kBytes;

@@ -25,10 +25,9 @@ __device__ __forceinline__ int kv8_self_plan(const Kv8DecodeParams& p, int32_t* 
             len = len < 0 ? 0 : p.cap;
         }
         const int nch = (int)((len + kChunk - 1) / kChunk);
-        // a sequence of more positions than an int: over the limit in any case
         const long long c = nch ? (long long)(nch + p.unit_cost) * p.units_per_b : 0;
-        cnt[x] = (int)min(c, 0x7fffffffLL);
-        sum += cnt[x];
+        cnt[x] = (int)c;  // (beyond an int: so is the total, and nothing is done)
+        sum += c;
     }
     long long incl = sum;
 #pragma unroll

@@ -185,7 +185,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     const int f_end = cta < nw ? f0 + sw + (cta < rr ? 1 : 0) : f0;
     // rows of sequences with no tokens are zeros
     for (int b = cta; b < p.batch; b += gridDim.x) {
-        if (prefix[b] != prefix[b + 1]) continue;
+        if (prefix[b] != prefix[b + 1] && nw > 0) continue;
         const long long vecs = (long long)p.rows.n_queries * p.rows.n_q_heads * D / 8;
         uint4* dst = reinterpret_cast<uint4*>(p.out) + b * vecs;
         for (long long x = tid; x < vecs; x += kThreads) dst[x] = make_uint4(0u, 0u, 0u, 0u);

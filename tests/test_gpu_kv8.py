@@ -504,6 +504,24 @@ def test_attention_bad_inputs(Hq):
     assert out.isfinite().all()
 
 
+@pytest.mark.parametrize("B", [1, 300])
+@pytest.mark.parametrize("group", [1, 64])
+def test_more_positions_than_32_bits(B, group):
+    """A batch whose chunks over all heads do not fit 32 bits is refused on the
+    device: flagged, and zeros."""
+    Hkv, D, P, n = 4096 // group, 64, 16, 16 * (600000 if B == 1 else 2000) * group
+    k = torch.zeros((2, Hkv, P, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.full((2, Hkv, 1, 2), 127, dtype=torch.uint8, device="cuda").view(
+        torch.float8_e8m0fnu)
+    table = torch.zeros((B, n // P), dtype=torch.int32, device="cuda")
+    q = torch.randn(B, Hkv * group, D).half().cuda()
+    out = torch.full_like(q, float("nan"))
+    ws = pkv.alloc_kv8_workspace(B, Hkv * group, Hkv, D)
+    pkv.paged_decode_attention_kv8(q, k, k, s, table, i32([n] * B), 0.1, out, ws)
+    assert pkv.pkv_read_device_status(ws) == pkv.DEV_BAD_LEN
+    assert (out == 0).all()
+
+
 @pytest.mark.parametrize("Hq", [8, 140])
 def test_page_ids_and_reruns_do_not_matter(Hq):
     c = Cache(14, [700, 30, 260], 2, 128, 32).gpu()
