@@ -53,8 +53,7 @@ struct Layout {
     static constexpr int kOffEnd = kOffV + kCols * kColBytes;
     static constexpr int kOffMax = kOffEnd;                  // [parts][128] floats
     static constexpr int kOffChunk = kOffMax + kParts * 128 * 4;  // [8] ChunkInfo
-    static constexpr int kOffPages = kOffChunk + kBlockChunks * 16;  // [2][8] ids, [8] scales
-    static constexpr int kOffBar = kOffPages + 3 * kBlockChunks * 4;
+    static constexpr int kOffBar = kOffChunk + kBlockChunks * 16;
     static constexpr int kOffPlan = kOffBar + 32;
     static constexpr int kUsed = kOffPlan + (kKv8SelfPlan + 1) * 4 + 1024;
     // at least 80 KiB: no more CTAs on an SM than its tensor memory serves
@@ -130,7 +129,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kSlack = 8.f;  // as in kv8_decode.cuh
     constexpr int PPR = D / 16;    // 16-byte pieces of a token's e4m3 row
-    constexpr int ROWS = kThreads / PPR, LOADS = kBlockTok / ROWS;  // token rows a pass; passes
+    constexpr int RPP = 32 / PPR, LOADS = kChunk / RPP;  // token rows of a warp's pass; passes
+    static_assert(kThreads / 32 == kBlockChunks, "a warp a chunk");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
@@ -138,8 +138,6 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     const uint32_t sb = raw + pad;
     float* s_max = reinterpret_cast<float*>(base + Lay::kOffMax);
     ChunkInfo* s_chunk = reinterpret_cast<ChunkInfo*>(base + Lay::kOffChunk);
-    int32_t* s_pages = reinterpret_cast<int32_t*>(base + Lay::kOffPages);
-    uint32_t* s_scales = reinterpret_cast<uint32_t*>(s_pages + 2 * kBlockChunks);
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
     uint32_t* s_flags = tmem_slot + 1;
@@ -234,76 +232,50 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         return true;
     };
 
-    // This thread's part of a block's bytes: piece tid % PPR of token rows
-    // tid / PPR + ROWS i, K's and V's at different times (the L1 that the shared
-    // memory leaves holds the lines of about one side of two CTAs on the way; more
-    // loads wait for room).  Threads 0 .. 7 ask for the page ids of the block after
-    // the next one at the same time, and for the next one's scales, both into
-    // shared memory, so that no load waits for another one inside a segment.
+    // A warp brings one chunk of a block: lane (rr, pc) the pieces pc of token rows
+    // rr + RPP i, K's and V's at different times (the L1 that the shared memory
+    // leaves holds the lines of about one side of two CTAs on the way; more loads
+    // wait for room).  The page id of its chunk of the block after is asked for at
+    // the same time, so that no load waits for another one inside a segment.
+    const int lane = tid & 31, pc = lane % PPR, rr0 = lane / PPR;
     uint4 kr[LOADS], vr[LOADS];
-    int pg[LOADS];       // page ids of this thread's rows of the next block
-    uint32_t info = 0u;  // threads 0 .. 7: tokens of the chunk that count; bit 31: its scales
-                         // are the upper half of their word
-    int turn = 0;        // which half of s_pages has the next block's ids
-    const int pc = tid % PPR, r0 = tid / PPR;
+    int page_after = -1;  // page of this warp's chunk of the block after the next one
+    int nv = 0;           // tokens of its chunk of the next block that count (bad pages: 0)
+    uint32_t sc = 0u;     // the chunk's scale bytes
+    long long at = 0;     // this lane's first piece of it
     auto page_of = [&](const Block& c, int k) {
-        return p.table + (long long)c.b * p.table_stride + kv8_page_col(k, p.page_magic);
+        return __ldg(p.table + (long long)c.b * p.table_stride + kv8_page_col(k, p.page_magic));
     };
-    auto copy4 = [&](const void* dst, const void* src) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
-                     : "memory");
-    };
-    auto load_side = [&](const Block& c, const uint8_t* pool, uint4 (&v)[LOADS]) {
+    auto load_side = [&](const uint8_t* pool, uint4 (&v)[LOADS]) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int r = r0 + ROWS * i, k = c.k + r / kChunk;
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            // rows behind the sequence's end: zeros
-            if (pg[i] >= 0 && pg[i] < p.num_pages && r % kChunk < c.len - k * kChunk) {
-                const int in_page = k - kv8_page_col(k, p.page_magic) * p.chunks_per_page;
-                const long long at =
-                    (((long long)(pg[i] * p.n_kv_heads + c.h) * p.chunks_per_page + in_page) *
-                         kChunk + r % kChunk) * D + pc * 16;
-                v[i] = __ldg(reinterpret_cast<const uint4*>(pool + at));
-            }
+            v[i] = make_uint4(0u, 0u, 0u, 0u);  // rows behind the sequence's end
+            if (rr0 + RPP * i < nv)
+                v[i] = __ldg(reinterpret_cast<const uint4*>(pool + at + i * (RPP * D)));
         }
     };
     auto fetch_k = [&](const Block& c) {
-        if (c.first) {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int ch = (r0 + ROWS * i) / kChunk;
-                pg[i] = ch < c.cnt ? __ldg(page_of(c, c.k + ch)) : -1;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int ch = (r0 + ROWS * i) / kChunk;
-                pg[i] = ch < c.cnt ? s_pages[turn * kBlockChunks + ch] : -1;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            if ((r0 + ROWS * i) / kChunk < c.cnt && (pg[i] < 0 || pg[i] >= p.num_pages))
-                flags |= PKV_DEV_BAD_PAGE;
-        load_side(c, k_pool, kr);
-        info = 0u;
-        if (tid < c.cnt) {
-            const int k = c.k + tid;
-            const int page = c.first ? __ldg(page_of(c, k)) : s_pages[turn * kBlockChunks + tid];
+        const int k = c.k + warp;
+        int page = page_after;
+        if (c.first && warp < c.cnt) page = page_of(c, k);
+        nv = 0;
+        sc = 0u;
+        if (warp < c.cnt) {
             if (page >= 0 && page < p.num_pages) {
-                const int in_page = k - kv8_page_col(k, p.page_magic) * p.chunks_per_page;
+                nv = min(kChunk, c.len - k * kChunk);
                 const long long blk =
-                    (long long)(page * p.n_kv_heads + c.h) * p.chunks_per_page + in_page;
-                copy4(s_scales + tid, p.scales + (blk & ~1ll));
-                info = (uint32_t)min(kChunk, c.len - k * kChunk) | (uint32_t)(blk & 1) << 31;
+                    (long long)(page * p.n_kv_heads + c.h) * p.chunks_per_page +
+                    (k - kv8_page_col(k, p.page_magic) * p.chunks_per_page);
+                at = blk * (kChunk * D) + rr0 * D + pc * 16;
+                sc = (uint32_t)__ldg(p.scales + blk);
+            } else {
+                flags |= PKV_DEV_BAD_PAGE;
             }
         }
-        turn ^= 1;
-        if (!c.last && tid < kBlockChunks && c.k + c.cnt + tid < c.nch)
-            copy4(s_pages + turn * kBlockChunks + tid, page_of(c, c.k + c.cnt + tid));
+        load_side(k_pool, kr);
+        if (!c.last && k + c.cnt < c.nch) page_after = page_of(c, k + c.cnt);
     };
-    auto fetch_v = [&](const Block& c) { load_side(c, v_pool, vr); };
+    auto fetch_v = [&]() { load_side(v_pool, vr); };
     // 16 converted bytes into the tile at `off`: pieces 2 q, 2 q + 1 of a row (the
     // upper column block's in the other order, so that a row's stores hit
     // different banks)
@@ -325,7 +297,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     bool more = advance();
     if (more) {
         fetch_k(nx);
-        fetch_v(nx);
+        fetch_v();
     }
     while (more) {
         cur = nx;
@@ -337,7 +309,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
             // a row, a 16-byte vector each
             constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row; rows of a warp side by side
             constexpr int PASSES = kRows / (kThreads / 32) / RPW;
-            const int lane = tid & 31, qp = lane % LPR;
+            const int qp = lane % LPR;
             const int rows = p.rows.rows(un.sg);
             uint4 q[PASSES];
 #pragma unroll
@@ -389,13 +361,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
 
         // ---- S = Q K^T of the converted K
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) put(Lay::kOffK, r0 + ROWS * i, kr[i]);
-        if (tid < kBlockChunks) {
-            asm volatile("cp.async.wait_all;" ::: "memory");  // its scales, the page ids after
-            const uint32_t sc = s_scales[tid] >> (info >> 31 ? 16 : 0);
-            const int e = kv8_clamp_exp((int)((sc >> 8) & 0xffu) - 127);
-            s_chunk[tid] = {__uint_as_float((sc & 0xffu) << 23), (float)e, exp2i(-e),
-                            (int)(info & 0xffffu)};
+        for (int i = 0; i < LOADS; ++i) put(Lay::kOffK, warp * kChunk + rr0 + RPP * i, kr[i]);
+        if (lane == 0) {
+            const int e = kv8_clamp_exp((int)(sc >> 8) - 127);
+            s_chunk[warp] = {__uint_as_float((sc & 0xffu) << 23), (float)e, exp2i(-e), nv};
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -422,7 +391,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
                 nan |= any_nan(v);
                 v = without_nan(v);
             }
-            put(Lay::kOffV, r0 + ROWS * i, v);
+            put(Lay::kOffV, warp * kChunk + rr0 + RPP * i, v);
         }
         more = advance();
         if (more) fetch_k(nx);  // comes behind the product and the softmax
@@ -526,7 +495,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         const int state = __syncthreads_or((fail ? 1 : 0) | (nan != 0u ? 2 : 0));
         const bool fix = masked && state && __syncthreads_or(nan != 0u);
         if (__builtin_expect(state != 0, 0) && __syncthreads_or(fail)) break;
-        if (more && !fix) fetch_v(nx);
+        if (more && !fix) fetch_v();
         // ---- O += P V
         auto product = [&](uint32_t d, bool keep) {
             tc_fence_after();
@@ -549,7 +518,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
             // in S's place
             if (__syncthreads_or(fail)) break;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) put(Lay::kOffV, r0 + ROWS * i, nan_ones(vr[i]));
+            for (int i = 0; i < LOADS; ++i) put(Lay::kOffV, warp * kChunk + rr0 + RPP * i, nan_ones(vr[i]));
 #pragma unroll
             for (int q = 0; q < 2 * kPartChunks; ++q) {
                 uint32_t w[4];
@@ -584,7 +553,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
             tmem_wait_st();
             tc_fence_before();
             __syncthreads();
-            if (more) fetch_v(nx);
+            if (more) fetch_v();
         }
         in_flight = false;
 
