@@ -783,7 +783,7 @@ def paged_decode_combine(out: torch.Tensor, n_kv_heads: int, workspace: torch.Te
 # expression of cheap tensor queries; only when it is false does _kv8_explain look
 # for what is wrong (and raises the usual error).
 _SCALE_DTYPES = (torch.float8_e8m0fnu, torch.uint8)
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _I32 = torch.int32
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -851,17 +851,18 @@ def _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status
         ok = (dev >= 0 and v_new.get_device() == dev
               and page_table.get_device() == dev and positions.get_device() == dev
               and v_new.dtype is k_new.dtype and page_table.dtype is _I32
-              and positions.dtype is _I32 and k_new.dim() == 3 and page_table.dim() == 2
-              and positions.dim() == 1 and k_new.is_contiguous() and v_new.is_contiguous()
+              and positions.dtype is _I32 and page_table.dim() == 2
+              and positions.dim() == 1 and k_new.dtype in _DT and k_new.is_contiguous() and v_new.is_contiguous()
               and page_table.is_contiguous() and positions.is_contiguous()
               and dev == _get_device())
     except AttributeError:
         ok = False
     if not ok:
         _dev(k_new, "k_new", None, 3)
+        _dtype_code(k_new)
         _kv8_explain((v_new, "v_new", k_new.dtype, 3), (page_table, "page_table", _I32, 2),
                      (positions, "positions", _I32, 1))
-    dt = _dtype_code(k_new)
+    dt = _DT[k_new.dtype]
     N = positions.shape[0]
     if k_new.shape != (N, pool.n_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
         raise ValueError("k_new/v_new must be [tokens, Hkv, D] matching the pool and positions")
@@ -940,41 +941,47 @@ def alloc_kv8_workspace(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: i
 
 
 def _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out, workspace, ndim):
-    """(current device, Hkv, D, P, NP, dtype code) of an attention call's checked arguments."""
+    """(current device, table columns, pages, Hkv, P, D, dtype code) of an attention
+    call's checked arguments.  (The numbers of dims are checked with the shapes.)"""
     dev = -1
     try:
         dev = q.get_device()
+        dtype = q.dtype
+        sdt = scales.dtype
         ok = (dev >= 0 and out.get_device() == dev and k_pool.get_device() == dev
               and v_pool.get_device() == dev and scales.get_device() == dev
               and page_table.get_device() == dev and context_lens.get_device() == dev
-              and workspace.get_device() == dev and out.dtype is q.dtype
+              and workspace.get_device() == dev and out.dtype is dtype
               and k_pool.dtype is _E4M3 and v_pool.dtype is _E4M3 and page_table.dtype is _I32
               and context_lens.dtype is _I32 and workspace.dtype is torch.uint8
-              and q.dim() == ndim and k_pool.dim() == 4 and scales.dim() == 4
-              and page_table.dim() == 2 and context_lens.dim() == 1 and q.is_contiguous()
+              and (sdt is _E8M0 or sdt is torch.uint8) and q.is_contiguous()
               and out.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
               and scales.is_contiguous() and page_table.is_contiguous()
               and context_lens.is_contiguous() and workspace.is_contiguous()
               and dev == _get_device())
+        if ok:
+            qs, ks, ts = q.shape, k_pool.shape, page_table.shape
+            ok = len(qs) == ndim and len(ks) == 4 and len(ts) == 2 and dtype in _DT
     except AttributeError:
         ok = False
     if not ok:
         _dev(q, "q", None, ndim)
+        _dtype_code(q)
+        _dev(scales, "scales", None, 4)
+        _kv8_scales(scales)
         _kv8_explain((out, "out", q.dtype, ndim), (k_pool, "k_pool", _E4M3, 4),
-                     (v_pool, "v_pool", _E4M3, 4), (scales, "scales", None, 4),
-                     (page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
+                     (v_pool, "v_pool", _E4M3, 4), (page_table, "page_table", _I32, 2),
+                     (context_lens, "context_lens", _I32, 1),
                      (workspace, "workspace", torch.uint8))
-    dt = _dtype_code(q)
-    _kv8_scales(scales)
-    NP, Hkv, P, D = k_pool.shape
-    B = q.shape[0]
-    if v_pool.shape != k_pool.shape or scales.shape != (NP, Hkv, P // 16, 2):
+    NP, Hkv, P, D = ks
+    B, cols = ts
+    if v_pool.shape != ks or scales.shape != (NP, Hkv, P // 16, 2):
         raise ValueError("k_pool/v_pool must be [NP, Hkv, P, D] and scales [NP, Hkv, P / 16, 2]")
-    if q.shape[-1] != D or out.shape != q.shape:
+    if qs[-1] != D or out.shape != qs:
         raise ValueError("q/out [..., Hq, D] and pools [NP, Hkv, P, D] disagree")
-    if page_table.shape[0] != B or context_lens.shape[0] != B:
+    if qs[0] != B or context_lens.shape != (B,):
         raise ValueError("page_table rows or context_lens != batch")
-    return dev, Hkv, D, P, NP, dt
+    return dev, cols, NP, Hkv, P, D, _DT[dtype]
 
 
 def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -984,12 +991,12 @@ def paged_decode_attention_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: to
                                stream=None) -> torch.Tensor:
     """paged_decode_attention over an 8-bit cache: q, out [B, Hq, D] in float16
     or bfloat16, pools float8_e4m3fn, scales float8_e8m0fnu."""
-    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                       workspace, 3)
+    dev, cols, NP, Hkv, P, D, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens,
+                                             out, workspace, 3)
     B, Hq, _ = q.shape
     _check(load_library().paged_decode_attention_kv8(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
-        page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP,
+        page_table.data_ptr(), cols, context_lens.data_ptr(), B, Hq, Hkv, D, P, NP,
         dt, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         int(num_workers), _current(stream, dev)), "paged_decode_attention_kv8")
     return out
@@ -1002,12 +1009,12 @@ def paged_decode_attention_multi_kv8(q: torch.Tensor, k_pool: torch.Tensor, v_po
                                      stream=None) -> torch.Tensor:
     """paged_decode_attention_multi over an 8-bit cache: q, out [B, Qn, Hq, D],
     query j of sequence b attends causally to tokens 0 .. context_lens[b] - Qn + j."""
-    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                       workspace, 4)
+    dev, cols, NP, Hkv, P, D, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens,
+                                             out, workspace, 4)
     B, Qn, Hq, _ = q.shape
     _check(load_library().paged_decode_attention_multi_kv8(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(),
-        page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(), B, Qn, Hq, Hkv, D, P,
+        page_table.data_ptr(), cols, context_lens.data_ptr(), B, Qn, Hq, Hkv, D, P,
         NP, dt, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         int(num_workers), _current(stream, dev)), "paged_decode_attention_multi_kv8")
     return out
@@ -1024,8 +1031,8 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
     """One decode step over an 8-bit cache: append k_new/v_new [B, Hkv, D] at
     positions[b], then decode attention into out; with rope_theta > 0 the rotary
     embedding of q and k_new (after the optional per-head RMS norm) comes first."""
-    dev, Hkv, D, P, NP, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens, out,
-                                       workspace, 3)
+    dev, cols, NP, Hkv, P, D, dt = _kv8_call(q, k_pool, v_pool, scales, page_table, context_lens,
+                                             out, workspace, 3)
     B, Hq, _ = q.shape
     try:
         ok = (k_new.get_device() == dev and v_new.get_device() == dev
@@ -1044,10 +1051,10 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
     _check(load_library().paged_decode_step_kv8(
         k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), q.data_ptr(),
         k_pool.data_ptr(), v_pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(),
-        page_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, P, NP, dt, float(scale),
-        float(rope_theta), _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps),
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(), int(num_workers),
-        _current(stream, dev)), "paged_decode_step_kv8")
+        cols, context_lens.data_ptr(), B, Hq, Hkv, D, P, NP, dt, float(scale), float(rope_theta),
+        _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps), out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), int(num_workers), _current(stream, dev)),
+        "paged_decode_step_kv8")
     return out
 
 
