@@ -4,16 +4,21 @@
 // A run is the longest stretch of consecutive tokens of one sequence, at
 // consecutive positions, within one block of 16: the unit that sets a block's
 // scale.  Its first token (its leader) is found from the token and the one
-// before it alone, so a CTA needs no list of sequences: CTA i owns the runs
-// whose leaders lie among tokens S i .. S i + S - 1, which are the tokens from
+// before it alone, so a CTA needs no list of sequences: CTA (i, y) has the runs
+// whose leaders lie among tokens 16 i .. 16 i + 15, which are the tokens from
 // its first leader up to the next CTA's.  The cos / sin of those tokens are
 // formed once in shared memory for all heads; then a group of lanes takes a
 // row of q, and a warp takes one (run, head, side): the whole block in
-// registers, one pass over the data.
+// registers, one pass over the data.  The CTAs of one i share these tasks.
 //
-// What bounds it: long prompts, HBM (q read and written in 16 bits, K and V
-// read in 16 and written in 8); a step's single tokens, latency.
+// What bounds it: long prompts, HBM (q read and written in 16 bits, K and V read
+// in 16 and written in 8) and the instructions around it -- 8 prompts of 509 to 4096
+// tokens, 32/8 heads of 128, norm and rotation: 325 MB in 66.6 us, 72% of the
+// measured copy rate, 53% of the issue slots; a step's single tokens, latency (256
+// tokens, 28/4 heads: 3.3 us).
 #include <math.h>
+
+#include <algorithm>
 
 #include "kv8.cuh"
 
@@ -25,7 +30,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDepth = 2;   // tasks of a warp whose rows are on the way
 constexpr int kVecs = 8;    // 16-byte vectors a lane holds of a task's rows
-constexpr int kMaxSpan = 16 + kChunk - 1;  // tokens a CTA may own (S <= 16)
+constexpr int kSlots = 2 * 152;  // CTAs that run at the same time
+constexpr int kSpan = 16;   // tokens a CTA looks for leaders among
+constexpr int kMaxSpan = kSpan + kChunk - 1;  // tokens it may own
 
 // Pairs of floats: the packed multiply and fused multiply-add of this part (each
 // half rounds as the scalar one does) halve the arithmetic's instructions.
@@ -164,8 +171,8 @@ __device__ __forceinline__ float max_abs8(const f2 (&x)[4], float m) {
 
 // A lane's vectors of a task come through shared memory by asynchronous copies
 // (its own vectors only: no other lane waits for them), two tasks ahead: in
-// registers the loads in flight would have to wait for the arithmetic of the task
-// before (96 us against ... of the prompts below).
+// registers the loads would wait for the arithmetic of the task before (82.5 us of
+// the prompts above, against 68.0; three tasks ahead leave one CTA an SM: 98).
 __device__ __forceinline__ void copy_vec(uint32_t dst, const uint4* src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(ok ? 16 : 0)
@@ -348,7 +355,7 @@ constexpr int kSmemBytes = 2 * kMaxSpan * (D / 2) * 4 + 2 * D * 4 + kWarps * kDe
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
-kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* status) {
+kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* status) {
     constexpr int HALF = D / 2, HV = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];  // kSmemBytes<D>
     float* ctab = reinterpret_cast<float*>(smem);
@@ -361,7 +368,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
     __shared__ Run s_runs[kMaxSpan];
     __shared__ int s_first, s_end, s_nruns;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int base = blockIdx.x * span;  // the CTA's leaders: tokens base .. base + span - 1
+    const int base = blockIdx.x * kSpan;  // the CTA's leaders: tokens base .. base + 15
 
     pdl_wait();
     if (a.q_norm_w || a.k_norm_w) {
@@ -375,7 +382,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
     }
     if (warp == 0) {
         // token base + lane and the one before it; the last one a CTA can own
-        // is base + span + 14, so lane 31 sees the next CTA's first leader
+        // is base + kSpan + 14, so lane 31 sees the next CTA's first leader
         const int i = base + lane;
         const bool in = i < a.n_tokens;
         const int pos = in ? a.positions[i] : -1;
@@ -389,8 +396,8 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
                           (pos & (kChunk - 1)) != 0;
         // tokens past the last one end the last run
         const unsigned lead = __ballot_sync(kFull, !cont);
-        const int first = __ffs(lead & (span == 16 ? 0xffffu : (1u << span) - 1u)) - 1;
-        const unsigned after = lead >> span << span;
+        const int first = __ffs(lead & ((1u << kSpan) - 1u)) - 1;
+        const unsigned after = lead >> kSpan << kSpan;
         const int end = min(after ? __ffs(after) - 1 : 32, a.n_tokens - base);
         const bool mine = first >= 0 && lane >= first && lane < end;
         // runs of the CTA: leaders among its tokens that are appended
@@ -441,6 +448,8 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
     const int blocks = s_nruns * per_run;
     const int stretches = a.q ? (a.n_q_heads + U * RPP - 1) / (U * RPP) : 0;
     const int tasks = blocks + ntok * stretches;
+    const int step = kWarps * gridDim.y, x0 = blockIdx.y * kWarps + warp;
+    if (x0 - warp >= tasks) return;
     const int jl = lane % HV, rl = lane / HV;
     auto fetch = [&](int x, int buf) {
         const uint32_t dst = ring + buf * (kVecs * 512);
@@ -473,7 +482,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int k = 0; k < kDepth; ++k) fetch(warp + k * kWarps, k);
+    for (int k = 0; k < kDepth; ++k) fetch(x0 + k * step, k);
     if (a.rope) {  // while the first rows come
         for (int x = tid; x < ntok * HALF; x += kThreads) {
             const int tk = x / HALF, i = x - tk * HALF;
@@ -483,7 +492,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
         __syncthreads();
     }
     int buf = 0;
-    for (int x = warp; x < tasks; x += kWarps) {
+    for (int x = x0; x < tasks; x += step) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
         uint4 v[kVecs];
 #pragma unroll
@@ -491,7 +500,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int span, uint32_t* s
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
                          : "r"(ring + (buf * kVecs + k) * 512));
-        fetch(x + kDepth * kWarps, buf);
+        fetch(x + kDepth * step, buf);
         buf = buf + 1 == kDepth ? 0 : buf + 1;
         if (x < blocks) {
             const int ri = x / per_run, y = x - ri * per_run;
@@ -704,11 +713,19 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* st
         PKV_KV8_SINGLE(__half, 64);
 #undef PKV_KV8_SINGLE
     }
-    // leaders a CTA looks for among so many tokens: few tokens, a CTA for every
-    // block; many, one for about every block of a prompt, so that its angles serve
-    // a whole one
-    const int span = a.n_tokens <= 2048 ? 1 : 16;
-    const dim3 grid((unsigned)(a.n_tokens / span + (a.n_tokens % span ? 1 : 0)));
+    // CTAs that share the tasks of 16 tokens: while there are few, twice as many in
+    // all as the device holds, up to a task a warp where every token is a run of its
+    // own (8 prompts, 32/8 heads of 128, norm and rotation, us with 1 / 2 / 4 / 8: 640
+    // tokens 29.5 / 16.6 / 10.6 / 9.3; 1500: 29.0 / 17.7 / 14.5 / 15.1; 4200: 34.2 /
+    // 28.3 / 29.9 / 34.9; 8300: 48.4 / 47.1 / 52.2 / 65.5; 17700: 67.6 / 72.1 / 85.9 /
+    // 110.4, each forms the angles of its tokens again).
+    const int groups = a.n_tokens / kSpan + (a.n_tokens % kSpan ? 1 : 0);
+    const int stretch = kVecs / 2 * (32 / (head_dim / 16));  // q rows of a task
+    const long long tasks =
+        2LL * a.n_kv_heads + (a.q ? (a.n_q_heads + stretch - 1) / stretch : 0);  // a token's
+    const long long most = (kSpan * tasks + kWarps - 1) / kWarps;
+    const dim3 grid((unsigned)groups,
+                    (unsigned)std::max(1LL, std::min(most, (long long)(2 * kSlots / groups))));
     // more shared memory than a kernel has unasked (cheap, and per device: asked
     // for with every launch)
 #define PKV_KV8_APPEND(T, D)                                                                     \
@@ -718,7 +735,7 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* st
                                                    kSmemBytes<D>);                               \
         if (e != cudaSuccess) return e;                                                          \
         return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), kSmemBytes<D>, stream,  \
-                          a, span, status);                                                      \
+                          a, status);                                                            \
     } while (0)
     if (a.bf16) {
         if (head_dim == 128) PKV_KV8_APPEND(__nv_bfloat16, 128);
