@@ -1449,8 +1449,12 @@ namespace {
 // tcgen05 one, which takes over from kKv8UmmaMinRows rows of a KV head on.
 constexpr int kKv8UnitRows = 32;
 constexpr int kKv8UmmaMinRows = 64;
-// A unit's start on the tcgen05 kernel, in chunks.
-constexpr int kKv8UmmaUnitCost = 8;
+// A unit's start and end on the tcgen05 kernel (its queries converted, its sums
+// written) in chunks (us with 8 / 12 / 16 / 20 / 24 / 32; 4 sequences of 1000 to 8192
+// tokens, 64 query tokens: 59.5 / 57.5 / 56.3 / 55.1 / 54.9 / 57.2; 32 of 512 to 4096,
+// 16 query tokens: 87.8 / 85.3 / 85.9 / 86.6 / 87.4 / 90.7; 9 of 100 to 900, 64: - /
+// 42.5 / 40.9 / 38.8 / 38.8 / 41.6).
+constexpr int kKv8UmmaUnitCost = 20;
 
 pkv_status setup_kv8(int batch, int n_queries, int n_q_heads, int n_kv_heads, int head_dim,
                      int page_size, pkv_dtype dtype, int num_workers, DecodeSetup* s) {

@@ -11,14 +11,23 @@
 //   P = 2^(x - m)     two threads a row, half of the tokens each
 //   O = O 2^(m_old - m) + P V     M = 128, N = D, K = tokens
 //
-// The e4m3 bytes come by plain 16-byte loads into registers a block ahead (their
-// latency passes behind the products and the softmax), are converted to fp16,
-// which holds them exactly, and stored in the 128-byte swizzled layout that the
-// tensor cores read; K's place takes P once S is done, so that two CTAs share an
-// SM and one's products run under the other's conversion and softmax.
+// The e4m3 bytes come by plain 16-byte loads into registers, a warp a chunk (its
+// page, scales and length are then the warp's), K's during the softmax of the block
+// before and V's during its last product.  They are converted to fp16, which holds
+// them exactly, and stored in the 128-byte swizzled layout that the tensor cores
+// read; K's place takes P once S is done, so that two CTAs share an SM and one's
+// products run under the other's conversion and softmax.  (Tensor copies would
+// need 32 KiB more for the raw bytes, and leave one CTA an SM.)
 //
-// What bounds it: the exponentials (16 a cycle and SM, so 1024 cycles a block of
-// 128 x 128 against 650 for its two products) and the instructions around them.
+// What bounds it: the chain of a block's phases -- convert, product, maximum,
+// exponentials, product, with a barrier or a wait between them -- of about 8000
+// cycles, of which two CTAs an SM overlap; the floor beneath is 1024 cycles of
+// exponentials (16 a cycle and SM) and as many of products for a block of 128 x
+// 128.  4 sequences of 1000 to 8192 tokens with 64 query tokens, 32/8 heads of 128:
+// 56 us and 11 for the combine by themselves, 59.6 us in a row (270 TFLOP/s),
+// against 107 on the warp kernel; the issue slots are 38% busy, the tensor pipe
+// 14%.  It takes over at 64 rows of a KV head: 32 sequences of 512 to 4096 tokens,
+// 16 query tokens: 95.9 us against 106.8; 12 (48 rows): 92.2 against 81.1.
 //
 // Every wait is bounded: on a timeout the CTA reports PKV_DEV_TIMEOUT, waits
 // (bounded) once more for its products in flight, frees its tensor memory and
@@ -35,8 +44,7 @@ namespace {
 constexpr int kRows = kKv8UmmaRows;   // M: one tensor-memory lane a row
 constexpr int kBlockChunks = 8;
 constexpr int kBlockTok = kBlockChunks * kChunk;
-// (Four threads a row, in 64 registers each, spill: 86 against 63 us of
-// the 64 tokens of 4 sequences of 1000 to 8192 below.)
+// (Four threads a row, in 64 registers each, spill: 86 against 63 us.)
 constexpr int kThreads = 256;
 constexpr int kParts = kThreads / 128;             // threads a row: each its part of the tokens
 constexpr int kPartChunks = kBlockChunks / kParts;  // ... and of O's columns
