@@ -1446,9 +1446,12 @@ pkv_status paged_decode_attention_multi(const void* q, const void* k_pool, const
 namespace {
 
 // Rows of a unit: at most 32 (four tiles of 8) on the warp kernel, 128 on the
-// tcgen05 one, which takes over from kKv8UmmaMinRows rows of a KV head on.
+// tcgen05 one, which takes over from kKv8UmmaMinRows rows of a KV head on.  (us, warp
+// kernel / tcgen05, bf16, 32/8 heads of 128; 32 sequences of 512 to 4096 tokens: 40
+// rows 77.6 / 80.8, 48 rows 79.8 / 82.5, 64 rows 106.8 / 86.6; 4 of 1000 to 8192: 32
+// rows 31.6 / 30.4, 40 rows 32.2 / 31.0, 48 rows 33.3 / 31.6.)
 constexpr int kKv8UnitRows = 32;
-constexpr int kKv8UmmaMinRows = 64;
+constexpr int kKv8UmmaMinRows = 49;
 // A unit's start and end on the tcgen05 kernel (its queries converted, its sums
 // written) in chunks (us with 8 / 12 / 16 / 20 / 24 / 32; 4 sequences of 1000 to 8192
 // tokens, 64 query tokens: 59.5 / 57.5 / 56.3 / 55.1 / 54.9 / 57.2; 32 of 512 to 4096,
@@ -1606,7 +1609,7 @@ pkv_status kv8_run(const Kv8Call& c, const void* q, const DecodeSetup& s, bool a
     p.self_plan = c.batch <= pkv::kKv8SelfPlan;
     p.after_append = append_flags;
     p.unit_cost = s.kernel.q8.umma ? kKv8UmmaUnitCost : pkv::kKv8UnitCost;
-    p.merge = s.units * s.gs <= pkv::kKv8RowCtas ? warps : 1;
+    p.merge = pkv::kv8_merge_warps((int)s.units, s.workers, warps);
     p.workers_req = c.num_workers;
     p.workers_auto = s.workers_auto;
     p.batch = c.batch;

@@ -64,10 +64,12 @@ __device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
 
 // --- decode (kv8_decode.cuh) ------------------------------------------------
 // Batches up to this size: every CTA of the decode kernel works the ranges out
-// for itself; larger ones: the plan kernel does, once.
-constexpr int kKv8SelfPlan = 256;
+// for itself; larger ones: the plan kernel does, once (256 sequences of 100 to 500
+// tokens: 34.5 us, 36.5 with the plan kernel; 400: 47.8 against 50.7).
+constexpr int kKv8SelfPlan = 512;
 // A unit's start (its queries, its result) counts as this many chunks when the
-// ranges are cut.
+// ranges are cut (112 sequences of 5 to 4000 tokens, us with 1 / 2 / 4 / 7 / 10:
+// 82.4 / 75.0 / 71.1 / 72.6 / 74.5).
 constexpr int kKv8UnitCost = 4;
 // Automatic worker count: at least this many positions each.
 constexpr int kKv8MinPositions = 4;
@@ -106,14 +108,15 @@ __host__ __device__ __forceinline__ void kv8_ranges(int total, int workers_req, 
 constexpr int kKv8RowCtas = 512;
 
 // Workers whose parts of one unit are merged by their CTA before they leave it:
-// `most` (a CTA's, or 1: beyond kKv8RowCtas rows, and where a worker is a CTA)
-// when units are few beside the workers (nw); else 1, none are.  Merging costs the
-// decode kernel 1.5 us at its end (32 sequences of 512 to 4096 tokens, 7 workers a
-// unit: 23.6 against 22.1 us); one sequence of 32768 tokens (228 a unit) gains
-// more in the combine (23.4 us both together against 24.4, and 15.2 against 18.7
-// with one KV head).
+// `most` (a CTA's, or 1 where a worker is a CTA) when units are few beside the
+// workers (nw); else 1, none are.  Merging costs the decode kernel 1.5 us at its end
+// (32 sequences of 512 to 4096 tokens, 7 workers a unit: 23.6 against 22.1 us); one
+// sequence of 32768 tokens (228 a unit) gains more in the combine (23.4 us both
+// together against 24.4, and 15.2 against 18.7 with one KV head), and so do several
+// query tokens, whose states are large (5 query tokens: 4 sequences of 1000 to 8192
+// tokens, 38 workers a unit, 25.7 against 29.8; 8, 19 a unit, 30.6 against 33.0).
 __host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw, int most) {
-    return nw / 32 > units ? most : 1;
+    return nw / 16 > units ? most : 1;
 }
 
 struct Kv8DecodeParams {

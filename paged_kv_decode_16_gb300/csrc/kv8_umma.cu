@@ -24,10 +24,8 @@
 // cycles, of which two CTAs an SM overlap; the floor beneath is 1024 cycles of
 // exponentials (16 a cycle and SM) and as many of products for a block of 128 x
 // 128.  4 sequences of 1000 to 8192 tokens with 64 query tokens, 32/8 heads of 128:
-// 56 us and 11 for the combine by themselves, 59.6 us in a row (270 TFLOP/s),
-// against 107 on the warp kernel; the issue slots are 38% busy, the tensor pipe
-// 14%.  It takes over at 64 rows of a KV head: 32 sequences of 512 to 4096 tokens,
-// 16 query tokens: 95.9 us against 106.8; 12 (48 rows): 92.2 against 81.1.
+// 55.3 us with the combine (290 TFLOP/s), against 107 on the warp kernel; the issue
+// slots are 38% busy, the tensor pipe 14%.
 //
 // Every wait is bounded: on a timeout the CTA reports PKV_DEV_TIMEOUT, waits
 // (bounded) once more for its products in flight, frees its tensor memory and

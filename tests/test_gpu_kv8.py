@@ -337,6 +337,7 @@ SHAPES = [  # lens, Hq, Hkv, D, P
     ([700], 64, 1, 128, 16),          # a group that fills half a tensor-core tile
     ([90, 1500, 0, 17], 96, 1, 64, 32),
     ([640, 33], 260, 2, 128, 48),     # 130 rows a KV head: two tiles
+    ([1200] * 16 + [1111], 32, 1, 128, 16),  # parts merged in their CTA, a warp a row after
 ]
 
 
@@ -447,6 +448,10 @@ def test_decode_nan_where_seen_only():
     (40, [41, 700, 2, 0, 129], 4, 2, 128, 16),   # 80 rows a KV head
     (64, [2000, 1], 5, 1, 64, 64),               # 320 rows: three tiles
     (17, [400, 18], 24, 3, 128, 48),             # 136 rows
+    (8, [1500, 900, 1211], 32, 8, 128, 16),      # parts merged in their CTA
+    (3, [1500, 700, 9, 1211, 900], 48, 8, 64, 32),
+    (12, [800, 90], 8, 2, 128, 16),              # the most rows of the warp kernel
+    (7, [800, 90], 14, 2, 64, 16),               # the fewest of the tensor-core tile
 ])
 def test_multi(dtype, workers, Q, lens, Hq, Hkv, D, P):
     c = Cache(11, lens, Hkv, D, P).poison().gpu()
@@ -504,7 +509,7 @@ def test_attention_bad_inputs(Hq):
     assert out.isfinite().all()
 
 
-@pytest.mark.parametrize("B", [1, 300])
+@pytest.mark.parametrize("B", [1, 300, 600])
 @pytest.mark.parametrize("group", [1, 64])
 def test_more_positions_than_32_bits(B, group):
     """A batch whose chunks over all heads do not fit 32 bits is refused on the
