@@ -71,8 +71,12 @@ constexpr int kKv8SelfPlan = 512;
 // ranges are cut (112 sequences of 5 to 4000 tokens, us with 1 / 2 / 4 / 7 / 10:
 // 82.4 / 75.0 / 71.1 / 72.6 / 74.5).
 constexpr int kKv8UnitCost = 4;
-// Automatic worker count: at least this many positions each.
-constexpr int kKv8MinPositions = 4;
+// Automatic worker count: at least this many positions each (us with 1 / 2 / 4 / 8; 32/8
+// heads of 128, one query token; one sequence of 200: 8.4 / 9.1 / 10.0 / 12.5, of 1500:
+// 10.8 / 10.1 / 10.9 / 12.8, of 4000: 13.0 / 11.5 / 11.6 / 13.5; 16 of 64 tokens, a
+// unit no longer whole: 12.5 / 12.2 / 11.0 / -; 8 query tokens of 4 sequences of 900: 22.3
+// / 21.7 / 24.1 / -; the tcgen05 kernel within 1 us of 1 to 8).
+constexpr int kKv8MinPositions = 2;
 
 constexpr int kKv8Warps = 4;  // workers (warps) of a CTA of the decode kernel
 

@@ -398,6 +398,23 @@ def test_decode_large_batches():
         assert (two[3] == 0).all()
 
 
+@pytest.mark.parametrize("B", [511, 512, 513])
+@pytest.mark.parametrize("Hq", [4, 140])
+def test_decode_batches_around_the_plan(B, Hq):
+    """The largest batches whose ranges every CTA works out, the smallest beyond."""
+    lens = np.random.default_rng(B).integers(0, 50, B)
+    lens[-1] = 41
+    c = Cache(25, lens, 2, 64, 16).poison().gpu()
+    q = torch.randn(B, Hq, 64, generator=torch.Generator().manual_seed(4)).half().cuda()
+    out = decode(c, q, 0.125)
+    sel = np.r_[0:20, B - 20:B]
+    sub = Cache.__new__(Cache)
+    sub.__dict__.update(c.__dict__)
+    sub.table, sub.lens = c.table[sel], c.lens[sel]
+    check(sub, q[sel][:, None], out[sel][:, None], 0.125)
+    assert (out[c.lens_g == 0] == 0).all()
+
+
 def test_decode_queries_of_any_size():
     """bf16 queries far outside fp16's range, zero rows and mixed sizes in a row."""
     c = Cache(9, [100, 300, 64], 2, 128, 16).gpu()
