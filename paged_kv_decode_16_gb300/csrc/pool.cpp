@@ -55,9 +55,10 @@ static pkv_status check_pool_built(int page_size, int head_dim) {
 static pkv_status allocate_pool(pkv_pool* p, size_t bytes, size_t scale_bytes) {
     bool ok = cudaGetDevice(&p->device) == cudaSuccess &&
               cudaMalloc(&p->k, bytes) == cudaSuccess && cudaMalloc(&p->v, bytes) == cudaSuccess;
-    if (ok && scale_bytes)
+    if (ok && scale_bytes)  // zeroed before any stream can append to the pool
         ok = cudaMalloc(&p->scales, scale_bytes) == cudaSuccess &&
-             cudaMemset(p->scales, 0, scale_bytes) == cudaSuccess;
+             cudaMemset(p->scales, 0, scale_bytes) == cudaSuccess &&
+             cudaStreamSynchronize(nullptr) == cudaSuccess;
     if (ok) {
         p->owned = true;
         return PKV_OK;
