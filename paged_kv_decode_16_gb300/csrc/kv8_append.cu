@@ -4,16 +4,16 @@
 // A run is the longest stretch of consecutive tokens of one sequence, at
 // consecutive positions, within one block of 16: the unit that sets a block's
 // scale.  Its first token (its leader) is found from the token and the one
-// before it alone, so a CTA needs no list of sequences: CTA (i, y) has the runs
+// before it alone, so a CTA needs no list of sequences: a CTA of group i has the runs
 // whose leaders lie among tokens 16 i .. 16 i + 15, which are the tokens from
-// its first leader up to the next CTA's.  The cos / sin of those tokens are
+// its first leader up to the next group's.  The cos / sin of those tokens are
 // formed once in shared memory for all heads; then a group of lanes takes a
 // row of q, and a warp takes one (run, head, side): the whole block in
-// registers, one pass over the data.  The CTAs of one i share these tasks.
+// registers, one pass over the data.  The CTAs of a group share these tasks.
 //
 // What bounds it: long prompts, HBM (q read and written in 16 bits, K and V read
 // in 16 and written in 8) and the instructions around it -- 8 prompts of 509 to 4096
-// tokens, 32/8 heads of 128, norm and rotation: 325 MB in 66.6 us, 72% of the
+// tokens, 32/8 heads of 128, norm and rotation: 325 MB in 65.9 us, 73% of the
 // measured copy rate, 53% of the issue slots; a step's single tokens, latency (256
 // tokens, 28/4 heads: 3.3 us).
 #include <math.h>
@@ -355,7 +355,8 @@ constexpr int kSmemBytes = 2 * kMaxSpan * (D / 2) * 4 + 2 * D * 4 + kWarps * kDe
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
-kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* status) {
+kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int alone, int rest,
+                  int parts, uint32_t* status) {
     constexpr int HALF = D / 2, HV = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];  // kSmemBytes<D>
     float* ctab = reinterpret_cast<float*>(smem);
@@ -368,7 +369,11 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* status) {
     __shared__ Run s_runs[kMaxSpan];
     __shared__ int s_first, s_end, s_nruns;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int base = blockIdx.x * kSpan;  // the CTA's leaders: tokens base .. base + 15
+    // the CTA's leaders: tokens base .. base + 15, the first `alone` groups of 16 a
+    // CTA each, the others `parts`
+    const int bx = blockIdx.x, past = bx - alone;
+    const int base = (past < 0 ? bx : alone + past % rest) * kSpan;
+    const int part = past < 0 ? 0 : past / rest, n_parts = past < 0 ? 1 : parts;
 
     pdl_wait();
     if (a.q_norm_w || a.k_norm_w) {
@@ -448,7 +453,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, uint32_t* status) {
     const int blocks = s_nruns * per_run;
     const int stretches = a.q ? (a.n_q_heads + U * RPP - 1) / (U * RPP) : 0;
     const int tasks = blocks + ntok * stretches;
-    const int step = kWarps * gridDim.y, x0 = blockIdx.y * kWarps + warp;
+    const int step = kWarps * n_parts, x0 = part * kWarps + warp;
     if (x0 - warp >= tasks) return;
     const int jl = lane % HV, rl = lane / HV;
     auto fetch = [&](int x, int buf) {
@@ -713,19 +718,25 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* st
         PKV_KV8_SINGLE(__half, 64);
 #undef PKV_KV8_SINGLE
     }
-    // CTAs that share the tasks of 16 tokens: while there are few, twice as many in
-    // all as the device holds, up to a task a warp where every token is a run of its
-    // own (8 prompts, 32/8 heads of 128, norm and rotation, us with 1 / 2 / 4 / 8: 640
-    // tokens 29.5 / 16.6 / 10.6 / 9.3; 1500: 29.0 / 17.7 / 14.5 / 15.1; 4200: 34.2 /
-    // 28.3 / 29.9 / 34.9; 8300: 48.4 / 47.1 / 52.2 / 65.5; 17700: 67.6 / 72.1 / 85.9 /
-    // 110.4, each forms the angles of its tokens again).
+    // Groups of 16 tokens: as many as fill the device once or several times have a CTA
+    // each; the rest, or all when they are fewer, share what it holds, twice over:
+    // several CTAs to a group, up to a task a warp where every token is a run of its
+    // own, behind groups with a CTA each two tasks of a prompt's.  (8 prompts, 32/8 heads
+    // of 128, norm and rotation, us with 1 / 2 / 4 / 8 CTAs to every group: 640 tokens
+    // 29.5 / 16.6 / 10.6 / 9.3; 1500: 29.0 / 17.7 / 14.5 / 15.1; 4200: 34.2 / 28.3 /
+    // 29.9 / 34.9; 8300: 48.4 / 47.1 / 52.2 / 65.5, by this rule 44.1; 17700: 67.6 /
+    // 72.1 / 85.9 / 110.4, 65.9: each forms the angles of its tokens again.  D = 64,
+    // 16/2 heads, 17700: 24.2, 25.7 with fewer tasks a warp.)
     const int groups = a.n_tokens / kSpan + (a.n_tokens % kSpan ? 1 : 0);
+    const int alone = groups / kSlots * kSlots, rest = groups - alone;
     const int stretch = kVecs / 2 * (32 / (head_dim / 16));  // q rows of a task
-    const long long tasks =
-        2LL * a.n_kv_heads + (a.q ? (a.n_q_heads + stretch - 1) / stretch : 0);  // a token's
-    const long long most = (kSpan * tasks + kWarps - 1) / kWarps;
-    const dim3 grid((unsigned)groups,
-                    (unsigned)std::max(1LL, std::min(most, (long long)(2 * kSlots / groups))));
+    const long long per_tok = a.q ? (a.n_q_heads + stretch - 1) / stretch : 0;
+    const long long most =
+        alone ? (2LL * a.n_kv_heads + kSpan * per_tok) / (2 * kWarps)
+              : (kSpan * (2LL * a.n_kv_heads + per_tok) + kWarps - 1) / kWarps;
+    const int parts =
+        rest ? (int)std::max(1LL, std::min(most, (long long)(2 * kSlots / rest))) : 1;
+    const dim3 grid((unsigned)(alone + rest * parts));
     // more shared memory than a kernel has unasked (cheap, and per device: asked
     // for with every launch)
 #define PKV_KV8_APPEND(T, D)                                                                     \
@@ -735,7 +746,7 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* st
                                                    kSmemBytes<D>);                               \
         if (e != cudaSuccess) return e;                                                          \
         return launch_pdl(kv8_append_kernel<T, D>, grid, dim3(kThreads), kSmemBytes<D>, stream,  \
-                          a, status);                                                            \
+                          a, alone, rest, parts, status);                                        \
     } while (0)
     if (a.bf16) {
         if (head_dim == 128) PKV_KV8_APPEND(__nv_bfloat16, 128);
