@@ -288,6 +288,37 @@ def test_append_rope(dtype, D, Hq, Hkv, theta, qn, kn_, big):
     assert all(np.array_equal(a, b) for a, b in zip(again, (gk, gv, gs))), "a second append"
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D,count", [(128, [1777, 3090, 133]), (64, [4864]), (128, [4863, 1]),
+                                     (64, [2000, 7777, 5, 18])])
+def test_append_many_tokens(dtype, D, count):
+    """More tokens than the device takes at once: the same bytes as a call a prompt."""
+    Hq, Hkv, P = 64, 4, 32
+    count = np.array(count)
+    B = len(count)
+    c = Cache(26, count, Hkv, D, P).gpu()
+    one = Cache(26, count, Hkv, D, P).gpu()
+    seq = np.repeat(np.arange(B), count)
+    pos = np.concatenate([np.arange(n) for n in count])
+    kn, vn = new_rows(c, len(pos), dtype)
+    q = torch.randn(len(pos), Hq, D, device="cuda").to(dtype)
+    wq = (1 + 0.2 * torch.randn(D)).to(dtype).cuda()
+    out, two = torch.empty_like(q), torch.empty_like(q)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.kv8_append_rope(c.pool(), q, kn, vn, c.table_g, i32(pos), 10000.0, out, i32(seq),
+                        dev_status=st, q_norm_weight=wq, k_norm_weight=wq)
+    for b in range(B):
+        x = slice(int(count[:b].sum()), int(count[:b + 1].sum()))
+        for y in range(x.start, x.stop, 1600):  # pieces of whole blocks, each a small call
+            z = slice(y, min(y + 1600, x.stop))
+            pkv.kv8_append_rope(one.pool(), q[z], kn[z], vn[z], one.table_g, i32(pos[z]), 10000.0,
+                                two[z], i32(seq[z]), dev_status=st, q_norm_weight=wq,
+                                k_norm_weight=wq)
+    assert int(st) == 0
+    assert torch.equal(out, two)
+    assert all(np.array_equal(a, b) for a, b in zip(c.back(), one.back()))
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
