@@ -5,7 +5,7 @@
 // rows have many segments then), a CTA per row, whose warps take every eighth
 // segment each and meet in shared memory.  Rows that the decode kernel finished
 // end at once.  A warp's loads -- its segments' maxima and sums, and the weighted
-// sums of its first eight segments -- go out together, before the first of them
+// sums of its first six or eight segments -- go out together, before the first of them
 // is used: one round of loads behind the one for the ranges is what the kernel
 // takes.  CTA 0 collects the workers' status bits.
 //
@@ -47,12 +47,17 @@ __device__ __forceinline__ Segs kv8_segments(int sw, int r, int u, int a, int e,
 }
 
 constexpr int kWarps = 8;
-constexpr int kBlock = 8;  // segments whose sums are in flight together
+// Segments whose sums are in flight together, where a warp takes a row: 6, and 4 CTAs
+// an SM (us with 8 and 3 / 6 and 4 / 4 and 5: 32 sequences of 512 to 4096 tokens 26.7 /
+// 26.9 / 27.4; with 16 query tokens 86.3 / 85.1 / 84.1; 256 of 16 to 8192 66.3 / 66.0 /
+// 65.9; 4 of 1000 to 8192, 64 query tokens 55.2 / 54.3 / 54.2); where a CTA does: 8 (one
+// sequence of 32768 22.8, with 6 23.3).
+constexpr int kRowBlock = 6, kRowCtasSm = 4, kCtaBlock = 8;
 
 // Segments 0 .. n - 1 of a row by one warp, relative to their own largest
 // maximum M: lane x has elements 4x .. 4x + 3 of the weighted sum.  at(s): the
 // segment's slot; o, m, l: the row's places in a slot.
-template <int D, class At>
+template <int D, int kBlock, class At>
 __device__ __forceinline__ float4 merge_some(const At& at, int n, int o, int m, int l, int lane,
                                              float& M, float& den) {
     const bool act = lane < D / 4;
@@ -76,23 +81,26 @@ __device__ __forceinline__ float4 merge_some(const At& at, int n, int o, int m, 
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) den += __shfl_xor_sync(kFull, den, k);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < n; x0 += kBlock) {
-        if (x0 > 0) {
+    for (int base = 0; base < n; base += 32) {
+        const int stop = min(n, base + 32);
+        if (base > 0)  // weights of the next 32
+            w = base + lane < n ? merge_weight(__ldcg(at(base + lane) + m), M) : 0.f;
+        for (int x0 = base; x0 < stop; x0 += kBlock) {
+            if (x0 > 0) {
 #pragma unroll
-            for (int x = 0; x < kBlock; ++x)
-                if (act && x0 + x < n)
-                    v[x] = __ldcg(reinterpret_cast<const float4*>(at(x0 + x) + o) + lane);
-            if ((x0 & 31) == 0)  // weights of the next 32
-                w = x0 + lane < n ? merge_weight(__ldcg(at(x0 + lane) + m), M) : 0.f;
-        }
+                for (int x = 0; x < kBlock; ++x)
+                    if (act && x0 + x < stop)
+                        v[x] = __ldcg(reinterpret_cast<const float4*>(at(x0 + x) + o) + lane);
+            }
 #pragma unroll
-        for (int x = 0; x < kBlock; ++x) {
-            const float wt = __shfl_sync(kFull, w, (x0 + x) & 31);
-            if (act && x0 + x < n) {
-                acc.x = fmaf(wt, v[x].x, acc.x);
-                acc.y = fmaf(wt, v[x].y, acc.y);
-                acc.z = fmaf(wt, v[x].z, acc.z);
-                acc.w = fmaf(wt, v[x].w, acc.w);
+            for (int x = 0; x < kBlock; ++x) {
+                const float wt = __shfl_sync(kFull, w, (x0 - base + x) & 31);
+                if (act && x0 + x < stop) {
+                    acc.x = fmaf(wt, v[x].x, acc.x);
+                    acc.y = fmaf(wt, v[x].y, acc.y);
+                    acc.z = fmaf(wt, v[x].z, acc.z);
+                    acc.w = fmaf(wt, v[x].w, acc.w);
+                }
             }
         }
     }
@@ -115,7 +123,7 @@ __device__ __forceinline__ void store_row(const float4& acc, float den, int lane
 enum Form { kWarpRow, kWarpRowMerged, kCtaRow };
 
 template <typename T, int D, Form kForm>
-__global__ void __launch_bounds__(kWarps * 32, kForm == kCtaRow ? 1 : 3)
+__global__ void __launch_bounds__(kWarps * 32, kForm == kCtaRow ? 1 : kRowCtasSm)
 kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     constexpr bool kRowCta = kForm == kCtaRow;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,7 +168,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
         __shared__ float s_m[kWarps], s_den[kWarps];
         float M, den;
         const int n = segs.count > warp ? (segs.count - warp + kWarps - 1) / kWarps : 0;
-        const float4 acc = merge_some<D>(
+        const float4 acc = merge_some<D, kCtaBlock>(
             [&](int s) { return a.partials + segs.slot(warp + s * kWarps) * stride; }, n, g * D,
             a.gs * D + g, a.gs * D + a.gs + g, lane, M, den);
         if (lane < D / 4) s_acc[warp][lane] = acc;
@@ -189,7 +197,7 @@ kv8_combine_kernel(const __grid_constant__ Kv8CombineArgs a) {
     } else {
         float M, den;
         const float* slots = a.partials + (segs.u + segs.w0) * (long long)stride;
-        const float4 acc = merge_some<D>(
+        const float4 acc = merge_some<D, kRowBlock>(
             [&](int s) {
                 return kForm == kWarpRowMerged ? a.partials + segs.slot(s) * stride
                                                : slots + s * stride;

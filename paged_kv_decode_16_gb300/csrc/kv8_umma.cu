@@ -24,7 +24,7 @@
 // cycles, of which two CTAs an SM overlap; the floor beneath is 1024 cycles of
 // exponentials (16 a cycle and SM) and as many of products for a block of 128 x
 // 128.  4 sequences of 1000 to 8192 tokens with 64 query tokens, 32/8 heads of 128:
-// 55.3 us with the combine (290 TFLOP/s), against 107 on the warp kernel; the issue
+// 54.3 us with the combine (294 TFLOP/s), against 107 on the warp kernel; the issue
 // slots are 38% busy, the tensor pipe 14%.
 //
 // Every wait is bounded: on a timeout the CTA reports PKV_DEV_TIMEOUT, waits

@@ -446,6 +446,16 @@ def test_decode_batches_around_the_plan(B, Hq):
     assert (out[c.lens_g == 0] == 0).all()
 
 
+@pytest.mark.parametrize("long", [500, 1100, 9000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_one_long_among_many(long, D):
+    """One sequence of many segments (tens to hundreds) where most have one."""
+    lens = np.array([3] * 100 + [long] + [3] * 155)
+    c = Cache(27, lens, 2, D, 16).poison().gpu()
+    q = torch.randn(256, 8, D, generator=torch.Generator().manual_seed(4)).half().cuda()
+    check(c, q[:, None], decode(c, q, 0.1)[:, None], 0.1)
+
+
 def test_decode_queries_of_any_size():
     """bf16 queries far outside fp16's range, zero rows and mixed sizes in a row."""
     c = Cache(9, [100, 300, 64], 2, 128, 16).gpu()
