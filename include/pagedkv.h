@@ -673,7 +673,8 @@ pkv_status paged_decode_kv8_workspace_size(int batch, int n_queries, int n_q_hea
 
 /* paged_decode_attention over an 8-bit cache: q, out [batch][n_q_heads]
  * [head_dim] in dtype; arithmetic in fp32 on the stored values (e4m3 enters
- * the products exactly; the softmax weights with 11 bits or more), out rounded once.
+ * the products exactly; the softmax weights with 11 bits, those below 2^-14 of
+ * their row's sum to 2^-25 of it, whatever the blocks' scales), out rounded once.
  * A NaN in a row that a query attends to gives NaN, elsewhere (behind a
  * sequence's end) none; V scales outside [2^-60, 2^40] are taken as the
  * nearer end, which no append writes.  Results do not depend on page ids or

@@ -20,7 +20,7 @@ namespace pkv {
 
 // Range of the scales' exponents.  100 binary orders: the attention keeps one
 // running maximum for p * 2^e and the softmax's sum alike, and fp32 holds the
-// sum's terms of both ends beside each other that far apart (kv8_decode.cuh).
+// terms of both ends beside each other that far apart (kv8_decode.cuh).
 constexpr int kKv8MinExp = -60;
 constexpr int kKv8MaxExp = 40;
 
@@ -40,6 +40,20 @@ __host__ __device__ __forceinline__ int kv8_need_exp(float a) {
 __host__ __device__ __forceinline__ int kv8_clamp_exp(int e) {
     return e < kKv8MinExp ? kKv8MinExp : (e > kKv8MaxExp ? kKv8MaxExp : e);
 }
+
+// The weights P of a product are fp16, 2^(x - m + lift) for a reference m of the row that x
+// may pass by `slack` before m moves up to it: they stay below 2^15.  x = s + ev holds
+// the exponent of the V scale, so a block of a large one lifts m above the others'
+// weights, whatever its own share in the softmax, down to zero in fp16 (a value of 2^28
+// among ordinary ones: outputs off by as much as they are).  So m suits one exponent,
+// ev_ref: m <= (the row's largest s) + ev_ref.  A block whose ev is larger moves ev_ref
+// up; one whose ev is more than `span` below it moves m down first, to log2 of the row's
+// sum of 2^s, + ev.  Either way a weight has all 11 bits down to 2^-14 of the row's sum,
+// wherever the scales lie.  The fp32 sums cannot overflow by it: the row's l becomes
+// 2^(lift - ev), at most 2^67, and o / l is a mean of values, at most 2^49.
+constexpr float kKv8Slack = 8.f;
+constexpr float kKv8Lift = 7.f;
+constexpr int kKv8Span = 7;
 
 // 2^e, e in [-126, 127].
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }

@@ -18,7 +18,9 @@
 // the exponent, the largest p is about 1 whatever the scales are, and (m, l, o)
 // merge like any other partial states.  (A term of l weighs 2^(s_t - m); a
 // block whose p has left fp32's range, below 2^-126, still has no weight in l
-// because the scales span at most 2^100.)
+// because the scales span at most 2^100.)  P is fp16, so m must suit the chunk at
+// hand: a chunk whose ev lies far below the ones before it lowers m first (kKv8Span,
+// kv8.cuh).
 //
 // Both products run transposed on m16n8k16 (fp16 in, fp32 accumulate), the 16
 // tokens (S^T = K Q^T) or 16 elements of a head (O^T = V^T P^T) as the rows and
@@ -195,10 +197,6 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
     constexpr int DPL = D / 8;      // V elements a lane takes of a row
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr bool kSplitP = !kBf16;  // P in two fp16 pieces
-    // a row's scores may pass m by this much (in binary orders) before m moves:
-    // p stays below 2^8, far inside fp16, and after a range's first chunk the
-    // accumulators are hardly ever rescaled
-    constexpr float kSlack = 8.f;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -364,8 +362,11 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         uint32_t qf[Lay::kQShared ? 1 : NT][KSTEPS][2];  // B fragments of Q^T
         float fs[NT][2];  // score factors of rows 2t, 2t+1 of a tile: scale log2(e) / row scale
         float o[NT][MT][4];  // O^T: elements DPL j + 2i (c0, c1), + 1 (c2, c3) of rows 2t, 2t+1
-        float m[NT][2], mr[NT][2];  // reference of rows 2t, 2t+1; the same with 0 for -inf
-        float l[NT][2];             // this lane's part of the rows' sums
+        // reference of rows 2t, 2t+1; the same with 0 for -inf, less kKv8Lift (after a
+        // range's first chunk the accumulators are hardly ever rescaled: kKv8Slack)
+        float m[NT][2], mr[NT][2];
+        float l[NT][2];           // this lane's part of the rows' sums
+        int ev_ref = kKv8MinExp;  // the V exponent that the references suit
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -445,6 +446,8 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
             const float fk = __uint_as_float((sc & 0xffu) << 23);  // 2^ek (byte 0: 0)
             const int evi = kv8_clamp_exp((int)((sc >> 8) & 0xffu) - 127);
             const float ev = (float)evi, inv_v = exp2i(-evi);
+            const bool low = evi < ev_ref - kKv8Span;
+            ev_ref = low ? evi : max(ev_ref, evi);
             const int nv = (sc >> 16) ? 0 : min(kChunk, len - tok0);  // tokens that count
             // rows see every token of the chunk, or masks apply
             const bool masked = nv < kChunk || tok0 + kChunk - 1 > lim_min;
@@ -526,9 +529,11 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                     }
                     top[e & 1] = fmaxf(top[e & 1], s[n][e]);
                 }
-                above |= top[0] > m[n][0] + kSlack || top[1] > m[n][1] + kSlack;
+                above |= top[0] > m[n][0] + kKv8Slack || top[1] > m[n][1] + kKv8Slack;
             }
-            if (__any_sync(kFull, above)) {
+            // (Three tiles, whose registers are all in use: 45.8 us of 5 query tokens with
+            // the hint, 46.5 without; one: 89.1 and 88.8 of 8 sequences of 32768.)
+            if (__builtin_expect(__any_sync(kFull, above) || low, NT < 3)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -537,10 +542,18 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                        const float m_new = fmaxf(m[n][c], mx);
+                        float m_new = fmaxf(m[n][c], mx);
+                        if (low) {  // down to what suits the row's sum so far
+                            float lr = l[n][c];
+                            lr += __shfl_xor_sync(kFull, lr, 4);
+                            lr += __shfl_xor_sync(kFull, lr, 8);
+                            lr += __shfl_xor_sync(kFull, lr, 16);
+                            m_new = fminf(m_new, fmaxf(mx, __log2f(lr) + mr[n][c] + ev));
+                        }
                         // a row that has seen no token yet: reference 0, weights 0
-                        mr[n][c] = m_new == -INFINITY ? 0.f : m_new;
-                        const float alpha = fast_exp2(m[n][c] - mr[n][c]);
+                        const float ref = m_new == -INFINITY ? 0.f : m_new;
+                        mr[n][c] = ref - kKv8Lift;
+                        const float alpha = fast_exp2(m[n][c] - ref);
                         m[n][c] = m_new;
                         l[n][c] *= alpha;
 #pragma unroll

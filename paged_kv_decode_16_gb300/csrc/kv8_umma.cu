@@ -11,6 +11,9 @@
 //   P = 2^(x - m)     two threads a row, half of the tokens each
 //   O = O 2^(m_old - m) + P V     M = 128, N = D, K = tokens
 //
+// A block with a V exponent too far from those before it (kKv8Span, kv8.cuh) takes
+// the last two steps a chunk at a time, each with a reference that suits it.
+//
 // The e4m3 bytes come by plain 16-byte loads into registers, a warp a chunk (its
 // page, scales and length are then the warp's), K's during the softmax of the block
 // before and V's during its last product.  They are converted to fp16, which holds
@@ -44,6 +47,7 @@ constexpr int kBlockChunks = 8;
 constexpr int kBlockTok = kBlockChunks * kChunk;
 // (Four threads a row, in 64 registers each, spill: 86 against 63 us.)
 constexpr int kThreads = 256;
+constexpr int kNoExp = -100;  // below every exponent: no chunk, or none with tokens yet
 constexpr int kParts = kThreads / 128;             // threads a row: each its part of the tokens
 constexpr int kPartChunks = kBlockChunks / kParts;  // ... and of O's columns
 
@@ -59,7 +63,8 @@ struct Layout {
     static constexpr int kOffEnd = kOffV + kCols * kColBytes;
     static constexpr int kOffMax = kOffEnd;                  // [parts][128] floats
     static constexpr int kOffChunk = kOffMax + kParts * 128 * 4;  // [8] ChunkInfo
-    static constexpr int kOffBar = kOffChunk + kBlockChunks * 16;
+    static constexpr int kOffEv = kOffChunk + kBlockChunks * 16;  // [8] V exponents, a byte each
+    static constexpr int kOffBar = kOffEv + kBlockChunks;
     static constexpr int kOffPlan = kOffBar + 32;
     static constexpr int kUsed = kOffPlan + (kKv8SelfPlan + 1) * 4 + 1024;
     // at least 80 KiB: no more CTAs on an SM than its tensor memory serves
@@ -127,13 +132,114 @@ struct Unit {
     }
 };
 
+// What a thread's row has come to.
+struct RowState {
+    float m, mr, l;  // reference, the same less kKv8Lift, this part's sum
+    int ev_ref;
+    uint32_t ph;     // phase of the barrier that the products arrive at
+    bool fail;
+};
+
+// Softmax and O += P V of a block, a chunk at a time.  In a function of its own: it
+// hardly ever runs, and inside the kernel it takes registers from the path that
+// does (64 query tokens of 4 sequences: 56.0 us, against 54.6).  Every thread of the
+// CTA calls it, with S of the block done; on a timeout `fail` is set for all of them.
+template <int D>
+__device__ __noinline__ void chunks_apart(RowState* st, uint8_t* base, uint32_t lane_base,
+                                          uint32_t tmem, float fs, int lim, int cnt, bool fresh) {
+    using Lay = Layout<D>;
+    float* s_sum = reinterpret_cast<float*>(base + Lay::kOffMax);
+    const ChunkInfo* s_chunk = reinterpret_cast<const ChunkInfo*>(base + Lay::kOffChunk);
+    const int8_t* s_ev = reinterpret_cast<const int8_t*>(base + Lay::kOffEv);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar);
+    const uint32_t sb = smem_u32(base);
+    const int tid = threadIdx.x, row = tid & 127, part = tid >> 7;
+    RowState z = *st;
+#pragma unroll 1
+    for (int c = 0; c < cnt && !z.fail; ++c) {
+        const int ev = s_ev[c];
+        if (ev == kNoExp) continue;
+        const bool low = ev < z.ev_ref - kKv8Span;
+        z.ev_ref = low ? ev : max(z.ev_ref, ev);
+        s_sum[part * 128 + row] = z.l;
+        __syncthreads();
+        uint32_t v[16];
+        tmem_ld(lane_base + c * kChunk, v);
+        const float4 ci = *reinterpret_cast<const float4*>(&s_chunk[c]);
+        const int see = min(__float_as_int(ci.w), lim - c * kChunk + 1);
+        const float g = fs * ci.x;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (e < see) mx = fmaxf(mx, __uint_as_float(v[e]));
+        if (see > 0) mx = fmaf(mx, g, ci.y);
+        float m_new = fmaxf(z.m, mx);
+        if (low) {  // down to what suits the row's sum so far
+            float l = 0.f;
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) l += s_sum[x * 128 + row];
+            m_new = fminf(m_new, fmaxf(mx, __log2f(l) + z.mr + ci.y));
+        }
+        float alpha = 1.f;
+        if (m_new > -INFINITY) {  // the row has seen a token
+            alpha = fast_exp2(z.m - m_new);
+            z.m = m_new;
+            z.mr = m_new - kKv8Lift;
+            z.l *= alpha;
+        }
+        // 8 of the 16 tokens a thread
+        float y[8], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = __uint_as_float(part ? v[8 + e] : v[e]);
+            y[e] = 8 * part + e < see ? fast_exp2(fmaf(s, g, ci.y - z.mr)) : 0.f;
+            sum += y[e];
+        }
+        z.l = fmaf(sum, ci.z, z.l);
+        *reinterpret_cast<uint4*>(base + Lay::kOffK + (c >> 2) * Lay::kColBytes +
+                                  swz(row, 2 * (c & 3) + part)) =
+            make_uint4(Cvt<__half>::pack2(y[0], y[1]), Cvt<__half>::pack2(y[2], y[3]),
+                       Cvt<__half>::pack2(y[4], y[5]), Cvt<__half>::pack2(y[6], y[7]));
+        if (!fresh) {
+#pragma unroll 1
+            for (int x = 0; x < D / kParts; x += 8) {
+                const uint32_t at = lane_base + Lay::kColsS + part * (D / kParts) + x;
+                uint32_t o[8];
+                tmem_ld(at, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st(at, o);
+            }
+            tmem_wait_st();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after();
+            umma_f16(tmem + Lay::kColsS,
+                     umma_sdesc(sb + Lay::kOffK, 16, 1024) +
+                         (((c >> 2) * Lay::kColBytes + (c & 3) * 32) >> 4),
+                     umma_sdesc(sb + Lay::kOffV, Lay::kColBytes, 1024) + ((c * kChunk * 128) >> 4),
+                     umma_idesc(kRows, D, false, true), !fresh);
+            umma_commit(bar);
+        }
+        const bool done = mbar_wait_bounded(bar, z.ph);
+        z.ph ^= 1u;
+        tc_fence_after();
+        z.fail = __syncthreads_or(!done);
+        fresh = false;
+    }
+    *st = z;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
 kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __restrict__ k_pool,
                 const uint8_t* __restrict__ v_pool) {
     using Lay = Layout<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr float kSlack = 8.f;  // as in kv8_decode.cuh
     constexpr int PPR = D / 16;    // 16-byte pieces of a token's e4m3 row
     constexpr int RPP = 32 / PPR, LOADS = kChunk / RPP;  // token rows of a warp's pass; passes
     static_assert(kThreads / 32 == kBlockChunks, "a warp a chunk");
@@ -144,6 +250,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     const uint32_t sb = raw + pad;
     float* s_max = reinterpret_cast<float*>(base + Lay::kOffMax);
     ChunkInfo* s_chunk = reinterpret_cast<ChunkInfo*>(base + Lay::kOffChunk);
+    int8_t* s_ev = reinterpret_cast<int8_t*>(base + Lay::kOffEv);
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + Lay::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
     uint32_t* s_flags = tmem_slot + 1;
@@ -298,6 +405,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     uint32_t ph = 0;
     bool fail = false, in_flight = false;
     float m_run = -INFINITY, mr = 0.f, l_run = 0.f, fs = 0.f;
+    int ev_ref = kNoExp;           // the V exponent that m suits (kv8.cuh)
     int lim_row = 0, lim_min = 0;  // last token that this thread's row, the unit's first row, sees
     Block cur;
     bool more = advance();
@@ -357,6 +465,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
             m_run = -INFINITY;
             mr = 0.f;
             l_run = 0.f;
+            ev_ref = kNoExp;
             const int last = cur.len - p.rows.n_queries;
             lim_min = last + p.rows.first_query(un.sg);
             lim_row = min(last + p.rows.query(un.sg, row), cur.len - 1);
@@ -368,13 +477,16 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         // ---- S = Q K^T of the converted K
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) put(Lay::kOffK, warp * kChunk + rr0 + RPP * i, kr[i]);
+        const int e = kv8_clamp_exp((int)(sc >> 8) - 127), ev = nv > 0 ? e : kNoExp;
         if (lane == 0) {
-            const int e = kv8_clamp_exp((int)(sc >> 8) - 127);
             s_chunk[warp] = {__uint_as_float((sc & 0xffu) << 23), (float)e, exp2i(-e), nv};
+            s_ev[warp] = (int8_t)ev;
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        __syncthreads();
+        // an exponent out of the band that m suits?
+        const bool look =
+            __syncthreads_or(ev != kNoExp && (ev > ev_ref || ev < ev_ref - kKv8Span));
         if (tid == 0) {
             tc_fence_after();
             const uint32_t idesc = umma_idesc(kRows, ntok, false, false);
@@ -404,105 +516,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         if (!mbar_wait_bounded(bar, ph)) fail = true;
         ph ^= 1u;
         tc_fence_after();
-
-        // ---- softmax: this thread's part of row `row`
-        // (twice out of tensor memory, for the maximum and for the weights, a chunk at
-        // a time: beside the next block's bytes there are no registers for more, and
-        // what the compiler moves to local memory instead does not stay in the little
-        // L1 that the shared memory leaves)
-        float mx = -INFINITY;
-        const bool have = part * kPartChunks < cur.cnt;
-        if (!fail && have) {
-#pragma unroll
-            for (int c = 0; c < kPartChunks; ++c) {
-                const int ch = part * kPartChunks + c;
-                if (ch >= cur.cnt) break;
-                uint32_t v[16];
-                tmem_ld(lane_base + ch * kChunk, v);
-                const float4 ci = *reinterpret_cast<const float4*>(&s_chunk[ch]);
-                // tokens of the chunk that the row sees (bad pages: none)
-                const int see = min(__float_as_int(ci.w), lim - ch * kChunk + 1);
-                float top = -INFINITY;
-                if (see >= kChunk) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(v[e]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (e < see) top = fmaxf(top, __uint_as_float(v[e]));
-                }
-                if (see > 0) mx = fmaxf(mx, fmaf(top, fs * ci.x, ci.y));
-            }
-        }
-        s_max[part * 128 + row] = mx;
-        // the warps that share these 32 rows
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(kParts * 32) : "memory");
-#pragma unroll
-        for (int x = 0; x < kParts; ++x) mx = fmaxf(mx, s_max[x * 128 + row]);
-        float alpha = 1.f;
-        if (mx > m_run + kSlack) {
-            mr = mx;  // finite, or +inf (then NaN, as it should be)
-            alpha = fast_exp2(m_run - mr);
-            m_run = mx;
-            l_run *= alpha;
-        }
-        // the products S = Q K^T of the block are done: K's place takes P
-        if (have) {
-#pragma unroll
-            for (int c = 0; c < kPartChunks; ++c) {
-                const int ch = part * kPartChunks + c;
-                if (ch >= cur.cnt) break;
-                uint32_t v[16];
-                float y[16];
-                tmem_ld(lane_base + ch * kChunk, v);
-                const float4 ci = *reinterpret_cast<const float4*>(&s_chunk[ch]);
-                const int see = min(__float_as_int(ci.w), lim - ch * kChunk + 1);
-                const float g = fs * ci.x, off = ci.y - mr;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    y[e] = fast_exp2(fmaf(__uint_as_float(v[e]), g, off));
-                if (see < kChunk) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (e >= see) y[e] = 0.f;
-                }
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) sum += y[e];
-                l_run = fmaf(sum, ci.z, l_run);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float* w = y + 8 * q;
-                    *reinterpret_cast<uint4*>(base + Lay::kOffK + (ch >> 2) * Lay::kColBytes +
-                                              swz(row, 2 * (ch & 3) + q)) =
-                        make_uint4(Cvt<__half>::pack2(w[0], w[1]), Cvt<__half>::pack2(w[2], w[3]),
-                                   Cvt<__half>::pack2(w[4], w[5]), Cvt<__half>::pack2(w[6], w[7]));
-                }
-            }
-        }
-        // the earlier blocks' O to the new reference: its part of the columns a thread
-        if (!cur.first && __any_sync(kFull, alpha != 1.f)) {
-#pragma unroll
-            for (int x = 0; x < D / kParts; x += 16) {
-                const uint32_t at = lane_base + Lay::kColsS + part * (D / kParts) + x;
-                uint32_t v[16];
-                tmem_ld(at, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                tmem_st(at, v);
-            }
-            tmem_wait_st();
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        // A NaN in V at a token that some row does not see must not reach that row
-        // through its weight 0: such a block is multiplied without its NaNs, and
-        // below they are given back to the rows that see them.
-        const int state = __syncthreads_or((fail ? 1 : 0) | (nan != 0u ? 2 : 0));
-        const bool fix = masked && state && __syncthreads_or(nan != 0u);
-        if (__builtin_expect(state != 0, 0) && __syncthreads_or(fail)) break;
-        if (more && !fix) fetch_v();
-        // ---- O += P V
+        // D (+)= P V
         auto product = [&](uint32_t d, bool keep) {
             tc_fence_after();
             const uint32_t idesc = umma_idesc(kRows, D, false, true);
@@ -515,10 +529,138 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
                              vd + ((kt * kChunk * 128) >> 4), idesc, keep || kt > 0);
             umma_commit(bar);
         };
-        if (tid == 0) product(tmem + Lay::kColsS, !cur.first);
-        if (!mbar_wait_bounded(bar, ph)) fail = true;
-        ph ^= 1u;
-        tc_fence_after();
+        bool apart = false;  // too far from each other, or all below ev_ref's band
+        if (look) {
+            int hi = ev_ref, lo = kKv8MaxExp;
+#pragma unroll
+            for (int c = 0; c < kBlockChunks; ++c) {
+                const int x = s_ev[c];
+                hi = max(hi, x);
+                if (c < cur.cnt && x != kNoExp) lo = min(lo, x);
+            }
+            apart = lo < hi - kKv8Span;
+            if (!apart) ev_ref = hi;
+        }
+        bool fix = false;
+        if (__builtin_expect(apart, 0)) {
+            if (__syncthreads_or(fail)) break;
+            fix = masked && __syncthreads_or(nan != 0u);
+            RowState z = {m_run, mr, l_run, ev_ref, ph, false};
+            chunks_apart<D>(&z, base, lane_base, tmem, fs, lim, cur.cnt, cur.first);
+            m_run = z.m;
+            mr = z.mr;
+            l_run = z.l;
+            ev_ref = z.ev_ref;
+            ph = z.ph;
+            fail = z.fail;
+            if (fail) break;
+            if (more && !fix) fetch_v();
+        } else {
+            // ---- softmax: this thread's part of row `row`
+            // (twice out of tensor memory, for the maximum and for the weights, a chunk at
+            // a time: beside the next block's bytes there are no registers for more, and
+            // what the compiler moves to local memory instead does not stay in the little
+            // L1 that the shared memory leaves)
+            float mx = -INFINITY;
+            const bool have = part * kPartChunks < cur.cnt;
+            if (!fail && have) {
+#pragma unroll
+                for (int c = 0; c < kPartChunks; ++c) {
+                    const int ch = part * kPartChunks + c;
+                    if (ch >= cur.cnt) break;
+                    uint32_t v[16];
+                    tmem_ld(lane_base + ch * kChunk, v);
+                    const float4 ci = *reinterpret_cast<const float4*>(&s_chunk[ch]);
+                    // tokens of the chunk that the row sees (bad pages: none)
+                    const int see = min(__float_as_int(ci.w), lim - ch * kChunk + 1);
+                    float top = -INFINITY;
+                    if (see >= kChunk) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e < see) top = fmaxf(top, __uint_as_float(v[e]));
+                    }
+                    if (see > 0) mx = fmaxf(mx, fmaf(top, fs * ci.x, ci.y));
+                }
+            }
+            s_max[part * 128 + row] = mx;
+            // the warps that share these 32 rows
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(kParts * 32) : "memory");
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) mx = fmaxf(mx, s_max[x * 128 + row]);
+            float alpha = 1.f;
+            if (mx > m_run + kKv8Slack) {
+                mr = mx - kKv8Lift;  // finite, or +inf (then NaN, as it should be)
+                alpha = fast_exp2(m_run - mx);
+                m_run = mx;
+                l_run *= alpha;
+            }
+            // the products S = Q K^T of the block are done: K's place takes P
+            if (have) {
+#pragma unroll
+                for (int c = 0; c < kPartChunks; ++c) {
+                    const int ch = part * kPartChunks + c;
+                    if (ch >= cur.cnt) break;
+                    uint32_t v[16];
+                    float y[16];
+                    tmem_ld(lane_base + ch * kChunk, v);
+                    const float4 ci = *reinterpret_cast<const float4*>(&s_chunk[ch]);
+                    const int see = min(__float_as_int(ci.w), lim - ch * kChunk + 1);
+                    const float g = fs * ci.x, off = ci.y - mr;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = fast_exp2(fmaf(__uint_as_float(v[e]), g, off));
+                    if (see < kChunk) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e >= see) y[e] = 0.f;
+                    }
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum += y[e];
+                    l_run = fmaf(sum, ci.z, l_run);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float* w = y + 8 * q;
+                        *reinterpret_cast<uint4*>(base + Lay::kOffK + (ch >> 2) * Lay::kColBytes +
+                                                  swz(row, 2 * (ch & 3) + q)) =
+                            make_uint4(
+                                Cvt<__half>::pack2(w[0], w[1]), Cvt<__half>::pack2(w[2], w[3]),
+                                Cvt<__half>::pack2(w[4], w[5]), Cvt<__half>::pack2(w[6], w[7]));
+                    }
+                }
+            }
+            // the earlier blocks' O to the new reference: its part of the columns a thread
+            if (!cur.first && __any_sync(kFull, alpha != 1.f)) {
+#pragma unroll
+                for (int x = 0; x < D / kParts; x += 16) {
+                    const uint32_t at = lane_base + Lay::kColsS + part * (D / kParts) + x;
+                    uint32_t v[16];
+                    tmem_ld(at, v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                    tmem_st(at, v);
+                }
+                tmem_wait_st();
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            // A NaN in V at a token that some row does not see must not reach that row
+            // through its weight 0: such a block is multiplied without its NaNs, and
+            // below they are given back to the rows that see them.
+            const int state = __syncthreads_or((fail ? 1 : 0) | (nan != 0u ? 2 : 0));
+            fix = masked && state && __syncthreads_or(nan != 0u);
+            if (__builtin_expect(state != 0, 0) && __syncthreads_or(fail)) break;
+            if (more && !fix) fetch_v();
+            // ---- O += P V
+            if (tid == 0) product(tmem + Lay::kColsS, !cur.first);
+            if (!mbar_wait_bounded(bar, ph)) fail = true;
+            ph ^= 1u;
+            tc_fence_after();
+        }
         if (fix) {
             // which outputs see a NaN: (row sees token) x (NaN at token), counted
             // in S's place
