@@ -335,7 +335,15 @@ struct DecodeParams {
 
 // Launch a kernel on `stream` with programmatic stream serialization, so that
 // it can be scheduled while the previous kernel of the stream finishes; every
-// kernel of this library calls pdl_wait() before touching global memory.
+// kernel of this library calls pdl_wait() before it touches what that one may write or
+// still read.  For most that is global memory altogether; the merges and the prefix
+// pass first read what a plan has left (plans let the next kernel start only by
+// completing), and the 8-bit attention kernels of a step work their ranges out: the
+// append in front of them lets them start only behind its own wait, so all that came
+// before it is done, and it writes neither the lengths nor the ranges' place in the
+// workspace.  What the kernel in front may still write comes by ordinary or L2 loads
+// behind the wait: the read-only path wants data that nobody writes while the kernel
+// is resident.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args... args) {

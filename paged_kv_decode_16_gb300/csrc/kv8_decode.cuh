@@ -105,7 +105,7 @@ struct Kv8Stream {
             const int blk = (page * p.n_kv_heads + uidx / p.sub_groups) * p.chunks_per_page +
                             (d.k - col * p.chunks_per_page);
             d.row = blk * kChunk;  // below 2^31: checked on the host
-            d.sc = (uint32_t)__ldg(p.scales + blk);
+            d.sc = (uint32_t)p.scales[blk];  // (an append may write it before the wait)
         } else {
             flags |= PKV_DEV_BAD_PAGE;
         }

@@ -14,7 +14,7 @@
 // A block with a V exponent too far from those before it (kKv8Span, kv8.cuh) takes
 // the last two steps a chunk at a time, each with a reference that suits it.
 //
-// The e4m3 bytes come by plain 16-byte loads into registers, a warp a chunk (its
+// The e4m3 bytes come by 16-byte loads from L2 into registers, a warp a chunk (its
 // page, scales and length are then the warp's), K's during the softmax of the block
 // before and V's during its last product.  They are converted to fp16, which holds
 // them exactly, and stored in the 128-byte swizzled layout that the tensor cores
@@ -236,8 +236,8 @@ __device__ __noinline__ void chunks_apart(RowState* st, uint8_t* base, uint32_t 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
-kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __restrict__ k_pool,
-                const uint8_t* __restrict__ v_pool) {
+kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool,
+                const uint8_t* v_pool) {
     using Lay = Layout<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int PPR = D / 16;    // 16-byte pieces of a token's e4m3 row
@@ -348,7 +348,9 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
     // A warp brings one chunk of a block: lane (rr, pc) the pieces pc of token rows
     // rr + RPP i, K's and V's at different times (the L1 that the shared memory
     // leaves holds the lines of about one side of two CTAs on the way; more loads
-    // wait for room).  The page id of its chunk of the block after is asked for at
+    // wait for room), past L1, which has no use for them (16 query tokens of 32
+    // sequences: 83.6 us, through L1 84.4).  The page id of its chunk of the block
+    // after is asked for at
     // the same time, so that no load waits for another one inside a segment.
     const int lane = tid & 31, pc = lane % PPR, rr0 = lane / PPR;
     uint4 kr[LOADS], vr[LOADS];
@@ -364,7 +366,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
         for (int i = 0; i < LOADS; ++i) {
             v[i] = make_uint4(0u, 0u, 0u, 0u);  // rows behind the sequence's end
             if (rr0 + RPP * i < nv)
-                v[i] = __ldg(reinterpret_cast<const uint4*>(pool + at + i * (RPP * D)));
+                v[i] = __ldcg(reinterpret_cast<const uint4*>(pool + at + i * (RPP * D)));
         }
     };
     auto fetch_k = [&](const Block& c) {
@@ -380,7 +382,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* __rest
                     (long long)(page * p.n_kv_heads + c.h) * p.chunks_per_page +
                     (k - kv8_page_col(k, p.page_magic) * p.chunks_per_page);
                 at = blk * (kChunk * D) + rr0 * D + pc * 16;
-                sc = (uint32_t)__ldg(p.scales + blk);
+                sc = (uint32_t)p.scales[blk];
             } else {
                 flags |= PKV_DEV_BAD_PAGE;
             }
