@@ -225,10 +225,9 @@ __device__ __noinline__ void chunks_apart(RowState* st, uint8_t* base, uint32_t 
                      umma_idesc(kRows, D, false, true), !fresh);
             umma_commit(bar);
         }
-        const bool done = mbar_wait_bounded(bar, z.ph);
-        z.ph ^= 1u;
+        z.fail = __syncthreads_or(!mbar_wait_bounded(bar, z.ph));
+        if (!z.fail) z.ph ^= 1u;
         tc_fence_after();
-        z.fail = __syncthreads_or(!done);
         fresh = false;
     }
     *st = z;
@@ -405,10 +404,18 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
     };
 
     uint32_t ph = 0;
-    bool fail = false, in_flight = false;
+    bool fail = false;  // a wait gave up: the same for the whole CTA
     float m_run = -INFINITY, mr = 0.f, l_run = 0.f, fs = 0.f;
     int ev_ref = kNoExp;           // the V exponent that m suits (kv8.cuh)
     int lim_row = 0, lim_min = 0;  // last token that this thread's row, the unit's first row, sees
+    // Wait for the products in flight; true: given up.  Every thread learns the same, so
+    // nobody touches what products may still use after anybody gave up.
+    auto wait_all = [&]() -> bool {
+        const bool late = __syncthreads_or(!mbar_wait_bounded(bar, ph));
+        if (!late) ph ^= 1u;
+        tc_fence_after();
+        return late;
+    };
     Block cur;
     bool more = advance();
     if (more) {
@@ -501,7 +508,6 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             }
             umma_commit(bar);
         }
-        in_flight = true;
         // ---- beside it: V converted (its place is free, the product before is done)
         uint32_t nan = 0u;
 #pragma unroll
@@ -515,9 +521,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
         }
         more = advance();
         if (more) fetch_k(nx);  // comes behind the product and the softmax
-        if (!mbar_wait_bounded(bar, ph)) fail = true;
-        ph ^= 1u;
-        tc_fence_after();
+        fail = wait_all();
+        if (fail) break;
         // D (+)= P V
         auto product = [&](uint32_t d, bool keep) {
             tc_fence_after();
@@ -545,7 +550,6 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
         }
         bool fix = false;
         if (__builtin_expect(apart, 0)) {
-            if (__syncthreads_or(fail)) break;
             fix = masked && __syncthreads_or(nan != 0u);
             RowState z = {m_run, mr, l_run, ev_ref, ph, false};
             chunks_apart<D>(&z, base, lane_base, tmem, fs, lim, cur.cnt, cur.first);
@@ -565,7 +569,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             // L1 that the shared memory leaves)
             float mx = -INFINITY;
             const bool have = part * kPartChunks < cur.cnt;
-            if (!fail && have) {
+            if (have) {
 #pragma unroll
                 for (int c = 0; c < kPartChunks; ++c) {
                     const int ch = part * kPartChunks + c;
@@ -653,20 +657,16 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             // A NaN in V at a token that some row does not see must not reach that row
             // through its weight 0: such a block is multiplied without its NaNs, and
             // below they are given back to the rows that see them.
-            const int state = __syncthreads_or((fail ? 1 : 0) | (nan != 0u ? 2 : 0));
-            fix = masked && state && __syncthreads_or(nan != 0u);
-            if (__builtin_expect(state != 0, 0) && __syncthreads_or(fail)) break;
+            fix = __syncthreads_or(nan != 0u);  // (looked for in masked blocks only)
             if (more && !fix) fetch_v();
             // ---- O += P V
             if (tid == 0) product(tmem + Lay::kColsS, !cur.first);
-            if (!mbar_wait_bounded(bar, ph)) fail = true;
-            ph ^= 1u;
-            tc_fence_after();
+            fail = wait_all();
+            if (fail) break;
         }
         if (fix) {
             // which outputs see a NaN: (row sees token) x (NaN at token), counted
             // in S's place
-            if (__syncthreads_or(fail)) break;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) put(Lay::kOffV, warp * kChunk + rr0 + RPP * i, nan_ones(vr[i]));
 #pragma unroll
@@ -686,10 +686,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             tc_fence_before();
             __syncthreads();
             if (tid == 0) product(tmem, false);
-            if (!mbar_wait_bounded(bar, ph)) fail = true;
-            ph ^= 1u;
-            tc_fence_after();
-            if (__syncthreads_or(fail)) break;
+            fail = wait_all();
+            if (fail) break;
 #pragma unroll 1
             for (int x = 0; x < D / kParts; x += 8) {
                 uint32_t n[8], v[8];
@@ -705,12 +703,11 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             __syncthreads();
             if (more) fetch_v();
         }
-        in_flight = false;
 
         // ---- the segment's end
         if (cur.last) {
             s_max[part * 128 + row] = l_run;
-            if (__syncthreads_or(fail)) break;
+            __syncthreads();
             float l = 0.f;
 #pragma unroll
             for (int x = 0; x < kParts; ++x) l += s_max[x * 128 + row];
@@ -754,8 +751,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8DecodeParams p, const uint8_t* k_pool
             __syncthreads();
         }
     }
-    if (fail) flags |= PKV_DEV_TIMEOUT;
-    if (fail && in_flight) mbar_wait_bounded(bar, ph ^ 1u);  // products still in flight
+    if (fail) {
+        flags |= PKV_DEV_TIMEOUT;
+        mbar_wait_bounded(bar, ph);  // once more for the products in flight
+    }
     if (flags) atomicOr(s_flags, flags);
     tc_fence_before();
     __syncthreads();
