@@ -107,8 +107,9 @@ def edges(c, q, Q):
         x = c.rng.standard_normal((2, n, c.Hkv, c.D))
         x[0, :, :, 0] = 0.0
         lo = max(0, n - Q - 1)
-        # weight of the last ones together: about that of all the others
-        x[0, lo:, :, 0] = np.log(max(1.0, n / (n - lo + 1.0))) / 3.0 * c.D ** 0.5 if n else 0.0
+        # the same weight for every row, of the last ones together about that of the rest
+        x[0, lo:] = 0.0
+        x[0, lo:, :, 0] = np.log(max(1.0, 2.0 * n / (n - lo + 1.0))) / 3.0 * c.D ** 0.5
         x[1, lo:] += 3.0 * np.sign(x[1, lo:])
         k.append(x[0])
         v.append(x[1])
