@@ -56,7 +56,7 @@ def attention(q, k, v, scales, table, lens, scale, dtype):
             lost = np.minimum(np.minimum(w, 2.0 ** -25), far)
             d_s = np.where(see, size * 2 * D * 2.0 ** -23 + (np.abs(s) * 1.4427 + np.abs(ev[h]).max())
                            * 2.0 ** -22, 0.0)
-            assert (w * d_s).sum(1).max() < 1e-3, "scores too large for a bound that shows anything"
+            assert (w * d_s).sum(1).max() < 4e-3, "scores too large for a bound of a percent"
             rel = d_s + (w * d_s).sum(1, keepdims=True) + 2.0 ** -11 + 2 * n * 2.0 ** -23 + 2.0 ** -18
             a = np.abs(vv[h])
             o = w @ vv[h]
