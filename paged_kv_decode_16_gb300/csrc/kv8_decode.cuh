@@ -347,7 +347,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
         const int u = __shfl_sync(kFull, ws.a.u, i & 31);
         int k0 = __shfl_sync(kFull, ws.a.k, i & 31);
         const int len = __shfl_sync(kFull, ws.a.len, i & 31);
-        const int nch = (len + kChunk - 1) / kChunk;
+        const int nch = len / kChunk + (len % kChunk != 0);  // (len + 15 may pass 32 bits)
         if (!q_coming) fetch_q(i);
         const int end = i + min(nch - k0, ws.n - i);
         for (; k0 < 0 && i < end; ++i, ++k0) release(i);  // cost positions hold nothing
