@@ -838,6 +838,7 @@ def kv8_pool_create(num_pages: int, page_size: int, n_kv_heads: int, head_dim: i
     pool = Pool(h.value, k_pool, v_pool, num_pages, page_size, n_kv_heads, head_dim,
                 torch.float8_e4m3fn)
     pool._keep = (k_pool, v_pool, scales)
+    pool.device = _get_device()
     return pool
 
 
@@ -862,6 +863,8 @@ def _kv8_new_rows(pool, k_new, v_new, page_table, positions, seq_ids, dev_status
         _dtype_code(k_new)
         _kv8_explain((v_new, "v_new", k_new.dtype, 3), (page_table, "page_table", _I32, 2),
                      (positions, "positions", _I32, 1))
+    if pool.device != dev:
+        raise ValueError(f"pool is on cuda:{pool.device} but k_new is on cuda:{dev}")
     dt = _DT[k_new.dtype]
     N = positions.shape[0]
     if k_new.shape != (N, pool.n_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
