@@ -49,7 +49,9 @@ __host__ __device__ __forceinline__ int kv8_clamp_exp(int e) {
 // ev_ref: m <= (the row's largest s) + ev_ref.  A block whose ev is larger moves ev_ref
 // up; one whose ev is more than `span` below it moves m down first, to log2 of the row's
 // sum of 2^s, + ev.  Either way a weight has all 11 bits down to 2^-14 of the row's sum,
-// wherever the scales lie.  The fp32 sums cannot overflow by it: the row's l becomes
+// wherever the scales lie.  (One block of 16 tokens in 16 of a 2^20 times larger
+// scale: 32 sequences of 512 to 4096 tokens 28.0 us instead of 27.0, with 5 query tokens
+// 50.9 instead of 46.2.)  The fp32 sums cannot overflow by it: the row's l becomes
 // 2^(lift - ev), at most 2^67, and o / l is a mean of values, at most 2^49.
 constexpr float kKv8Slack = 8.f;
 constexpr float kKv8Lift = 7.f;
@@ -127,12 +129,13 @@ constexpr int kKv8RowCtas = 512;
 
 // Workers whose parts of one unit are merged by their CTA before they leave it:
 // `most` (a CTA's, or 1 where a worker is a CTA) when units are few beside the
-// workers (nw); else 1, none are.  Merging costs the decode kernel 1.5 us at its end
-// (32 sequences of 512 to 4096 tokens, 7 workers a unit: 23.6 against 22.1 us); one
-// sequence of 32768 tokens (228 a unit) gains more in the combine (23.4 us both
-// together against 24.4, and 15.2 against 18.7 with one KV head), and so do several
-// query tokens, whose states are large (5 query tokens: 4 sequences of 1000 to 8192
-// tokens, 38 workers a unit, 25.7 against 29.8; 8, 19 a unit, 30.6 against 33.0).
+// workers (nw); else 1, none are.  us of a call, decode and combine together, none
+// merged / all merged, 32/8 heads of 128: 32 sequences of 512 to 4096 tokens (7 workers a
+// unit) 26.9 / 26.6, with 5 query tokens 46.2 / 48.8; 16 of them (14) 21.2 / 21.7, 8 (28)
+// 14.5 / 14.9; 256 of 16 to 8192, 28/4 heads, 66.4 / 67.5.  Large states and many workers
+// gain: 5 query tokens of 8 sequences of 1000 to 8192 (19 a unit) 33.7 / 31.5, of 4 (38)
+// 33.1 / 26.5, 8 of 4 (19) 39.8 / 32.4; one sequence of 32768 (228) 24.2 / 22.9, with one
+// KV head 28.2 / 20.1.
 __host__ __device__ __forceinline__ int kv8_merge_warps(int units, int nw, int most) {
     return nw / 16 > units ? most : 1;
 }

@@ -30,7 +30,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDepth = 2;   // tasks of a warp whose rows are on the way
 constexpr int kVecs = 8;    // 16-byte vectors a lane holds of a task's rows
-constexpr int kSlots = 2 * 152;  // CTAs that run at the same time
+constexpr int kSlots = 2 * 152;  // CTAs at the same time: two on each SM of a GB300
 constexpr int kSpan = 16;   // tokens a CTA looks for leaders among
 constexpr int kMaxSpan = kSpan + kChunk - 1;  // tokens it may own
 
@@ -722,11 +722,12 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int head_dim, uint32_t* st
     // each; the rest, or all when they are fewer, share what it holds, twice over:
     // several CTAs to a group, up to a task a warp where every token is a run of its
     // own, behind groups with a CTA each two tasks of a prompt's.  (8 prompts, 32/8 heads
-    // of 128, norm and rotation, us with 1 / 2 / 4 / 8 CTAs to every group: 640 tokens
-    // 29.5 / 16.6 / 10.6 / 9.3; 1500: 29.0 / 17.7 / 14.5 / 15.1; 4200: 34.2 / 28.3 /
-    // 29.9 / 34.9; 8300: 48.4 / 47.1 / 52.2 / 65.5, by this rule 44.1; 17700: 67.6 /
-    // 72.1 / 85.9 / 110.4, 65.9: each forms the angles of its tokens again.  D = 64,
-    // 16/2 heads, 17700: 24.2, 25.7 with fewer tasks a warp.)
+    // of 128, norm and rotation, us with 1 / 2 / 4 / 8 CTAs to every group, and by this
+    // rule: 567 tokens 29.4 / 16.5 / 10.5 / 9.2, 8.5; 1485: 29.2 / 17.9 / 14.9 / 15.5, 15.3;
+    // 4095: 34.3 / 28.9 / 30.7 / 35.0, 29.0; 8192: 48.9 / 47.9 / 53.4 / 65.0, 44.1; 14433:
+    // 68.7 / 73.3 / 88.0 / 109.2, 65.8: each forms the angles of its tokens again.  Of those
+    // 14433, no norm and no rotation: 24.9 / 29.7 / 38.5 / 53.4, 24.8; D = 64, 16/2
+    // heads: 24.1 / 30.3 / 41.4 / 56.7, 24.1.)
     const int groups = a.n_tokens / kSpan + (a.n_tokens % kSpan ? 1 : 0);
     const int alone = groups / kSlots * kSlots, rest = groups - alone;
     const int stretch = kVecs / 2 * (32 / (head_dim / 16));  // q rows of a task

@@ -43,10 +43,10 @@
 // tokens (537 MB): 83.4 us, 95% of the measured copy rate, and 5 more for the
 // combine; 32 of 512 to 4096: 22 us of which about 4 are the start (the ranges, the
 // page ids, the first copies, one after the other) and the uneven end, 77%.  About
-// 310 instructions a chunk and warp (434 with the 16-bit kernel's chunk stream, 57 us
-// for 8 sequences of 16384 against 49.6), 40% of the issue slots, 16% of the tensor
+// 330 instructions a chunk and warp (434 with the 16-bit kernel's chunk stream, 57 us
+// for 8 sequences of 16384 against 50.2), 41% of the issue slots, 16% of the tensor
 // pipe.  Units of 17 to 32 rows: the latency of their longer chunks at 8 warps an
-// SM (5 query tokens, 20 rows: 45 us, 38% of HBM).
+// SM (5 query tokens, 20 rows: 46 us, 37% of HBM).
 #pragma once
 
 #include <cuda.h>

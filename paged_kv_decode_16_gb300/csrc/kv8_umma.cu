@@ -19,7 +19,9 @@
 // before and V's during its last product.  They are converted to fp16, which holds
 // them exactly, and stored in the 128-byte swizzled layout that the tensor cores
 // read; K's place takes P once S is done, so that two CTAs share an SM and one's
-// products run under the other's conversion and softmax.  (Tensor copies would
+// products run under the other's conversion and softmax.  (No place is left for what
+// P's rounding to fp16 leaves, which the warp kernel takes along for fp16 outputs: 64
+// query tokens' error against 64 bits is 2.7e-4 of the norm, there 2.1e-4.)  (Tensor copies would
 // need 32 KiB more for the raw bytes, and leave one CTA an SM.)
 //
 // What bounds it: the chain of a block's phases -- convert, product, maximum,
@@ -28,7 +30,7 @@
 // exponentials (16 a cycle and SM) and as many of products for a block of 128 x
 // 128.  4 sequences of 1000 to 8192 tokens with 64 query tokens, 32/8 heads of 128:
 // 54.3 us with the combine (294 TFLOP/s), against 107 on the warp kernel; the issue
-// slots are 38% busy, the tensor pipe 14%.
+// slots are 40% busy, the tensor pipe 15%.
 //
 // Every wait is bounded: on a timeout the CTA reports PKV_DEV_TIMEOUT, waits
 // (bounded) once more for its products in flight, frees its tensor memory and
@@ -142,8 +144,9 @@ struct RowState {
 
 // Softmax and O += P V of a block, a chunk at a time.  In a function of its own: it
 // hardly ever runs, and inside the kernel it takes registers from the path that
-// does (64 query tokens of 4 sequences: 56.0 us, against 54.6).  Every thread of the
-// CTA calls it, with S of the block done; on a timeout `fail` is set for all of them.
+// does (64 query tokens of 4 sequences: 56.0 us, against 54.6).  With one block of 16
+// tokens in 512 of a 2^20 times larger scale these take 65 us, one in 16: 90.  Every thread
+// of the CTA calls it, with S of the block done; on a timeout `fail` is set for all of them.
 template <int D>
 __device__ __noinline__ void chunks_apart(RowState* st, uint8_t* base, uint32_t lane_base,
                                           uint32_t tmem, float fs, int lim, int cnt, bool fresh) {
