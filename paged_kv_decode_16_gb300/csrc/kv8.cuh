@@ -50,8 +50,8 @@ __host__ __device__ __forceinline__ int kv8_clamp_exp(int e) {
 // up; one whose ev is more than `span` below it moves m down first, to log2 of the row's
 // sum of 2^s, + ev.  Either way a weight has all 11 bits down to 2^-14 of the row's sum,
 // wherever the scales lie.  (One block of 16 tokens in 16 of a 2^20 times larger
-// scale: 32 sequences of 512 to 4096 tokens 28.0 us instead of 27.0, with 5 query tokens
-// 50.9 instead of 46.2.)  The fp32 sums cannot overflow by it: the row's l becomes
+// scale: 32 sequences of 512 to 4096 tokens 27.9 us instead of 26.7, with 5 query tokens
+// 51.4 instead of 46.5.)  The fp32 sums cannot overflow by it: the row's l becomes
 // 2^(lift - ev), at most 2^67, and o / l is a mean of values, at most 2^49.
 constexpr float kKv8Slack = 8.f;
 constexpr float kKv8Lift = 7.f;
@@ -131,7 +131,7 @@ constexpr int kKv8RowCtas = 512;
 // `most` (a CTA's, or 1 where a worker is a CTA) when units are few beside the
 // workers (nw); else 1, none are.  us of a call, decode and combine together, none
 // merged / all merged, 32/8 heads of 128: 32 sequences of 512 to 4096 tokens (7 workers a
-// unit) 26.9 / 26.6, with 5 query tokens 46.2 / 48.8; 16 of them (14) 21.2 / 21.7, 8 (28)
+// unit) 26.9 / 26.6, with 5 query tokens 46.5 / 48.8; 16 of them (14) 21.2 / 21.7, 8 (28)
 // 14.5 / 14.9; 256 of 16 to 8192, 28/4 heads, 66.4 / 67.5.  Large states and many workers
 // gain: 5 query tokens of 8 sequences of 1000 to 8192 (19 a unit) 33.7 / 31.5, of 4 (38)
 // 33.1 / 26.5, 8 of 4 (19) 39.8 / 32.4; one sequence of 32768 (228) 24.2 / 22.9, with one

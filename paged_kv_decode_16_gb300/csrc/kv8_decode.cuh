@@ -46,7 +46,7 @@
 // 330 instructions a chunk and warp (434 with the 16-bit kernel's chunk stream, 57 us
 // for 8 sequences of 16384 against 50.2), 41% of the issue slots, 16% of the tensor
 // pipe.  Units of 17 to 32 rows: the latency of their longer chunks at 8 warps an
-// SM (5 query tokens, 20 rows: 46 us, 37% of HBM).
+// SM (5 query tokens, 20 rows: 46.5 us, 37% of HBM).
 #pragma once
 
 #include <cuda.h>
@@ -531,9 +531,7 @@ kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p,
                 }
                 above |= top[0] > m[n][0] + kKv8Slack || top[1] > m[n][1] + kKv8Slack;
             }
-            // (Three tiles, whose registers are all in use: 45.8 us of 5 query tokens with
-            // the hint, 46.5 without; one: 89.1 and 88.8 of 8 sequences of 32768.)
-            if (__builtin_expect(__any_sync(kFull, above) || low, NT < 3)) {
+            if (__any_sync(kFull, above || low)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
