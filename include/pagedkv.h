@@ -8,8 +8,10 @@
  * rows into the page pool.  Around it: the rotary embedding (with an optional
  * per-head RMS norm) fused into the append, a shared-prefix decode that reads
  * a common prefix once per KV head, several causal query tokens per sequence,
- * a host radix cache of prompt prefixes over the pool, and the append and the
- * attention of a cache held in 8 bits.
+ * a host radix cache of prompt prefixes over the pool, the append and the
+ * attention of a cache held in 8 bits, and a step that attends to selected pages
+ * only (tables built on the GPU, appends of any tokens with every form of the
+ * rotary embedding, page bounds, selection, attention).
  *
  * Where the operations are defined (page title, section):
  *   - CacheIR, "Compiler Example": the decode graph lowers attention into
@@ -97,6 +99,7 @@ typedef enum pkv_dtype {
 #define PKV_DEV_TIMEOUT  0x4u   /* a bounded wait on a copy gave up (copy never landed) */
 #define PKV_DEV_BAD_PREFIX 0x8u /* a table row does not start with the shared prefix's pages */
 #define PKV_DEV_BAD_SEQ 0x10u   /* a sequence id outside [0, n_seqs) was skipped */
+#define PKV_DEV_NO_PAGES 0x20u  /* paged_tables_build: the list of free pages ran out */
 
 typedef struct CUstream_st* pkv_stream; /* same type as cudaStream_t */
 typedef struct pkv_pool pkv_pool;       /* opaque */
@@ -714,6 +717,183 @@ pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int
                                  const void* q_norm_weight, const void* k_norm_weight,
                                  float norm_eps, void* out, void* workspace, size_t ws_bytes,
                                  int num_workers, pkv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Serving with selected pages (16-bit pools).
+ * (CacheIR, "Current Capabilities": persistent page-backed KV pools, batched
+ *  decode over shared page tables; TorchInferno, "Runtime Scaffolds":
+ *  runtime.paged.  The calls below are this library's.)
+ *
+ * One step of a batch, in this order: paged_tables_build (page tables, slots
+ * and positions of the new tokens, on the GPU), kv_append_tokens (rotary
+ * embedding and the write of the new rows), kv_page_bounds (bounds on the keys
+ * of the pages that got rows), paged_select_pages (the pages that each query
+ * attends to) and paged_decode_attention_selected.  Each can be used alone.
+ * All report data errors in dev_status (device, nullable): a uint32 into which
+ * PKV_DEV_* bits are ORed.  All may be captured into CUDA graphs.
+ *
+ * A slot is a row of the pool: page * page_size + row of the page (int64).
+ * ------------------------------------------------------------------------ */
+
+/* For request b of the batch, cached_lens[b] tokens are in the cache and
+ * new_lens[b] are new (both int32 [batch], device).  The new tokens lie end to
+ * end in the batch's token rows: request b's are rows query_starts[b] ..
+ * query_starts[b + 1] - 1.  Pages that they need beyond the ceil(cached /
+ * page_size) that the request has come from free_pages (int32 [n_free_pages],
+ * device), in order from entry *free_begin on (int32, device; NULL: 0), request
+ * by request.  Written (device):
+ *   page_table   int32 [batch][table_stride]: the new pages' entries, no others
+ *   context_lens int32 [batch]: cached + new
+ *   query_starts int32 [batch + 1]
+ *   positions, seq_ids int32 [n_tokens], slots int64 [n_tokens]: each token's
+ *     position in its request, its request and its slot; -1 in all three for the
+ *     rows behind the last request's
+ *   *free_end    int32: free_begin plus the pages taken (not free_begin itself)
+ * A request gets nothing (no pages; context_lens = cached_lens; -1 as position
+ * and slot of its tokens, which keep their rows) when a length is negative or
+ * its tokens do not fit the table row or the n_tokens rows (PKV_DEV_BAD_LEN;
+ * a negative length counts as 0), or when the free pages run out before all
+ * that it needs (PKV_DEV_NO_PAGES); later requests that need no page, or, in
+ * the first case, whose own tokens fit, still get theirs.  A page id outside
+ * [0, num_pages) gives its tokens slot -1 (PKV_DEV_BAD_PAGE).  query_starts
+ * stops at n_tokens.  batch at most 16384 (UNSUPPORTED), outputs must not
+ * overlap inputs or one another (ALIAS).  One launch. */
+pkv_status paged_tables_build(const int32_t* cached_lens, const int32_t* new_lens, int batch,
+                              const int32_t* free_pages, int n_free_pages,
+                              const int32_t* free_begin, int32_t* free_end, int page_size,
+                              int num_pages, int32_t* page_table, int table_stride,
+                              int32_t* context_lens, int32_t* query_starts, int n_tokens,
+                              int32_t* positions, int32_t* seq_ids, int64_t* slots,
+                              uint32_t* dev_status, pkv_stream stream);
+
+/* How frequencies are scaled for contexts longer than the model was trained on
+ * (f_i = theta^(-2i/rotary_dim) before it, s = factor). */
+typedef enum pkv_rope_scaling {
+    PKV_ROPE_NONE = 0,
+    PKV_ROPE_LINEAR = 1, /* f_i / s */
+    PKV_ROPE_TURNS = 2,  /* g f_i + (1 - g) f_i / s, g rising from 0 to 1 while the turns
+                            original_context * f_i / 2 pi go from low_turns to high_turns */
+    PKV_ROPE_INDEX = 3   /* the same with g falling from 1 to 0 over the indexes i from
+                            floor(i(high_turns)) to ceil(i(low_turns)), where i(n) is the (real)
+                            index of n turns; both ends clamped to [0, rotary_dim - 1] */
+} pkv_rope_scaling;
+
+/* A rotary embedding: pair i < rotary_dim / 2 turns by position * f_i radians.
+ * Filled by pkv_rope_init, or by the caller (turns[i]: the fraction of
+ * f_i / 2 pi times 2^64). */
+typedef struct pkv_rope {
+    int32_t rotary_dim;  /* leading elements of a head that turn: a multiple of 16 */
+    int32_t interleaved; /* pair i is elements (2i, 2i + 1); else (i, i + rotary_dim / 2) */
+    float magnitude;     /* multiplies the turned elements (1: a pure rotation) */
+    uint32_t reserved;   /* 0 */
+    uint64_t turns[64];
+} pkv_rope;
+
+/* Fill *out (host).  rotary_dim: a multiple of 16, at most 128; theta, factor,
+ * magnitude finite and > 0; PKV_ROPE_TURNS and _INDEX: 0 < low_turns <
+ * high_turns, original_context > 0, and theta != 1 (_INDEX).  Else INVALID_ARG.
+ * factor is not read with PKV_ROPE_NONE, the last three not with _LINEAR. */
+pkv_status pkv_rope_init(pkv_rope* out, int rotary_dim, double theta, int interleaved,
+                         double magnitude, pkv_rope_scaling scaling, double factor,
+                         double low_turns, double high_turns, double original_context);
+
+/* Append n_tokens new tokens of any requests -- single tokens, prompts, or both
+ * in one batch -- at their slots (int64 [n_tokens], device; < 0: the token is
+ * not written; beyond the pool: PKV_DEV_BAD_PAGE and not written).  k_new, v_new
+ * [n_tokens][n_kv_heads][head_dim] in the pool's dtype, tokens k_stride /
+ * v_stride elements apart, heads contiguous (slices of a fused projection).
+ * Two tokens with one slot leave it with either's rows.
+ *
+ * With rope non-NULL (host), q [n_tokens][n_q_heads][head_dim] (q_stride) is
+ * turned at positions (int32 [n_tokens], device) into q_out (q_out_stride), and
+ * k_new before it is written:
+ *     y_a = m (x_a cos t - x_b sin t),  y_b = m (x_b cos t + x_a sin t)
+ * for each pair (a, b), t = position * f_i, m = magnitude; elements from
+ * rotary_dim on are copied.  A token with position < 0 is skipped whole: its
+ * row of q_out stays as it is.  q may be NULL (n_q_heads 0, q_out NULL): only
+ * keys turn.  q_out may be q (the same address and stride), and rows of q, k_new
+ * and v_new may interleave with its rows.  q_norm_weight / k_norm_weight
+ * [head_dim] (device, nullable, 16-byte aligned): the RMS norm of
+ * kv_append_rope first.  The angle is formed as an exact fraction of a turn;
+ * cos, sin, norm and rotation run in fp32 and are rounded once to the dtype.
+ * rope NULL: k_new is copied bit for bit; q, q_out, positions and the norm
+ * weights must be NULL.
+ *
+ * Strides: multiples of 8 elements, at least a token's heads * head_dim
+ * (INVALID_ARG).  8-bit pool, or rotary_dim above head_dim: UNSUPPORTED.  q_out
+ * or the pools over an input: ALIAS.  n_tokens = 0 launches nothing, else one
+ * launch. */
+pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, const int64_t* slots,
+                            int n_tokens, const void* q, int64_t q_stride, int n_q_heads,
+                            const int32_t* positions, const pkv_rope* rope,
+                            const void* q_norm_weight, const void* k_norm_weight, float norm_eps,
+                            void* q_out, int64_t q_out_stride, uint32_t* dev_status,
+                            pkv_stream stream);
+
+/* The smallest and the largest key, element by element, of every page that
+ * holds one of the slots (int64 [n_tokens], device; < 0 or beyond the pool:
+ * skipped, the latter with PKV_DEV_BAD_PAGE): for the last slot x of each run
+ * of consecutive slots of one page,
+ *     bounds[page][h][0][d] = min over rows r = 0 .. x % page_size of K[page][h][r][d]
+ * and [1] the max.  bounds [num_pages][n_kv_heads][2][head_dim] (device, the
+ * pool's dtype); other pages' are left as they are.  A NaN key gives NaN.  Call
+ * it behind the append of the same slots; a page's tokens have to be one run,
+ * in ascending order, in one call (else the page's bounds are those of one of
+ * its runs).  Rows behind x are not read; a page whose tokens are taken back
+ * keeps its (then wider) bounds until a row of it is written again.  8-bit pool: UNSUPPORTED; bounds over
+ * the pool or the slots: ALIAS.  One launch. */
+pkv_status kv_page_bounds(const pkv_pool* pool, const int64_t* slots, int n_tokens, void* bounds,
+                          uint32_t* dev_status, pkv_stream stream);
+
+/* Bytes of the workspace of paged_select_pages: 12 for each page of the table
+ * and KV head, and a little more.  A workspace serves one call at a time. */
+pkv_status paged_select_workspace_size(int batch, int n_kv_heads, int table_stride, size_t* bytes);
+
+/* The pages that the query of each request attends to, for each KV head h:
+ * with n = ceil(context_lens[b] / page_size) pages, all of them when n <=
+ * max_pages; else the first keep_first, the last keep_last, and of the others
+ * the max_pages - keep_first - keep_last with the highest score
+ *     score_j = max over the query heads of h of
+ *               sum_d max(q_d, 0) hi_j,d + min(q_d, 0) lo_j,d
+ * (lo, hi: kv_page_bounds of the page), which no q . k of the page exceeds.
+ * Equal scores: the lower index first; a NaN score is the highest.  selected
+ * int32 [batch][n_kv_heads][max_pages] (device): the indexes into the request's
+ * table row in ascending order, -1 behind them.  The choice is that of scores
+ * in 64 bits: pages whose 32-bit scores are too close to the border to tell are
+ * scored again in 64.
+ *
+ * q [batch][n_q_heads][head_dim] and bounds in dtype; page_table, context_lens
+ * as for the decode (device).  A page id outside [0, num_pages) scores -inf
+ * (PKV_DEV_BAD_PAGE); a length beyond the table row is clamped and a negative
+ * one is 0 (PKV_DEV_BAD_LEN).  keep_first, keep_last >= 0, their sum at most
+ * max_pages >= 1 (INVALID_ARG); table_stride at most 131072, batch at most
+ * 65535, at most 256 query heads a KV head (UNSUPPORTED).  selected over an
+ * input: ALIAS.  Two launches. */
+pkv_status paged_select_pages(const void* q, const void* bounds, const int32_t* page_table,
+                              int table_stride, const int32_t* context_lens, int batch,
+                              int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                              int num_pages, pkv_dtype dtype, int keep_first, int keep_last,
+                              int max_pages, int32_t* selected, void* workspace, size_t ws_bytes,
+                              uint32_t* dev_status, pkv_stream stream);
+
+/* paged_decode_attention over the listed pages only: query head hq of request
+ * b attends to the tokens t < context_lens[b] of the pages selected[b][h][..]
+ * (indexes into the table row; zeros when there are none).  Negative entries
+ * are skipped; an entry that is not above the one right before it, or not below
+ * ceil(context_lens[b] / page_size), is skipped with PKV_DEV_BAD_LEN.  Lists
+ * come from paged_select_pages or any other rule.  Lengths are clamped to the
+ * table row (PKV_DEV_BAD_LEN), a page id outside the pool is skipped
+ * (PKV_DEV_BAD_PAGE).  max_pages >= 1; num_pages * n_kv_heads * page_size at
+ * most 2^31 - 1 (UNSUPPORTED).  Arithmetic and errors as for
+ * paged_decode_attention; no workspace.  One launch. */
+pkv_status paged_decode_attention_selected(const void* q, const void* k_pool, const void* v_pool,
+                                           const int32_t* page_table, int table_stride,
+                                           const int32_t* context_lens, const int32_t* selected,
+                                           int max_pages, int batch, int n_q_heads,
+                                           int n_kv_heads, int head_dim, int page_size,
+                                           int num_pages, pkv_dtype dtype, float scale, void* out,
+                                           uint32_t* dev_status, pkv_stream stream);
 
 /* Copy the status of the last plan/decode/step call on this workspace to
  * *status_out (host): the OR of the PKV_DEV_* bits of its kernels.  This call

@@ -32,6 +32,9 @@ __all__ = [
     "kv8_pool_create", "kv8_append", "kv8_append_rope", "paged_decode_kv8_workspace_size",
     "alloc_kv8_workspace", "paged_decode_attention_kv8", "paged_decode_attention_multi_kv8",
     "paged_decode_step_kv8", "DEV_BAD_SEQ",
+    "paged_tables_build", "Rope", "kv_append_tokens", "kv_page_bounds",
+    "paged_select_workspace_size", "alloc_select_workspace", "paged_select_pages",
+    "paged_decode_attention_selected", "DEV_NO_PAGES",
     "pkv_read_device_status", "pkv_read_no_alloc_status", "alloc_workspace", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT",
     "VARIANT_AUTO", "VARIANT_CUDA_CORES", "VARIANT_TENSOR_CORES", "VARIANT_TCGEN05",
 ]
@@ -41,7 +44,7 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_ALIAS", 4: "PKV_ERR_OUT_OF_PAGES", 5: "PKV_ERR_WORKSPACE",
                 6: "PKV_ERR_CUDA", 7: "PKV_ERR_DEVICE_CHECK", 8: "PKV_ERR_REFCOUNT"}
 DEV_BAD_PAGE, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_PREFIX = 0x1, 0x2, 0x4, 0x8
-DEV_BAD_SEQ = 0x10
+DEV_BAD_SEQ, DEV_NO_PAGES = 0x10, 0x20
 # decode kernels (pkv_decode_variant)
 VARIANT_AUTO, VARIANT_CUDA_CORES, VARIANT_TENSOR_CORES, VARIANT_TCGEN05 = 0, 1, 2, 3
 # size of the library's fixed device scratch (PKV_NO_ALLOC_SCRATCH_BYTES)
@@ -78,6 +81,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         _build.build()
     lib = ctypes.CDLL(path)
     V, I, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    D, L = ctypes.c_double, ctypes.c_int64
     sig = {
         "pkv_status_string": ([I], ctypes.c_char_p),
         "pkv_version": ([], I),
@@ -135,6 +139,14 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
                                               V, Z, I, V], I),
         "paged_decode_step_kv8": ([V, V, V, V, V, V, V, V, I, V, I, I, I, I, I, I, I, F,
                                    ctypes.c_double, V, V, F, V, V, Z, I, V], I),
+        "paged_tables_build": ([V, V, I, V, I, V, V, I, I, V, I, V, V, I, V, V, V, V, V], I),
+        "pkv_rope_init": ([V, I, D, I, D, I, D, D, D, D], I),
+        "kv_append_tokens": ([V, V, L, V, L, V, I, V, L, I, V, V, V, V, F, V, L, V, V], I),
+        "kv_page_bounds": ([V, V, I, V, V, V], I),
+        "paged_select_workspace_size": ([I, I, I, ctypes.POINTER(Z)], I),
+        "paged_select_pages": ([V, V, V, I, V, I, I, I, I, I, I, I, I, I, I, V, V, Z, V, V], I),
+        "paged_decode_attention_selected": ([V, V, V, V, I, V, V, I, I, I, I, I, I, I, I, F, V, V,
+                                             V], I),
         "pkv_read_device_status": ([V, ctypes.POINTER(ctypes.c_uint32)], I),
         "pkv_read_no_alloc_status": ([ctypes.POINTER(ctypes.c_uint32)], I),
     }
@@ -296,7 +308,10 @@ def kv_pool_create(num_pages: int, page_size: int, n_kv_heads: int, head_dim: in
     _check(load_library().kv_pool_create(num_pages, page_size, n_kv_heads, head_dim, code_dt,
                                          _ptr(k_pool), _ptr(v_pool), ctypes.byref(h)),
            "kv_pool_create")
-    return Pool(h.value, k_pool, v_pool, num_pages, page_size, n_kv_heads, head_dim, dtype)
+    pool = Pool(h.value, k_pool, v_pool, num_pages, page_size, n_kv_heads, head_dim, dtype)
+    # the device of the pool's memory (None: borrowed addresses without a GPU)
+    pool.device = _get_device() if k_pool is not None or torch.cuda.is_available() else None
+    return pool
 
 
 class PrefixCache:
@@ -1058,6 +1073,301 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
         _ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps), out.data_ptr(),
         workspace.data_ptr(), workspace.numel(), int(num_workers), _current(stream, dev)),
         "paged_decode_step_kv8")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Serving with selected pages: tables, appends of any tokens, page bounds, the
+# selection and the attention over it
+# ---------------------------------------------------------------------------
+_I64 = torch.int64
+
+
+def _on(dev, *tensors) -> bool:
+    """Contiguous tensors on device `dev` (None entries pass)."""
+    for t in tensors:
+        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
+def _status_word(dev_status, dev):
+    if dev_status is None:
+        return None
+    if not (dev_status.get_device() == dev and dev_status.dtype is _I32
+            and dev_status.numel() >= 1 and dev_status.is_contiguous()):
+        _dev(dev_status, "dev_status", _I32)
+        raise ValueError("dev_status must hold an int32")
+    return dev_status.data_ptr()
+
+
+def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
+                       free_pages: torch.Tensor, free_begin: torch.Tensor | None,
+                       free_end: torch.Tensor, page_table: torch.Tensor, page_size: int,
+                       num_pages: int, context_lens: torch.Tensor, query_starts: torch.Tensor,
+                       positions: torch.Tensor, seq_ids: torch.Tensor, slots: torch.Tensor,
+                       dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """From the requests' cached and new lengths [B], on the GPU: the entries of
+    their new pages in page_table [B, cols] (taken in order from free_pages,
+    from entry free_begin[0] on; free_end[0] is where the next call goes on),
+    context_lens [B], query_starts [B + 1], and each token row's positions,
+    seq_ids and slots [tokens] (-1 behind the last request's)."""
+    dev = -1
+    try:
+        dev = cached_lens.get_device()
+        ok = (dev >= 0 and _on(dev, cached_lens, new_lens, free_pages, free_begin, free_end,
+                               page_table, context_lens, query_starts, positions, seq_ids, slots)
+              and cached_lens.dtype is _I32 and new_lens.dtype is _I32
+              and free_pages.dtype is _I32 and (free_begin is None or free_begin.dtype is _I32)
+              and free_end.dtype is _I32 and page_table.dtype is _I32
+              and context_lens.dtype is _I32 and query_starts.dtype is _I32
+              and positions.dtype is _I32 and seq_ids.dtype is _I32 and slots.dtype is _I64
+              and page_table.dim() == 2 and cached_lens.dim() == 1 and dev == _get_device())
+    except AttributeError:
+        ok = False
+    if not ok:
+        if free_begin is not None:
+            _dev(free_begin, "free_begin", _I32, 1)
+        _kv8_explain((cached_lens, "cached_lens", _I32, 1), (new_lens, "new_lens", _I32, 1),
+                     (free_pages, "free_pages", _I32, 1), (free_end, "free_end", _I32, 1),
+                     (page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
+                     (query_starts, "query_starts", _I32, 1), (positions, "positions", _I32, 1),
+                     (seq_ids, "seq_ids", _I32, 1), (slots, "slots", _I64, 1))
+    B, cols = page_table.shape
+    N = slots.numel()
+    if (cached_lens.shape[0] != B or new_lens.shape != (B,) or context_lens.shape != (B,)
+            or query_starts.shape != (B + 1,)):
+        raise ValueError("cached_lens, new_lens, context_lens must be [B] and query_starts "
+                         "[B + 1] for page_table [B, cols]")
+    if positions.shape != (N,) or seq_ids.shape != (N,) or slots.dim() != 1:
+        raise ValueError("positions, seq_ids and slots must be [tokens]")
+    if free_end.numel() != 1 or (free_begin is not None and free_begin.numel() != 1):
+        raise ValueError("free_begin and free_end must hold one int32")
+    _check(load_library().paged_tables_build(
+        cached_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
+        _ptr(free_begin), free_end.data_ptr(), int(page_size), int(num_pages),
+        page_table.data_ptr(), cols, context_lens.data_ptr(), query_starts.data_ptr(), N,
+        positions.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(), _status_word(dev_status, dev),
+        _current(stream, dev)), "paged_tables_build")
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "index": 3}
+
+
+class Rope:
+    """A rotary embedding (pkv_rope_init): the leading rotary_dim elements of a
+    head turn, in halves or (interleaved) neighbouring pairs, by position *
+    theta^(-2i / rotary_dim), scaled for long contexts by `scaling` ("none",
+    "linear", "turns" or "index") and `factor`; magnitude multiplies what turns."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, low_turns: float = 1.0,
+                 high_turns: float = 4.0, original_context: float = 8192.0,
+                 magnitude: float = 1.0):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+        self._s = _RopeStruct()
+        self._p = ctypes.addressof(self._s)
+        _check(load_library().pkv_rope_init(
+            self._p, int(rotary_dim), float(theta), int(bool(interleaved)), float(magnitude),
+            ROPE_SCALINGS[scaling], float(factor), float(low_turns), float(high_turns),
+            float(original_context)), "pkv_rope_init")
+
+    @property
+    def rotary_dim(self) -> int:
+        return self._s.rotary_dim
+
+    def turns(self) -> list[float]:
+        """Turns a position of each pair, as fractions of a turn."""
+        return [self._s.turns[i] / 2.0 ** 64 for i in range(self._s.rotary_dim // 2)]
+
+
+def _token_rows(t, name, dev, dtype, tokens, head_dim):
+    """The stride between tokens of t [tokens, heads, head_dim] on `dev`, whose
+    heads are contiguous (a slice of a fused projection may be passed)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != head_dim and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if tokens > 1 else shape[1] * head_dim
+
+
+def _selected_pool(pool):
+    if pool.dtype not in _DT:
+        raise ValueError("pool must be a 16-bit pool (kv_pool_create)")
+
+
+def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
+                     q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                     rope: Rope | None = None, q_out: torch.Tensor | None = None,
+                     q_norm_weight: torch.Tensor | None = None,
+                     k_norm_weight: torch.Tensor | None = None, norm_eps: float = 1e-6,
+                     dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Write k_new / v_new [tokens, Hkv, D] at slots [tokens] (int64, < 0: not
+    written); with a rope, turn q [tokens, Hq, D] at positions [tokens] into
+    q_out and k_new on its way, after the optional per-head RMS norms.  Rows may
+    be slices of a wider tensor; q_out may be q."""
+    _selected_pool(pool)
+    _dev(slots, "slots", _I64, 1)
+    dev = slots.get_device()
+    if pool.device is not None and pool.device != dev:
+        raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
+    dt, N, D, Hkv = pool.dtype, slots.shape[0], pool.head_dim, pool.n_kv_heads
+    ks = _token_rows(k_new, "k_new", dev, dt, N, D)
+    vs = _token_rows(v_new, "v_new", dev, dt, N, D)
+    if k_new.shape[1] != Hkv or v_new.shape[1] != Hkv:
+        raise ValueError("k_new/v_new must be [tokens, Hkv, D] matching the pool")
+    qs = os_ = Hq = 0
+    qp = op = None
+    if rope is None:
+        if q is not None or q_out is not None or positions is not None:
+            raise ValueError("q, q_out and positions need a rope")
+        if q_norm_weight is not None or k_norm_weight is not None:
+            raise ValueError("the norm weights need a rope")
+    else:
+        if positions is None:
+            raise ValueError("a rope needs positions")
+        _dev(positions, "positions", _I32, 1)
+        if positions.shape[0] != N:
+            raise ValueError("positions must have one entry per token")
+        if (q is None) != (q_out is None):
+            raise ValueError("give q and q_out, or neither")
+        if q is not None:
+            qs = _token_rows(q, "q", dev, dt, N, D)
+            os_ = _token_rows(q_out, "q_out", dev, dt, N, D)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            Hq = q.shape[1]
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        if q_norm_weight is not None or k_norm_weight is not None:
+            if q is None and q_norm_weight is not None:
+                raise ValueError("q_norm_weight needs q")
+            _norm_weights(q_norm_weight, k_norm_weight, dt, D)
+    _check(load_library().kv_append_tokens(
+        pool.handle, k_new.data_ptr(), ks, v_new.data_ptr(), vs, slots.data_ptr(), N, qp, qs, Hq,
+        _ptr(positions), None if rope is None else rope._p, _ptr(q_norm_weight),
+        _ptr(k_norm_weight), float(norm_eps), op, os_, _status_word(dev_status, dev),
+        _current(stream, dev)), "kv_append_tokens")
+    return q_out
+
+
+def kv_page_bounds(pool: Pool, slots: torch.Tensor, bounds: torch.Tensor,
+                   dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The smallest and largest key, element by element, of every page that holds
+    one of slots [tokens], into bounds [num_pages, Hkv, 2, D]."""
+    _selected_pool(pool)
+    _dev(slots, "slots", _I64, 1)
+    _dev(bounds, "bounds", pool.dtype, 4)
+    dev = slots.get_device()
+    if pool.device is not None and pool.device != dev:
+        raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
+    if bounds.shape != (pool.num_pages, pool.n_kv_heads, 2, pool.head_dim):
+        raise ValueError("bounds must be [num_pages, Hkv, 2, D] matching the pool")
+    _check(load_library().kv_page_bounds(pool.handle, slots.data_ptr(), slots.shape[0],
+                                         bounds.data_ptr(), _status_word(dev_status, dev),
+                                         _current(stream, dev)), "kv_page_bounds")
+    return bounds
+
+
+def paged_select_workspace_size(batch: int, n_kv_heads: int, table_cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().paged_select_workspace_size(batch, n_kv_heads, table_cols,
+                                                      ctypes.byref(n)),
+           "paged_select_workspace_size")
+    return n.value
+
+
+def alloc_select_workspace(batch: int, n_kv_heads: int, table_cols: int,
+                           device=None) -> torch.Tensor:
+    """A torch uint8 buffer of the size paged_select_pages needs."""
+    n = paged_select_workspace_size(batch, n_kv_heads, table_cols)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _selected_call(q, page_table, context_lens, selected, extra):
+    """(current device, B, Hq, D, table columns, dtype code) of checked arguments;
+    extra: (tensor, name, dtype, ndim) of the call's other tensors."""
+    dev = -1
+    try:
+        dev = q.get_device()
+        ok = (dev >= 0 and dev == _get_device() and _on(dev, q, page_table, context_lens, selected)
+              and q.dim() == 3 and q.dtype in _DT and page_table.dtype is _I32
+              and page_table.dim() == 2 and context_lens.dtype is _I32 and selected.dtype is _I32
+              and selected.dim() == 3)
+        for t, _, dtype, ndim in extra:
+            ok = (ok and t.get_device() == dev and t.is_contiguous() and t.dtype is dtype
+                  and (ndim is None or t.dim() == ndim))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _dev(q, "q", None, 3)
+        _dtype_code(q)
+        _kv8_explain((page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
+                     (selected, "selected", _I32, 3), *extra)
+    B, Hq, D = q.shape
+    if page_table.shape[0] != B or context_lens.shape != (B,) or selected.shape[0] != B:
+        raise ValueError("page_table rows, context_lens or selected != batch")
+    return dev, B, Hq, D, page_table.shape[1], _DT[q.dtype]
+
+
+def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor,
+                       context_lens: torch.Tensor, page_size: int, selected: torch.Tensor,
+                       workspace: torch.Tensor, keep_first: int = 1, keep_last: int = 1,
+                       dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The pages that q [B, Hq, D] attends to, for each KV head: the first
+    keep_first, the last keep_last and those of the highest score by bounds
+    [num_pages, Hkv, 2, D], into selected [B, Hkv, max_pages] (indexes into the
+    rows of page_table, ascending, -1 behind them)."""
+    dev, B, Hq, D, cols, dt = _selected_call(
+        q, page_table, context_lens, selected,
+        ((bounds, "bounds", getattr(q, "dtype", None), 4),
+         (workspace, "workspace", torch.uint8, None)))
+    NP, Hkv, two, D2 = bounds.shape
+    if two != 2 or D2 != D or selected.shape[1] != Hkv:
+        raise ValueError("bounds must be [num_pages, Hkv, 2, D] and selected [B, Hkv, max_pages]")
+    _check(load_library().paged_select_pages(
+        q.data_ptr(), bounds.data_ptr(), page_table.data_ptr(), cols, context_lens.data_ptr(), B,
+        Hq, Hkv, D, int(page_size), NP, dt, int(keep_first), int(keep_last), selected.shape[2],
+        selected.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _status_word(dev_status, dev), _current(stream, dev)), "paged_select_pages")
+    return selected
+
+
+def paged_decode_attention_selected(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                    page_table: torch.Tensor, context_lens: torch.Tensor,
+                                    selected: torch.Tensor, scale: float, out: torch.Tensor,
+                                    dev_status: torch.Tensor | None = None,
+                                    stream=None) -> torch.Tensor:
+    """Decode attention of q [B, Hq, D] over the pages selected[b][h] (indexes into
+    the rows of page_table; negative entries are skipped) into out."""
+    dtype = getattr(q, "dtype", None)
+    dev, B, Hq, D, cols, dt = _selected_call(
+        q, page_table, context_lens, selected,
+        ((k_pool, "k_pool", dtype, 4), (v_pool, "v_pool", dtype, 4), (out, "out", dtype, 3)))
+    NP, Hkv, P, D2 = k_pool.shape
+    if D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape:
+        raise ValueError("q/out [B, Hq, D] and pools [NP, Hkv, P, D] disagree")
+    if selected.shape[1] != Hkv:
+        raise ValueError("selected must be [B, Hkv, max_pages]")
+    _check(load_library().paged_decode_attention_selected(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), cols,
+        context_lens.data_ptr(), selected.data_ptr(), selected.shape[2], B, Hq, Hkv, D, P, NP, dt,
+        float(scale), out.data_ptr(), _status_word(dev_status, dev), _current(stream, dev)),
+        "paged_decode_attention_selected")
     return out
 
 

@@ -22,6 +22,7 @@
 #include "kv8.cuh"
 #include "merge.cuh"
 #include "pool_impl.hpp"
+#include "selected.cuh"
 
 namespace {
 
@@ -640,6 +641,11 @@ pkv_status validate_decode_args(const void* q, const void* k_pool, const void* v
 }
 
 }  // namespace
+
+pkv_status pkv::pool_rows_map(const void* pool, long long rows, int head_dim, pkv_dtype dtype,
+                              CUtensorMap* out) {
+    return pool_map(pool, rows, head_dim, dtype, out);
+}
 
 extern "C" {
 
