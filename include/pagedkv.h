@@ -820,7 +820,8 @@ pkv_status pkv_rope_init(pkv_rope* out, int rotary_dim, double theta, int interl
  * weights must be NULL.
  *
  * Strides: multiples of 8 elements, at least a token's heads * head_dim
- * (INVALID_ARG).  8-bit pool, or rotary_dim above head_dim: UNSUPPORTED.  q_out
+ * (INVALID_ARG).  8-bit pool, rotary_dim above head_dim, or more than 4096 rows a
+ * token (n_q_heads + 2 n_kv_heads): UNSUPPORTED.  q_out
  * or the pools over an input: ALIAS.  n_tokens = 0 launches nothing, else one
  * launch. */
 pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_stride,
@@ -868,8 +869,8 @@ pkv_status paged_select_workspace_size(int batch, int n_kv_heads, int table_stri
  * (PKV_DEV_BAD_PAGE); a length beyond the table row is clamped and a negative
  * one is 0 (PKV_DEV_BAD_LEN).  keep_first, keep_last >= 0, their sum at most
  * max_pages >= 1 (INVALID_ARG); table_stride at most 131072, batch at most
- * 65535, at most 256 query heads a KV head (UNSUPPORTED).  selected over an
- * input: ALIAS.  Two launches. */
+ * 65535, at most 192 query heads a KV head (UNSUPPORTED).  selected over an
+ * input: ALIAS.  One launch for short tables, else two. */
 pkv_status paged_select_pages(const void* q, const void* bounds, const int32_t* page_table,
                               int table_stride, const int32_t* context_lens, int batch,
                               int n_q_heads, int n_kv_heads, int head_dim, int page_size,

@@ -1115,14 +1115,16 @@ def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
     dev = -1
     try:
         dev = cached_lens.get_device()
-        ok = (dev >= 0 and _on(dev, cached_lens, new_lens, free_pages, free_begin, free_end,
-                               page_table, context_lens, query_starts, positions, seq_ids, slots)
-              and cached_lens.dtype is _I32 and new_lens.dtype is _I32
-              and free_pages.dtype is _I32 and (free_begin is None or free_begin.dtype is _I32)
-              and free_end.dtype is _I32 and page_table.dtype is _I32
-              and context_lens.dtype is _I32 and query_starts.dtype is _I32
-              and positions.dtype is _I32 and seq_ids.dtype is _I32 and slots.dtype is _I64
-              and page_table.dim() == 2 and cached_lens.dim() == 1 and dev == _get_device())
+        ok = dev >= 0 and dev == _get_device() and page_table.dim() == 2
+        if ok:
+            for t in (cached_lens, new_lens, free_pages, free_end, page_table, context_lens,
+                      query_starts, positions, seq_ids):
+                if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+                    ok = False
+            ok = (ok and slots.dtype is _I64 and slots.get_device() == dev
+                  and slots.is_contiguous()
+                  and (free_begin is None or (free_begin.dtype is _I32
+                                              and free_begin.get_device() == dev)))
     except AttributeError:
         ok = False
     if not ok:
@@ -1135,11 +1137,11 @@ def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
                      (seq_ids, "seq_ids", _I32, 1), (slots, "slots", _I64, 1))
     B, cols = page_table.shape
     N = slots.numel()
-    if (cached_lens.shape[0] != B or new_lens.shape != (B,) or context_lens.shape != (B,)
-            or query_starts.shape != (B + 1,)):
+    if (cached_lens.numel() != B or new_lens.numel() != B or context_lens.numel() != B
+            or query_starts.numel() != B + 1):
         raise ValueError("cached_lens, new_lens, context_lens must be [B] and query_starts "
                          "[B + 1] for page_table [B, cols]")
-    if positions.shape != (N,) or seq_ids.shape != (N,) or slots.dim() != 1:
+    if positions.numel() != N or seq_ids.numel() != N:
         raise ValueError("positions, seq_ids and slots must be [tokens]")
     if free_end.numel() != 1 or (free_begin is not None and free_begin.numel() != 1):
         raise ValueError("free_begin and free_end must hold one int32")
@@ -1188,7 +1190,7 @@ class Rope:
         return [self._s.turns[i] / 2.0 ** 64 for i in range(self._s.rotary_dim // 2)]
 
 
-def _token_rows(t, name, dev, dtype, tokens, head_dim):
+def _token_rows(t, name, dev, dtype, tokens, heads, head_dim):
     """The stride between tokens of t [tokens, heads, head_dim] on `dev`, whose
     heads are contiguous (a slice of a fused projection may be passed)."""
     if not isinstance(t, torch.Tensor):
@@ -1197,13 +1199,13 @@ def _token_rows(t, name, dev, dtype, tokens, head_dim):
         raise ValueError(f"{name} must be on cuda:{dev}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.shape != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] = "
+                         f"{(tokens, heads, head_dim)}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != head_dim and shape[1] > 1):
+    if s2 != 1 or (s1 != head_dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if tokens > 1 else shape[1] * head_dim
+    return s0 if tokens > 1 else heads * head_dim
 
 
 def _selected_pool(pool):
@@ -1227,10 +1229,8 @@ def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots
     if pool.device is not None and pool.device != dev:
         raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
     dt, N, D, Hkv = pool.dtype, slots.shape[0], pool.head_dim, pool.n_kv_heads
-    ks = _token_rows(k_new, "k_new", dev, dt, N, D)
-    vs = _token_rows(v_new, "v_new", dev, dt, N, D)
-    if k_new.shape[1] != Hkv or v_new.shape[1] != Hkv:
-        raise ValueError("k_new/v_new must be [tokens, Hkv, D] matching the pool")
+    ks = _token_rows(k_new, "k_new", dev, dt, N, Hkv, D)
+    vs = _token_rows(v_new, "v_new", dev, dt, N, Hkv, D)
     qs = os_ = Hq = 0
     qp = op = None
     if rope is None:
@@ -1247,11 +1247,9 @@ def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots
         if (q is None) != (q_out is None):
             raise ValueError("give q and q_out, or neither")
         if q is not None:
-            qs = _token_rows(q, "q", dev, dt, N, D)
-            os_ = _token_rows(q_out, "q_out", dev, dt, N, D)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-            Hq = q.shape[1]
+            Hq = q.shape[1] if q.dim() == 3 else 0
+            qs = _token_rows(q, "q", dev, dt, N, Hq, D)
+            os_ = _token_rows(q_out, "q_out", dev, dt, N, Hq, D)
             qp, op = q.data_ptr(), q_out.data_ptr()
         if q_norm_weight is not None or k_norm_weight is not None:
             if q is None and q_norm_weight is not None:
@@ -1298,30 +1296,35 @@ def alloc_select_workspace(batch: int, n_kv_heads: int, table_cols: int,
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def _selected_call(q, page_table, context_lens, selected, extra):
+def _selected_call(q, page_table, context_lens, selected, others, names):
     """(current device, B, Hq, D, table columns, dtype code) of checked arguments;
-    extra: (tensor, name, dtype, ndim) of the call's other tensors."""
+    others: the call's other tensors, of q's dtype, as named."""
     dev = -1
     try:
         dev = q.get_device()
-        ok = (dev >= 0 and dev == _get_device() and _on(dev, q, page_table, context_lens, selected)
-              and q.dim() == 3 and q.dtype in _DT and page_table.dtype is _I32
-              and page_table.dim() == 2 and context_lens.dtype is _I32 and selected.dtype is _I32
-              and selected.dim() == 3)
-        for t, _, dtype, ndim in extra:
-            ok = (ok and t.get_device() == dev and t.is_contiguous() and t.dtype is dtype
-                  and (ndim is None or t.dim() == ndim))
+        dtype = q.dtype
+        ok = (dev >= 0 and dev == _get_device() and dtype in _DT and q.is_contiguous()
+              and q.dim() == 3 and page_table.dim() == 2 and selected.dim() == 3)
+        if ok:
+            for t in (page_table, context_lens, selected):
+                if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+                    ok = False
+            for t in others:
+                if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                    ok = False
     except AttributeError:
         ok = False
     if not ok:
         _dev(q, "q", None, 3)
         _dtype_code(q)
         _kv8_explain((page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
-                     (selected, "selected", _I32, 3), *extra)
+                     (selected, "selected", _I32, 3),
+                     *((t, n, q.dtype) for t, n in zip(others, names)))
     B, Hq, D = q.shape
-    if page_table.shape[0] != B or context_lens.shape != (B,) or selected.shape[0] != B:
+    rows, cols = page_table.shape
+    if rows != B or context_lens.numel() != B or selected.shape[0] != B:
         raise ValueError("page_table rows, context_lens or selected != batch")
-    return dev, B, Hq, D, page_table.shape[1], _DT[q.dtype]
+    return dev, B, Hq, D, cols, _DT[dtype]
 
 
 def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor,
@@ -1332,16 +1335,20 @@ def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
     keep_first, the last keep_last and those of the highest score by bounds
     [num_pages, Hkv, 2, D], into selected [B, Hkv, max_pages] (indexes into the
     rows of page_table, ascending, -1 behind them)."""
-    dev, B, Hq, D, cols, dt = _selected_call(
-        q, page_table, context_lens, selected,
-        ((bounds, "bounds", getattr(q, "dtype", None), 4),
-         (workspace, "workspace", torch.uint8, None)))
+    dev, B, Hq, D, cols, dt = _selected_call(q, page_table, context_lens, selected, (bounds,),
+                                             ("bounds",))
+    if (workspace.dtype is not torch.uint8 or workspace.get_device() != dev
+            or not workspace.is_contiguous()):
+        _kv8_explain((workspace, "workspace", torch.uint8))
+    _, heads, keep = selected.shape
+    if bounds.dim() != 4:
+        _kv8_explain((bounds, "bounds", q.dtype, 4))
     NP, Hkv, two, D2 = bounds.shape
-    if two != 2 or D2 != D or selected.shape[1] != Hkv:
+    if two != 2 or D2 != D or heads != Hkv:
         raise ValueError("bounds must be [num_pages, Hkv, 2, D] and selected [B, Hkv, max_pages]")
     _check(load_library().paged_select_pages(
         q.data_ptr(), bounds.data_ptr(), page_table.data_ptr(), cols, context_lens.data_ptr(), B,
-        Hq, Hkv, D, int(page_size), NP, dt, int(keep_first), int(keep_last), selected.shape[2],
+        Hq, Hkv, D, int(page_size), NP, dt, int(keep_first), int(keep_last), keep,
         selected.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _status_word(dev_status, dev), _current(stream, dev)), "paged_select_pages")
     return selected
@@ -1354,18 +1361,20 @@ def paged_decode_attention_selected(q: torch.Tensor, k_pool: torch.Tensor, v_poo
                                     stream=None) -> torch.Tensor:
     """Decode attention of q [B, Hq, D] over the pages selected[b][h] (indexes into
     the rows of page_table; negative entries are skipped) into out."""
-    dtype = getattr(q, "dtype", None)
-    dev, B, Hq, D, cols, dt = _selected_call(
-        q, page_table, context_lens, selected,
-        ((k_pool, "k_pool", dtype, 4), (v_pool, "v_pool", dtype, 4), (out, "out", dtype, 3)))
-    NP, Hkv, P, D2 = k_pool.shape
-    if D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape:
+    dev, B, Hq, D, cols, dt = _selected_call(q, page_table, context_lens, selected,
+                                             (k_pool, v_pool, out), ("k_pool", "v_pool", "out"))
+    ks = k_pool.shape
+    if len(ks) != 4:
+        _kv8_explain((k_pool, "k_pool", q.dtype, 4))
+    NP, Hkv, P, D2 = ks
+    _, heads, keep = selected.shape
+    if D2 != D or v_pool.shape != ks or out.shape != q.shape:
         raise ValueError("q/out [B, Hq, D] and pools [NP, Hkv, P, D] disagree")
-    if selected.shape[1] != Hkv:
+    if heads != Hkv:
         raise ValueError("selected must be [B, Hkv, max_pages]")
     _check(load_library().paged_decode_attention_selected(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), cols,
-        context_lens.data_ptr(), selected.data_ptr(), selected.shape[2], B, Hq, Hkv, D, P, NP, dt,
+        context_lens.data_ptr(), selected.data_ptr(), keep, B, Hq, Hkv, D, P, NP, dt,
         float(scale), out.data_ptr(), _status_word(dev_status, dev), _current(stream, dev)),
         "paged_decode_attention_selected")
     return out

@@ -78,17 +78,15 @@ inline size_t pool_bytes(const pkv_pool* p) {
 }
 
 struct SelectLayout {
-    size_t scores, tile_max, total;
-    int tiles;
+    size_t scores, stats, total;
 };
 
 SelectLayout select_layout(int batch, int n_kv_heads, int table_stride) {
     SelectLayout w;
-    w.tiles = (table_stride + pkv::kSelectTile - 1) / pkv::kSelectTile;
     const size_t units = (size_t)batch * n_kv_heads;
     w.scores = align256(units * table_stride * 8);  // the 64-bit scores come first
-    w.tile_max = w.scores + align256(units * table_stride * 4);
-    w.total = w.tile_max + align256(units * w.tiles * 4);
+    w.stats = w.scores + align256(units * table_stride * 4);
+    w.total = w.stats + units * ((table_stride + pkv::kSelectTile - 1) / pkv::kSelectTile) * 16;
     return w;
 }
 
@@ -235,6 +233,8 @@ pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_s
         if ((q_norm_weight || k_norm_weight) && !(norm_eps >= 0.f && isfinite(norm_eps)))
             return PKV_ERR_INVALID_ARG;
     }
+    if ((int64_t)n_q_heads + 2 * (int64_t)pool->n_kv_heads > pkv::kMaxAppendRows)
+        return PKV_ERR_UNSUPPORTED;
     if (n_tokens == 0) return PKV_OK;
     if (!k_new || !v_new || !slots || (rope && !positions)) return PKV_ERR_INVALID_ARG;
     const int64_t kv_row = (int64_t)pool->n_kv_heads * D, q_row = (int64_t)n_q_heads * D;
@@ -379,10 +379,9 @@ pkv_status paged_select_pages(const void* q, const void* bounds, const int32_t* 
     a.keep_last = keep_last;
     a.max_pages = max_pages;
     a.selected = selected;
-    a.scores64 = reinterpret_cast<double*>(ws);
+    a.keys64 = reinterpret_cast<unsigned long long*>(ws);
     a.scores = reinterpret_cast<float*>(ws + w.scores);
-    a.tile_max = reinterpret_cast<uint32_t*>(ws + w.tile_max);
-    a.tiles = w.tiles;
+    a.stats = reinterpret_cast<uint4*>(ws + w.stats);
     a.status = dev_status;
     return cuda_status(pkv::launch_select(a, dtype == PKV_BF16, head_dim,
                                           reinterpret_cast<cudaStream_t>(stream)));

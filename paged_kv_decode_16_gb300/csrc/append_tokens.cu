@@ -6,25 +6,39 @@
 // / 2; interleaved: two neighbouring vectors), so that no lane needs another's elements,
 // and in both layouts the task's eight cosines and sines are those of pairs 8 j .. 8 j +
 // 7.  The D / 16 tasks of a row lie on neighbouring lanes, which is where the optional
-// norm sums its squares.  cos and sin are worked out once a token, into shared memory,
-// behind the loads of the CTA's first tasks.
+// norm sums its squares.
+//
+// A CTA takes groups of up to four tokens.  What a group's tasks share is worked out once,
+// in shared memory, while the group in front of it runs: cosines and sines, and the
+// addresses of every row (a source, and a destination with the row's kind and token in its
+// low bits).  The rows come by asynchronous copies, a few tasks ahead, into places of the
+// thread's own (no barrier).
 //
 // What bounds it: memory, 2 bytes read and 2 written an element.
+#include "packed.cuh"
 #include "selected.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens of a CTA
-constexpr int kBatch = 3;      // tasks of a thread whose loads are in flight together
+constexpr int kCtasPerSm = 4;    // a grid is one wave of them
+constexpr int kAhead = 2;        // a thread's tasks on their way
+constexpr int kMaxTokens = 4;    // tokens of a group (two bits of a destination)
+constexpr int kMaxRows = 1024;   // rows of a group, unless one token has more
 
-template <typename T>
-__device__ __forceinline__ void pack8(const float (&f)[8], uint4& v) {
-    v.x = Cvt<T>::pack2(f[0], f[1]);
-    v.y = Cvt<T>::pack2(f[2], f[3]);
-    v.z = Cvt<T>::pack2(f[4], f[5]);
-    v.w = Cvt<T>::pack2(f[6], f[7]);
+enum Kind { kV = 0, kQ = 1, kK = 2 };  // of a row, the low bits of its destination
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // (x, y) turned by the angle of (c, s).
@@ -34,179 +48,290 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) 
     x = a;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-append_tokens_kernel(const AppendTokensArgs a, int tokens_per_cta) {
-    constexpr int kTasks = D / 16;  // of a row
-    __shared__ __align__(16) float s_cos[kMaxTokens][64];
-    __shared__ __align__(16) float s_sin[kMaxTokens][64];
-    __shared__ long long s_slot[kMaxTokens];
-    __shared__ int s_pos[kMaxTokens];
+struct GroupShape {
+    int tokens;        // of a group
+    int rows;          // of a token: q, k, v
+    uint32_t by_rows;  // 2^32 / rows, rounded up: r / rows for the r of a group
+    int items;         // steps of kThreads tasks
+};
 
-    const int t0 = blockIdx.x * tokens_per_cta;
-    const int nt = min(tokens_per_cta, a.n_tokens - t0);
-    const int rows = a.n_q_heads + 2 * a.n_kv_heads;
-    const int per_token = rows * kTasks;
-    const int n = nt * per_token;
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+append_tokens_kernel(const AppendTokensArgs a, const GroupShape gs) {
+    constexpr int kTasks = D / 16;            // of a row
+    constexpr int kRows = kThreads / kTasks;  // rows of an item
+    __shared__ __align__(16) float s_cos[2][kMaxTokens][64];
+    __shared__ __align__(16) float s_sin[2][kMaxTokens][64];
+    __shared__ __align__(16) float s_w[2][2][D / 2];  // q's and k's norm weights, by vector
+    __shared__ long long s_base[2][kMaxTokens];       // a token's row of head 0 in the pools, or -1
+    __shared__ int s_pos[2][kMaxTokens];
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    uint4* s_ring = reinterpret_cast<uint4*>(s_dyn);  // [kAhead][2][kThreads]
+    const int pad = gs.items * kRows;
+    uint64_t* s_src = reinterpret_cast<uint64_t*>(s_ring + kAhead * 2 * kThreads);  // [3][pad]
+    uint64_t* s_dst = s_src + 3 * pad;                                              // [2][pad]
+
+    const int tid = threadIdx.x;
+    const int groups = (a.n_tokens + gs.tokens - 1) / gs.tokens;
     const bool rope = a.positions != nullptr;
     const bool normed = a.q_norm || a.k_norm;
     const int pairs = rope ? a.rope.rotary_dim >> 1 : 0;
     const int turning = rope ? a.rope.rotary_dim >> 4 : 0;  // tasks of a row that turn
+    const int j = tid % kTasks, row0 = tid / kTasks;        // the thread's place in an item
+    const bool near = a.rope.interleaved || j >= turning;   // its two vectors are neighbours
+    const int v0 = (near ? 2 * j : j) * 8, v1 = (near ? 2 * j + 1 : j + turning) * 8;
+    // tasks on their way: at most one group's, whose addresses are there
+    const bool deep = gs.items >= kAhead;
+    const int depth = deep ? kAhead : gs.items;
 
+    auto row_of = [&](int i, int& tk) {
+        tk = (int)__umulhi((uint32_t)i, gs.by_rows);
+        return i - tk * gs.rows;
+    };
+    auto fill_src = [&](int g, int buf) {
+        for (int i = tid; i < pad; i += kThreads) {
+            int tk;
+            const int r = row_of(i, tk);
+            const long long t = (long long)g * gs.tokens + tk;
+            const T* p = nullptr;
+            if (tk < gs.tokens && t < a.n_tokens) {
+                if (r < a.n_q_heads)
+                    p = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
+                else if (r < a.n_q_heads + a.n_kv_heads)
+                    p = static_cast<const T*>(a.k) + t * a.k_stride + (r - a.n_q_heads) * D;
+                else
+                    p = static_cast<const T*>(a.v) + t * a.v_stride +
+                        (r - a.n_q_heads - a.n_kv_heads) * D;
+            }
+            s_src[buf * pad + i] = reinterpret_cast<uint64_t>(p);
+        }
+    };
+    // What a token's rows go by: its position and its row in the pools.
+    long long tok_slot = -1;
+    int tok_pos = -1;
+    auto read_token = [&](int g) {
+        const long long t = (long long)g * gs.tokens + tid;
+        tok_slot = -1;
+        tok_pos = -1;
+        if (tid < gs.tokens && g < groups && t < a.n_tokens) {
+            tok_slot = a.slots[t];
+            tok_pos = rope ? a.positions[t] : 0;
+        }
+    };
+    auto keep_token = [&](int buf) {
+        if (tid >= gs.tokens) return;
+        if (tok_slot >= a.n_slots) {
+            set_status(a.status, PKV_DEV_BAD_PAGE);
+            tok_slot = -1;
+        }
+        const long long page = tok_slot / a.page_size;
+        s_base[buf][tid] = tok_slot < 0 || tok_pos < 0
+                               ? -1
+                               : (page * a.n_kv_heads * a.page_size +
+                                  (tok_slot - page * a.page_size)) * D;
+        s_pos[buf][tid] = tok_pos;
+    };
+    // Group g's destinations, cosines and sines.
+    auto fill = [&](int g, int buf) {
+        for (int i = tid; i < pad; i += kThreads) {
+            int tk;
+            const int r = row_of(i, tk);
+            uint64_t d = 0;
+            if (tk < gs.tokens) {
+                const long long t = (long long)g * gs.tokens + tk, base = s_base[buf][tk];
+                if (r < a.n_q_heads) {
+                    if (s_pos[buf][tk] >= 0)
+                        d = reinterpret_cast<uint64_t>(static_cast<T*>(a.q_out) +
+                                                       t * a.q_out_stride + r * D);
+                    d |= kQ;
+                } else {
+                    const bool k = r < a.n_q_heads + a.n_kv_heads;
+                    const int head = r - a.n_q_heads - (k ? 0 : a.n_kv_heads);
+                    if (base >= 0)
+                        d = reinterpret_cast<uint64_t>(
+                            static_cast<T*>(k ? a.k_pool : a.v_pool) + base +
+                            (long long)head * (a.page_size * D));
+                    d |= k ? kK : kV;
+                }
+                d |= (uint64_t)tk << 2;
+            }
+            s_dst[buf * pad + i] = d;
+        }
+        if (tid < gs.tokens * pairs) {
+            const int tk = tid / pairs, p = tid - tk * pairs, pos = s_pos[buf][tk];
+            // the turns' product wraps modulo one turn by itself; its top 32 bits as a
+            // signed fraction of half a turn give the angle to 2^-32 turns
+            const uint64_t ph = (uint64_t)(int64_t)pos * a.rope.turns[p];
+            float s, c;
+            sincospif((float)(int)(ph >> 32) * 4.6566128730773926e-10f, &s, &c);
+            s_cos[buf][tk][place<64>(p)] = c * a.rope.magnitude;
+            s_sin[buf][tk][place<64>(p)] = s * a.rope.magnitude;
+        }
+    };
+
+    int load_item = 0, load_buf = 0, stage_in = 0;
+    auto load = [&]() {  // the next task's two vectors, on their way to the thread's place
+        const T* src = reinterpret_cast<const T*>(s_src[load_buf * pad + load_item * kRows + row0]);
+        if (src) {
+            uint4* dst = s_ring + stage_in * 2 * kThreads + tid;
+            copy16(dst, src + v0);
+            copy16(dst + kThreads, src + v1);
+        }
+        copies_commit();
+        if (++load_item == gs.items) {
+            load_item = 0;
+            load_buf = load_buf == 2 ? 0 : load_buf + 1;
+        }
+        if (++stage_in == depth) stage_in = 0;
+    };
+
+    fill_src(blockIdx.x, 0);
+    fill_src(blockIdx.x + gridDim.x, 1);
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x < nt) {
-        long long s = a.slots[t0 + threadIdx.x];
-        const int p = rope ? a.positions[t0 + threadIdx.x] : 0;
-        uint32_t bits = 0;
-        if (s >= a.n_slots) {
-            bits = PKV_DEV_BAD_PAGE;
-            s = -1;
+    read_token(blockIdx.x);
+    if (normed && tid < 2 * kTasks) {
+        const T* w = static_cast<const T*>(tid < kTasks ? a.q_norm : a.k_norm);
+        float f[8], h[8];
+        if (w) {
+            Cvt<T>::unpack8(*reinterpret_cast<const uint4*>(w + v0), f);
+            Cvt<T>::unpack8(*reinterpret_cast<const uint4*>(w + v1), h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s_w[tid / kTasks][0][place<D / 2>(8 * j + e)] = f[e];
+                s_w[tid / kTasks][1][place<D / 2>(8 * j + e)] = h[e];
+            }
         }
-        if (p < 0) s = -1;
-        s_slot[threadIdx.x] = s;
-        s_pos[threadIdx.x] = p;
-        if (bits) set_status(a.status, bits);
     }
+    keep_token(0);
+    __syncthreads();
+    for (int u = 0; u < depth; ++u) load();
+    fill(blockIdx.x, 0);
+    read_token(blockIdx.x + gridDim.x);
+    keep_token(1);
 
-    bool table = false;  // the CTA's cosines and sines are there
-    for (int base = 0; base < n; base += kThreads * kBatch) {
-        uint4 x[kBatch], y[kBatch];
-        int tok[kBatch], row[kBatch], at[kBatch], v0[kBatch], v1[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int task = base + u * kThreads + threadIdx.x;
-            const bool in = task < n;
-            const int tk = in ? task / per_token : 0;
-            const int rem = in ? task - tk * per_token : 0;
-            const int r = rem / kTasks, j = rem % kTasks;
-            tok[u] = in ? tk : -1;
-            row[u] = r;
-            at[u] = j;
-            // the task's two vectors
-            if (a.rope.interleaved || j >= turning) {
-                v0[u] = 2 * j;
-                v1[u] = 2 * j + 1;
-            } else {
-                v0[u] = j;
-                v1[u] = j + turning;
-            }
-            if (!in) continue;
-            const T* src;
-            const long long t = t0 + tk;
-            if (r < a.n_q_heads)
-                src = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
-            else if (r < a.n_q_heads + a.n_kv_heads)
-                src = static_cast<const T*>(a.k) + t * a.k_stride + (r - a.n_q_heads) * D;
-            else
-                src = static_cast<const T*>(a.v) + t * a.v_stride +
-                      (r - a.n_q_heads - a.n_kv_heads) * D;
-            x[u] = *reinterpret_cast<const uint4*>(src + v0[u] * 8);
-            y[u] = *reinterpret_cast<const uint4*>(src + v1[u] * 8);
+    int stage = 0, buf = 0, src_buf = 2;
+    for (int g = blockIdx.x; g < groups; g += gridDim.x, buf ^= 1) {
+        __syncthreads();  // what this group goes by is there; the last group's readers are done
+        const bool more = g + gridDim.x < groups;
+        if (more) {
+            fill_src(g + 2 * gridDim.x, src_buf);
+            src_buf = src_buf == 2 ? 0 : src_buf + 1;
+            fill(g + gridDim.x, buf ^ 1);
+            read_token(g + 2 * gridDim.x);
         }
-        if (!table) {
-            table = true;
-            __syncthreads();
-            for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-                const int tk = i / pairs, p = i - tk * pairs;
-                // the turns' product wraps modulo one turn by itself; its top 32 bits as a
-                // signed fraction of half a turn give the angle to 2^-32 turns
-                const uint64_t ph = (uint64_t)(int64_t)s_pos[tk] * a.rope.turns[p];
-                float s, c;
-                sincospif((float)(int)(ph >> 32) * 4.6566128730773926e-10f, &s, &c);
-                s_cos[tk][p] = c * a.rope.magnitude;
-                s_sin[tk][p] = s * a.rope.magnitude;
-            }
-            __syncthreads();
-        }
+        for (int item = 0; item < gs.items; ++item) {
+            if (deep) copies_wait<kAhead - 1>();
+            else copies_wait<0>();
+            const uint64_t d = s_dst[buf * pad + item * kRows + row0];
+            const int kind = (int)d & 3, tk = (int)(d >> 2) & 3;
+            uint4* ring = s_ring + stage * 2 * kThreads + tid;
+            uint4 x = ring[0], y = ring[kThreads];
+            const bool turn = kind != kV && j < turning;
+            const bool norm = kind == kQ ? a.q_norm != nullptr : kind == kK && a.k_norm != nullptr;
+            if (__any_sync(kFull, turn || norm)) {
+                f2 f[4], h[4];
+                unpack<T>(x, f);
+                unpack<T>(y, h);
+                if (normed) {
+                    f2 sum2 = mul2(f[0], f[0]);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int tk = max(tok[u], 0), r = row[u], j = at[u];
-            const bool is_q = r < a.n_q_heads, is_k = !is_q && r < a.n_q_heads + a.n_kv_heads;
-            const bool turn = (is_q || is_k) && j < turning;
-            const void* norm = is_q ? a.q_norm : (is_k ? a.k_norm : nullptr);
-            float f[8], g[8];
-            if (turn || normed) {
-                Cvt<T>::unpack8(x[u], f);
-                Cvt<T>::unpack8(y[u], g);
-            }
-            if (normed) {  // the same for the whole grid: every lane shuffles
-                float sum = 0.f;
+                    for (int e = 1; e < 4; ++e) sum2 = fma2(f[e], f[e], sum2);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], fmaf(g[e], g[e], sum));
+                    for (int e = 0; e < 4; ++e) sum2 = fma2(h[e], h[e], sum2);
+                    float sum, other;
+                    split_f2(sum2, sum, other);
+                    sum += other;
 #pragma unroll
-                for (int o = kTasks / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-                if (norm) {
-                    const float inv = 1.0f / sqrtf(sum / (float)D + a.eps);
-                    float w[8], z[8];
-                    Cvt<T>::unpack8(reinterpret_cast<const uint4*>(norm)[v0[u]], w);
-                    Cvt<T>::unpack8(reinterpret_cast<const uint4*>(norm)[v1[u]], z);
+                    for (int o = kTasks / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+                    if (norm) {
+                        const float inv = rsqrtf(fmaf(sum, 1.0f / (float)D, a.eps));
+                        const f2 inv2 = make_f2(inv, inv);
+                        f2 w[4];
+                        load8<D / 2>(s_w[kind - 1][0], j, w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f[e] = f[e] * inv * w[e];
-                        g[e] = g[e] * inv * z[e];
+                        for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(f[e], inv2), w[e]);
+                        load8<D / 2>(s_w[kind - 1][1], j, w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = mul2(mul2(h[e], inv2), w[e]);
                     }
                 }
-            }
-            if (turn) {
-                float c[8], s[8];
+                if (turn) {
+                    f2 c[4], s[4];
+                    load8<64>(s_cos[buf][tk], j, c);
+                    load8<64>(s_sin[buf][tk], j, s);
+                    if (a.rope.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[tk][8 * j + e]);
-                    const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[tk][8 * j + e]);
-                    c[e] = c4.x, c[e + 1] = c4.y, c[e + 2] = c4.z, c[e + 3] = c4.w;
-                    s[e] = s4.x, s[e + 1] = s4.y, s[e + 2] = s4.z, s[e + 3] = s4.w;
-                }
-                if (a.rope.interleaved) {
+                        for (int e = 0; e < 4; ++e) {
+                            // elements 2 i and 2 i + 1 are one pair of floats
+                            f2(&z)[4] = e < 2 ? f : h;
+                            float c0, c1, s0, s1, p0, p1, q0, q1;
+                            split_f2(c[e], c0, c1);
+                            split_f2(s[e], s0, s1);
+                            split_f2(z[e % 2 * 2], p0, p1);
+                            split_f2(z[e % 2 * 2 + 1], q0, q1);
+                            turn_pair(p0, p1, c0, s0);
+                            turn_pair(q0, q1, c1, s1);
+                            z[e % 2 * 2] = make_f2(p0, p1);
+                            z[e % 2 * 2 + 1] = make_f2(q0, q1);
+                        }
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        turn_pair(f[2 * e], f[2 * e + 1], c[e], s[e]);
-                        turn_pair(g[2 * e], g[2 * e + 1], c[4 + e], s[4 + e]);
+                        for (int e = 0; e < 4; ++e) {
+                            const f2 z = fma2(f[e], c[e], neg2(mul2(h[e], s[e])));
+                            h[e] = fma2(f[e], s[e], mul2(h[e], c[e]));
+                            f[e] = z;
+                        }
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) turn_pair(f[e], g[e], c[e], s[e]);
+                }
+                if (turn || norm) {
+                    x = pack<T>(f);
+                    y = pack<T>(h);
                 }
             }
-            if (turn || norm) {
-                pack8<T>(f, x[u]);
-                pack8<T>(g, y[u]);
-            }
-            if (tok[u] < 0) continue;
-            T* dst = nullptr;
-            if (is_q) {
-                if (s_pos[tk] >= 0)
-                    dst = static_cast<T*>(a.q_out) + (long long)(t0 + tk) * a.q_out_stride + r * D;
-            } else if (s_slot[tk] >= 0) {
-                const long long slot = s_slot[tk], page = slot / a.page_size;
-                const int h = r - a.n_q_heads - (is_k ? 0 : a.n_kv_heads);
-                const long long to =
-                    ((page * a.n_kv_heads + h) * a.page_size + (slot - page * a.page_size)) * D;
-                dst = static_cast<T*>(is_k ? a.k_pool : a.v_pool) + to;
-            }
+            T* dst = reinterpret_cast<T*>(d & ~15ull);
             if (dst) {
-                *reinterpret_cast<uint4*>(dst + v0[u] * 8) = x[u];
-                *reinterpret_cast<uint4*>(dst + v1[u] * 8) = y[u];
+                *reinterpret_cast<uint4*>(dst + v0) = x;
+                *reinterpret_cast<uint4*>(dst + v1) = y;
             }
+            load();  // into the place just read (behind the last group: nothing)
+            if (++stage == depth) stage = 0;
         }
+        if (more) keep_token(buf);
     }
+    copies_wait<0>();
 }
 
-template <typename T>
-cudaError_t launch(const AppendTokensArgs& a, int head_dim, cudaStream_t stream) {
-    // a CTA a token while that fills the SMs, then up to kMaxTokens
-    int per = (a.n_tokens + 607) / 608;
-    per = per < 1 ? 1 : (per > kMaxTokens ? kMaxTokens : per);
-    const dim3 grid((a.n_tokens + per - 1) / per);
-    return launch_pdl(head_dim == 128 ? append_tokens_kernel<T, 128> : append_tokens_kernel<T, 64>,
-                      grid, dim3(kThreads), 0, stream, a, per);
+template <typename T, int D>
+cudaError_t launch(const AppendTokensArgs& a, cudaStream_t stream) {
+    constexpr int kItemRows = kThreads / (D / 16);
+    const int ctas = kCtasPerSm * sm_count();
+    // a token a CTA while that is one wave, then groups of up to kMaxTokens
+    GroupShape gs;
+    gs.rows = a.n_q_heads + 2 * a.n_kv_heads;
+    gs.tokens = 1 + (a.n_tokens - 1) / ctas;
+    if (gs.tokens > kMaxTokens) gs.tokens = kMaxTokens;
+    while (gs.tokens > 1 && gs.tokens * gs.rows > kMaxRows) --gs.tokens;
+    gs.by_rows = (uint32_t)(((1ull << 32) + gs.rows - 1) / gs.rows);
+    gs.items = (gs.tokens * gs.rows + kItemRows - 1) / kItemRows;
+    const int groups = 1 + (a.n_tokens - 1) / gs.tokens;
+    constexpr int kRing = kAhead * 2 * kThreads * 16;
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(append_tokens_kernel<T, D>),
+                                    kRing + 5 * 8 * (kMaxAppendRows + kItemRows));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(append_tokens_kernel<T, D>, dim3(groups < ctas ? groups : ctas),
+                      dim3(kThreads), kRing + 5 * 8 * gs.items * kItemRows, stream, a, gs);
 }
 
 }  // namespace
 
 cudaError_t launch_append_tokens(const AppendTokensArgs& a, bool bf16, int head_dim,
                                  cudaStream_t stream) {
-    return bf16 ? launch<__nv_bfloat16>(a, head_dim, stream) : launch<__half>(a, head_dim, stream);
+    if (bf16)
+        return head_dim == 128 ? launch<__nv_bfloat16, 128>(a, stream)
+                               : launch<__nv_bfloat16, 64>(a, stream);
+    return head_dim == 128 ? launch<__half, 128>(a, stream) : launch<__half, 64>(a, stream);
 }
 
 }  // namespace pkv

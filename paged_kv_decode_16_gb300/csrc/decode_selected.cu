@@ -10,8 +10,16 @@
 // and the warps' states are merged in shared memory, first within a CTA, then over the
 // cluster through distributed shared memory: no workspace, no second launch.
 //
-// What bounds it: memory, 4 D bytes a token and KV head; a small batch, the latency of
-// list -> table -> rows -> merge.
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that 16 tokens (16 elements
+// of the head) fill the 16 rows of an instruction and 8 query heads its 8 columns: half the
+// instructions of the form with the heads as rows, of which a group of 8 or less leaves
+// half empty.  P^T comes from S^T's accumulators by an 8 x 8 transpose (movmatrix).  P enters
+// in two 16-bit pieces, so that it keeps 16 (bf16) or 22 (fp16) significant bits.
+//
+// What bounds it: memory, 4 D bytes a token and KV head (256 units of 512 tokens, 134 MB:
+// 24 us, 5.6 TB/s, of which 4 are the chain below; 1024 units, 455 MB: 70 us, 6.5 TB/s); a
+// small batch, the latency of list -> table -> rows -> merge (3.4 us) and a warp's chunks one
+// after another (0.6 to 0.7 us each).
 #include <type_traits>
 
 #include "decode_mma.cuh"
@@ -20,39 +28,32 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStages = 3;
 
-template <int D, bool TWO>
+template <int D, int HT, int kWarps, int kStages>
 struct SelLayout {
-    static constexpr int kRows = TWO ? 16 : 8;                  // query rows kept of a tile
+    static constexpr int kRows = 8 * HT;                        // query heads of a unit
     static constexpr int kBoxes = D / 64;
     static constexpr int kBoxBytes = kChunk * 128;
     static constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;  // K boxes, then V boxes
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     // behind the chunks the ring's memory holds the states: o [rows][D] of each warp and of
-    // the CTA, then m and l of each
-    static constexpr int kStateFloats = kRows * D;
-    static constexpr int kOffBar = kRing;
+    // the CTA (rows 16 bytes apart: a warp's stores then meet no bank twice), then m and l
+    static constexpr int kRowFloats = D + 4;
+    static constexpr int kStateFloats = kRows * kRowFloats;
+    static constexpr int kOffBar = kRing > (kWarps + 1) * kStateFloats * 4
+                                       ? kRing : ((kWarps + 1) * kStateFloats * 4 + 15) / 16 * 16;
     static constexpr int kOffML = kOffBar + kWarps * kStages * 8;
     static constexpr int kBytes = kOffML + (kWarps + 1) * 2 * 16 * 4 + 1024;  // + alignment
-    static_assert((kWarps + 1) * kStateFloats * 4 <= kRing, "the states fit the ring");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+// The 8 x 8 matrix of 16-bit values that a warp holds (lane l: row l / 4, columns 2 (l % 4)
+// and the next), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
+
 // The shared-memory address `addr` of this CTA in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -73,13 +74,21 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
     return v;
 }
 
-template <typename T, int D, bool TWO>
+// P in two fp16 pieces, as split_bf16x2: what the first leaves keeps 11 bits more.
+__device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = Cvt<__half>::pack2(a - f.x, b - f.y);
+}
+
+template <typename T, int D, int HT, int kWarps, int kStages>
 __global__ void __launch_bounds__(kWarps * 32)
 selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
-    using Lay = SelLayout<D, TWO>;
+    using Lay = SelLayout<D, HT, kWarps, kStages>;
     constexpr int KSTEPS = D / 16;
-    constexpr int NT = D / 8;
+    constexpr int DT = D / 16;  // tiles of the output
     constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
 
     extern __shared__ uint8_t smem_raw[];
@@ -155,17 +164,18 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     describe(lane, &row_a, &used_a);
     describe(32 + lane, &row_b, &used_b);
 
-    uint32_t qa[KSTEPS][4];  // A fragments of Q (rows g_lo, g_lo + 8)
+    uint32_t qb[HT][KSTEPS][2];  // B fragments of Q^T: heads as columns
     {
         const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + q_row * D);
 #pragma unroll
-        for (int kk = 0; kk < KSTEPS; ++kk) {
-            const int c0 = (kk * 16 + tq) / 2, c1 = c0 + 4;
-            qa[kk][0] = g_lo < rows ? q[g_lo * (D / 2) + c0] : 0u;
-            qa[kk][2] = g_lo < rows ? q[g_lo * (D / 2) + c1] : 0u;
-            qa[kk][1] = TWO && g_lo + 8 < rows ? q[(g_lo + 8) * (D / 2) + c0] : 0u;
-            qa[kk][3] = TWO && g_lo + 8 < rows ? q[(g_lo + 8) * (D / 2) + c1] : 0u;
-        }
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+            for (int kk = 0; kk < KSTEPS; ++kk) {
+                const int at = (8 * ht + g_lo) * (D / 2) + (kk * 16 + tq) / 2;
+                const bool in = 8 * ht + g_lo < rows;
+                qb[ht][kk][0] = in ? q[at] : 0u;
+                qb[ht][kk][1] = in ? q[at + 4] : 0u;
+            }
     }
 
     const uint64_t policy = l2_evict_first_policy();
@@ -192,10 +202,18 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     int issued = 0;
     while (issued < kStages && issued < mine) issue(issued++);
 
-    float o[NT][4];
+    // O^T: rows d = 16 dt + g_lo and + 8, columns heads 8 ht + tq and + 1.  m: the maxima of
+    // those two heads, l: this lane's part of their sums.
+    float o[HT][DT][4];
+    float m[HT][2], l[HT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+            o[ht][dt][0] = o[ht][dt][1] = o[ht][dt][2] = o[ht][dt][3] = 0.f;
+        m[ht][0] = m[ht][1] = -INFINITY;
+        l[ht][0] = l[ht][1] = 0.f;
+    }
     const int mi = lane >> 3, rr = lane & 7;
 
     for (int i = 0; i < mine; ++i) {
@@ -222,66 +240,71 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
                 }
                 __syncwarp();
             }
-            // S = Q K^T: tokens 0 - 7 and 8 - 15, even and odd k-steps in chains of their own
-            float s[2][2][4] = {};
-            const int k_tok = (mi >> 1) * 8 + rr;
+            // S^T = K Q^T: tokens are the rows, even and odd k-steps in chains of their own
+            float s[HT][2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; ++kk) {
-                const int d = kk * 16 + (mi & 1) * 8;
-                uint32_t kb[4];
-                ldsm_x4(kst + (d / 64) * Lay::kBoxBytes + swz128(k_tok, (d % 64) / 8), kb);
-                Mma<T>::run(s[0][kk & 1], qa[kk], kb[0], kb[1]);
-                Mma<T>::run(s[1][kk & 1], qa[kk], kb[2], kb[3]);
+                const int d = kk * 16 + (mi >> 1) * 8;
+                uint32_t ka[4];
+                ldsm_x4(kst + (d / 64) * Lay::kBoxBytes + swz128((mi & 1) * 8 + rr, (d % 64) / 8), ka);
+#pragma unroll
+                for (int ht = 0; ht < HT; ++ht)
+                    Mma<T>::run(s[ht][kk & 1], ka, qb[ht][kk][0], qb[ht][kk][1]);
             }
-            uint32_t pa[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
+            uint32_t pb[HT][2], pl[HT][2];  // B fragments of P^T (and of what its bf16s leave)
 #pragma unroll
-            for (int half = 0; half < (TWO ? 2 : 1); ++half) {
-                float sc[4];
+            for (int ht = 0; ht < HT; ++ht) {
+                float e[4], alpha[2];  // e: (token g_lo, heads tq, tq + 1), (token g_lo + 8, ..)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int a = e >> 1, x = 2 * half + (e & 1);
-                    const int tok = a * 8 + tq + (e & 1);
-                    sc[e] = tok < used ? (s[a][0][x] + s[a][1][x]) * p.scale_log2 : -INFINITY;
+                for (int x = 0; x < 4; ++x) {
+                    const float v = (s[ht][0][x] + s[ht][1][x]) * p.scale_log2;
+                    e[x] = g_lo + (x & 2) * 4 < used ? v : -INFINITY;
                 }
-                float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-                const float m_new = fmaxf(m[half], mx);
-                const float ref = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = fast_exp2(m[half] - ref);
-                float e[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) e[x] = fast_exp2(sc[x] - ref);
-                float sum = (e[0] + e[1]) + (e[2] + e[3]);
-                sum += __shfl_xor_sync(kFull, sum, 1);
-                sum += __shfl_xor_sync(kFull, sum, 2);
-                l[half] = l[half] * alpha + sum;
-                m[half] = m_new;
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(e[c], e[2 + c]);
+                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                    const float m_new = fmaxf(m[ht][c], mx);
+                    const float ref = m_new == -INFINITY ? 0.f : m_new;
+                    alpha[c] = fast_exp2(m[ht][c] - ref);
+                    e[c] = fast_exp2(e[c] - ref);
+                    e[2 + c] = fast_exp2(e[2 + c] - ref);
+                    l[ht][c] = fmaf(l[ht][c], alpha[c], e[c] + e[2 + c]);
+                    m[ht][c] = m_new;
+                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    o[nt][2 * half] *= alpha;
-                    o[nt][2 * half + 1] *= alpha;
+                for (int dt = 0; dt < DT; ++dt) {
+                    o[ht][dt][0] *= alpha[0];
+                    o[ht][dt][1] *= alpha[1];
+                    o[ht][dt][2] *= alpha[0];
+                    o[ht][dt][3] *= alpha[1];
                 }
                 if constexpr (kSplitP) {
-                    split_bf16x2(e[0], e[1], pa[half], pl[half]);
-                    split_bf16x2(e[2], e[3], pa[2 + half], pl[2 + half]);
+                    split_bf16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
+                    split_bf16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
                 } else {
-                    pa[half] = Cvt<T>::pack2(e[0], e[1]);
-                    pa[2 + half] = Cvt<T>::pack2(e[2], e[3]);
+                    split_f16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
+                    split_f16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    pb[ht][x] = transpose8(pb[ht][x]);
+                    pl[ht][x] = transpose8(pl[ht][x]);
                 }
             }
-            // O += P V; P in bf16 as a high part and the rest, two products
-            const int v_tok = (mi & 1) * 8 + rr;
+            // O^T += V^T P^T, P as a high part and the rest: two products
 #pragma unroll
-            for (int np = 0; np < NT / 2; ++np) {
-                const int d = np * 16 + (mi >> 1) * 8;
-                uint32_t vb[4];
-                ldsm_x4_trans(vst + (d / 64) * Lay::kBoxBytes + swz128(v_tok, (d % 64) / 8), vb);
-                Mma<T>::run(o[2 * np], pa, vb[0], vb[1]);
-                Mma<T>::run(o[2 * np + 1], pa, vb[2], vb[3]);
-                if constexpr (kSplitP) {
-                    Mma<T>::run(o[2 * np], pl, vb[0], vb[1]);
-                    Mma<T>::run(o[2 * np + 1], pl, vb[2], vb[3]);
+            for (int dt = 0; dt < DT; ++dt) {
+                const int d = dt * 16 + (mi & 1) * 8;
+                uint32_t va[4];
+                ldsm_x4_trans(vst + (d / 64) * Lay::kBoxBytes + swz128((mi >> 1) * 8 + rr, (d % 64) / 8),
+                              va);
+#pragma unroll
+                for (int ht = 0; ht < HT; ++ht) {
+                    Mma<T>::run(o[ht][dt], va, pb[ht][0], pb[ht][1]);
+                    Mma<T>::run(o[ht][dt], va, pl[ht][0], pl[ht][1]);
                 }
             }
         }
@@ -299,16 +322,24 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     // ---- the warps' states, in the ring's memory (every copy has been waited for) ----
     __syncthreads();
 #pragma unroll
-    for (int half = 0; half < (TWO ? 2 : 1); ++half) {
-        const int g = g_lo + half * 8;
-        float* dst = s_o + warp * Lay::kStateFloats + g * D;
+    for (int ht = 0; ht < HT; ++ht) {
+        const int g = 8 * ht + tq;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            *reinterpret_cast<float2*>(dst + nt * 8 + tq) =
-                make_float2(o[nt][2 * half], o[nt][2 * half + 1]);
-        if ((lane & 3) == 0) {
-            s_m[warp * 32 + g] = m[half];
-            s_m[warp * 32 + 16 + g] = l[half];
+        for (int c = 0; c < 2; ++c) {
+            float* dst = s_o + warp * Lay::kStateFloats + (g + c) * Lay::kRowFloats + g_lo;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                dst[dt * 16] = o[ht][dt][c];
+                dst[dt * 16 + 8] = o[ht][dt][2 + c];
+            }
+            float sum = l[ht][c];
+            sum += __shfl_xor_sync(kFull, sum, 4);
+            sum += __shfl_xor_sync(kFull, sum, 8);
+            sum += __shfl_xor_sync(kFull, sum, 16);
+            if (g_lo == 0) {
+                s_m[warp * 32 + g + c] = m[ht][c];
+                s_m[warp * 32 + 16 + g + c] = sum;
+            }
         }
     }
     __syncthreads();
@@ -327,7 +358,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
         for (int w = 0; w < kWarps; ++w) {
             const float f = weight(s_m[w * 32 + g], top);
             const float4 x =
-                *reinterpret_cast<const float4*>(s_o + w * Lay::kStateFloats + g * D + c);
+                *reinterpret_cast<const float4*>(s_o + w * Lay::kStateFloats + g * Lay::kRowFloats + c);
             sum = fmaf(f, s_m[w * 32 + 16 + g], sum);
             acc.x = fmaf(f, x.x, acc.x);
             acc.y = fmaf(f, x.y, acc.y);
@@ -339,7 +370,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
             *reinterpret_cast<uint2*>(out + g * D + c) = make_uint2(
                 Cvt<T>::pack2(acc.x * inv, acc.y * inv), Cvt<T>::pack2(acc.z * inv, acc.w * inv));
         } else {
-            *reinterpret_cast<float4*>(s_o + kWarps * Lay::kStateFloats + g * D + c) = acc;
+            *reinterpret_cast<float4*>(s_o + kWarps * Lay::kStateFloats + g * Lay::kRowFloats + c) = acc;
             if (c == 0) {
                 s_m[kWarps * 32 + g] = top;
                 s_m[kWarps * 32 + 16 + g] = sum;
@@ -348,7 +379,8 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     }
     if (ranks == 1) return;
     // ---- the CTAs' states: each CTA writes its share of the outputs ----
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     const uint32_t my_o = smem_u32(s_o + kWarps * Lay::kStateFloats);
     const uint32_t my_m = smem_u32(s_m + kWarps * 32);
     for (int z = rank * kWarps * 32 + threadIdx.x; z < rows * (D / 4);
@@ -360,7 +392,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < ranks; ++r) {
             const float f = weight(peer_load(peer_addr(my_m + g * 4, r)), top);
-            const float4 x = peer_load4(peer_addr(my_o + (g * D + c) * 4, r));
+            const float4 x = peer_load4(peer_addr(my_o + (g * Lay::kRowFloats + c) * 4, r));
             sum = fmaf(f, peer_load(peer_addr(my_m + (16 + g) * 4, r)), sum);
             acc.x = fmaf(f, x.x, acc.x);
             acc.y = fmaf(f, x.y, acc.y);
@@ -371,29 +403,20 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
         *reinterpret_cast<uint2*>(out + g * D + c) = make_uint2(
             Cvt<T>::pack2(acc.x * inv, acc.y * inv), Cvt<T>::pack2(acc.z * inv, acc.w * inv));
     }
-    cluster_sync();  // no CTA leaves while another one reads its memory
+    cluster_arrive();
+    cluster_wait();  // no CTA leaves while another one reads its memory
 }
 
-template <typename T, int D, bool TWO>
-cudaError_t launch(const SelectedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                   cudaStream_t stream) {
-    constexpr int kBytes = SelLayout<D, TWO>::kBytes;
-    auto kernel = selected_kernel<T, D, TWO>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+template <typename T, int D, int HT, int kWarps, int kStages>
+cudaError_t launch_clusters(const SelectedParams& p, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, int ranks, cudaStream_t stream) {
+    constexpr int kBytes = SelLayout<D, HT, kWarps, kStages>::kBytes;
+    auto kernel = selected_kernel<T, D, HT, kWarps, kStages>;
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(kernel), kBytes);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-        return e;
-    // CTAs of a unit: a wave of two CTAs an SM, while a warp keeps two chunks
-    const long long units = (long long)p.batch * p.n_kv_heads * p.head_blocks;
-    const long long pages = p.max_pages < p.table_stride ? p.max_pages : p.table_stride;
-    const long long chunks = pages * (p.page_size / kChunk);
-    int ranks = 1;
-    while (ranks < 8 && units * ranks < 2 * sms && chunks >= 2LL * kWarps * 2 * ranks) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * ranks));
+    cfg.gridDim = dim3((unsigned)p.batch * p.n_kv_heads * p.head_blocks * ranks);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = kBytes;
     cfg.stream = stream;
@@ -409,15 +432,44 @@ cudaError_t launch(const SelectedParams& p, const CUtensorMap& kmap, const CUten
     return cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap);
 }
 
+// Up to a CTA an SM, the time is that of a warp's chunks one after another: eight warps a
+// CTA with three stages each (all of an SM's shared memory), and as many CTAs a unit as fit.
+// Beyond it, bytes in flight count, and a second wave costs: four warps with two stages,
+// three CTAs an SM.  us a call, bf16, D 128, group 4, eight warps / four (best cluster size
+// of each): 8 units of 256 chunks 7.7 / 9.4, 64 units 20.0 / 24.6, 152 units 46.2 / 48.9,
+// 192 units 66.5 / 58.5; 152 units of 16 chunks 4.7 / 5.6, 192 units 8.5 / 6.2.
+template <typename T, int D, int HT>
+cudaError_t launch(const SelectedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                   cudaStream_t stream) {
+    const long long units = (long long)p.batch * p.n_kv_heads * p.head_blocks;
+    const int sms = sm_count();
+    if (units > sms) return launch_clusters<T, D, HT, 4, 2>(p, kmap, vmap, 1, stream);
+    const long long pages = p.max_pages < p.table_stride ? p.max_pages : p.table_stride;
+    const long long chunks = pages * (p.page_size / kChunk);
+    // steps of a warp, and the cluster's merge, which costs about as much as one
+    // (8 units of 64 chunks, clusters of 1 / 2 / 4 / 8: 8.9 / 7.0 / 5.6 / 5.3 us; of 16 chunks
+    // 4.4 / 4.8 / 4.9 / 5.2)
+    int ranks = 1;
+    long long best = (chunks + 7) / 8;
+    for (int r = 2; r <= 8 && units * r <= sms; r *= 2) {
+        const long long steps = (chunks + 8 * r - 1) / (8 * r) + 1;
+        if (steps < best) {
+            best = steps;
+            ranks = r;
+        }
+    }
+    return launch_clusters<T, D, HT, 8, 3>(p, kmap, vmap, ranks, stream);
+}
+
 template <typename T>
 cudaError_t pick(const SelectedParams& p, int head_dim, const CUtensorMap& kmap,
                  const CUtensorMap& vmap, cudaStream_t stream) {
     const bool two = p.group > 8;
     if (head_dim == 128)
-        return two ? launch<T, 128, true>(p, kmap, vmap, stream)
-                   : launch<T, 128, false>(p, kmap, vmap, stream);
-    return two ? launch<T, 64, true>(p, kmap, vmap, stream)
-               : launch<T, 64, false>(p, kmap, vmap, stream);
+        return two ? launch<T, 128, 2>(p, kmap, vmap, stream)
+                   : launch<T, 128, 1>(p, kmap, vmap, stream);
+    return two ? launch<T, 64, 2>(p, kmap, vmap, stream)
+               : launch<T, 64, 1>(p, kmap, vmap, stream);
 }
 
 }  // namespace

@@ -109,7 +109,7 @@ cudaError_t launch(const BoundsArgs& a, int head_dim, cudaStream_t stream) {
     // a CTA where a page's tokens stand together
     int tile = kWarps;
     while (tile < kMaxTile && (long long)(a.n_tokens / tile) * a.n_kv_heads > 4096) tile *= 2;
-    const dim3 grid((a.n_tokens + tile - 1) / tile, a.n_kv_heads);
+    const dim3 grid(1 + (a.n_tokens - 1) / tile, a.n_kv_heads);
     return launch_pdl(head_dim == 128 ? page_bounds_kernel<T, 128> : page_bounds_kernel<T, 64>,
                       grid, dim3(kWarps * 32), 0, stream, a, tile);
 }

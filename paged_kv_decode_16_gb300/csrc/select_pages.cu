@@ -12,18 +12,22 @@
 // summed.  A product of two 16-bit values is exact in fp32; each of the 2 D / 16 steps adds 16
 // of them to the sum, every addend cut at 2^-24 of the largest at worst: 17 addends, 2 D /
 // 16 <= 16 steps, so a score is off by at most e = 2^-15 S (S = sum |q_d| max |bound|; the
-// count gives 2^-15.9).  The k-th largest score is then off by at most e too: pages more than 2 e above the
-// k-th fp32 score are chosen, those more than 2 e below are not, and only the few in
-// between are scored again in fp64, where that is not settled by their number.
-#include <type_traits>
-
+// count gives 2^-15.9, the last sum of two chains included).  The k-th largest score is then
+// off by at most e too: pages more than 2 e above the k-th fp32 score are chosen, those more
+// than 2 e below are not, and only the few in between are scored again to more bits, where
+// that is not settled by their number.
 #include "decode_mma.cuh"
 #include "selected.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kScoreWarps = 4;
+constexpr int kScoreThreads = 128;
+constexpr int kPickThreads = 512;
+constexpr int kSmallThreads = 256;  // of the kernel that does both
+constexpr int kFew = 256;           // pages that are ranked by comparing all pairs
+constexpr int kBins = 1024;         // of the histogram that finds the border
+constexpr int kScoreCache = 16384;  // scores kept in shared memory
 
 __device__ __forceinline__ int pages_of(const SelectArgs& a, int b, uint32_t* bits) {
     int len = a.lens[b];
@@ -35,123 +39,23 @@ __device__ __forceinline__ int pages_of(const SelectArgs& a, int b, uint32_t* bi
     return (int)(((long long)len + a.page_size - 1) / a.page_size);
 }
 
-// Largest magnitude of packed 16-bit floats, as bits (NaN above infinity above all).
+// Largest magnitudes of packed 16-bit floats, NaN above all.
+template <typename T>
+struct Abs2;
+template <>
+struct Abs2<__nv_bfloat16> {
+    using V = __nv_bfloat162;
+};
+template <>
+struct Abs2<__half> {
+    using V = __half2;
+};
+template <typename T>
 __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
-    return __vmaxu2(m, x & 0x7fff7fffu);
+    using V = typename Abs2<T>::V;
+    const V r = __hmax2_nan(*reinterpret_cast<const V*>(&m), __habs2(*reinterpret_cast<const V*>(&x)));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a) {
-    constexpr int kSegs = 2 * D / 32;           // 64-byte pieces of a row: two k-steps each
-    constexpr int kRowBytes = 4 * D + 64;       // a query's [q- | q+], rows 64 bytes apart mod 128
-    extern __shared__ __align__(16) uint8_t s_q[];
-    __shared__ uint32_t s_max[kScoreWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x, tile = blockIdx.y, b = blockIdx.z;
-    const int group = a.n_q_heads / a.n_kv_heads;
-    const int rows8 = (group + 7) / 8 * 8;
-    pdl_wait();
-    pdl_trigger();
-    uint32_t bits = 0;
-    const int n = pages_of(a, b, &bits);
-    const int first = tile * kSelectTile;
-    if (bits && h == 0 && tile == 0 && threadIdx.x == 0) set_status(a.status, bits);
-    if (n <= a.max_pages || first >= n) return;
-
-    // [q- | q+] of the head's queries; rows behind the group are zeros and not used
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                    ((long long)b * a.n_q_heads + h * group) * D);
-    for (int i = threadIdx.x; i < rows8 * (D / 8); i += kScoreWarps * 32) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < group) x = q[i];
-        uint32_t w[4] = {x.x, x.y, x.z, x.w}, neg[4], pos[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // by the sign bit; a NaN goes to one of the two and makes the score NaN
-            const uint32_t sign = (w[e] & 0x80008000u) >> 15;
-            const uint32_t mask = sign * 0xffffu;
-            neg[e] = w[e] & mask;
-            pos[e] = w[e] & ~mask;
-        }
-        uint8_t* at = s_q + r * kRowBytes + c * 16;
-        *reinterpret_cast<uint4*>(at) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
-        *reinterpret_cast<uint4*>(at + 2 * D) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
-    }
-    __syncthreads();
-
-    const int32_t* table = a.table + (long long)b * a.table_stride;
-    const T* bounds = static_cast<const T*>(a.bounds);
-    const long long unit = (long long)b * a.n_kv_heads + h;
-    const int g = lane >> 2, t = lane & 3;
-    uint32_t big = 0;
-    for (int j0 = first + warp * 16; j0 < min(first + kSelectTile, n); j0 += kScoreWarps * 16) {
-        // lanes 0 .. 15 find the pages, every lane then takes rows g and g + 8
-        const int j = j0 + (lane & 15);
-        int page = j < n ? table[j] : 0;
-        bool ok = page >= 0 && page < a.num_pages;
-        if (!ok) set_status(a.status, PKV_DEV_BAD_PAGE);
-        if (!ok) page = -1;
-        const int page0 = __shfl_sync(kFull, page, g), page1 = __shfl_sync(kFull, page, g + 8);
-        const bool use0 = j0 + g < n && page0 >= 0, use1 = j0 + g + 8 < n && page1 >= 0;
-        uint4 x[kSegs], y[kSegs];
-        const uint4* r0 = reinterpret_cast<const uint4*>(
-            bounds + ((long long)page0 * a.n_kv_heads + h) * 2 * D);
-        const uint4* r1 = reinterpret_cast<const uint4*>(
-            bounds + ((long long)page1 * a.n_kv_heads + h) * 2 * D);
-#pragma unroll
-        for (int s = 0; s < kSegs; ++s) {
-            x[s] = use0 ? r0[s * 4 + t] : make_uint4(0, 0, 0, 0);
-            y[s] = use1 ? r1[s * 4 + t] : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int s = 0; s < kSegs; ++s) {
-            big = max_abs2(max_abs2(big, x[s].x), x[s].y);
-            big = max_abs2(max_abs2(big, x[s].z), x[s].w);
-            big = max_abs2(max_abs2(big, y[s].x), y[s].y);
-            big = max_abs2(max_abs2(big, y[s].z), y[s].w);
-        }
-        float best0 = -INFINITY, best1 = -INFINITY;
-        for (int q0 = 0; q0 < group; q0 += 8) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint8_t* qrow = s_q + (q0 + g) * kRowBytes + t * 16;
-#pragma unroll
-            for (int s = 0; s < kSegs; ++s) {
-                const uint4 v = *reinterpret_cast<const uint4*>(qrow + s * 64);
-                const uint32_t a0[4] = {x[s].x, y[s].x, x[s].y, y[s].y};
-                const uint32_t a1[4] = {x[s].z, y[s].z, x[s].w, y[s].w};
-                Mma<T>::run(c, a0, v.x, v.y);
-                Mma<T>::run(c, a1, v.z, v.w);
-            }
-            const bool in0 = q0 + 2 * t < group, in1 = q0 + 2 * t + 1 < group;
-            if (in0) best0 = fmaxf(best0, c[0]), best1 = fmaxf(best1, c[2]);
-            if (in1) best0 = fmaxf(best0, c[1]), best1 = fmaxf(best1, c[3]);
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, o));
-            best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, o));
-        }
-        if (t == 0) {
-            float* out = a.scores + unit * a.table_stride + j0;
-            if (j0 + g < n) out[g] = use0 ? best0 : -INFINITY;
-            if (j0 + g + 8 < n) out[g + 8] = use1 ? best1 : -INFINITY;
-        }
-    }
-    big = max(big & 0xffffu, big >> 16);
-    big = __reduce_max_sync(kFull, big);
-    if (lane == 0) s_max[warp] = big;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int w = 1; w < kScoreWarps; ++w) big = max(big, s_max[w]);
-        a.tile_max[unit * a.tiles + tile] = big;
-    }
-}
-
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kFew = 256;  // undecided pages that are ranked by comparing all pairs
 
 // Keys whose order as unsigned numbers is that of the scores, NaN above all.
 __device__ __forceinline__ uint32_t key_of(float s) {
@@ -165,257 +69,501 @@ __device__ __forceinline__ unsigned long long key_of(double s) {
     return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-// Sum over the CTA, to every thread.  buf: kPickWarps + 1 ints; callers alternate two.
+__device__ __forceinline__ float score_of(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// A sum in two floats: hi + lo, |lo| at most half a step of hi.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+
+// The score of a page for one query head to more than 32 bits, as a key, worked out by a
+// warp (every lane gets it).  fp64 runs at a 64th of fp32's rate on this part, and a warp's
+// 8 D products of it cost 6 us beside the CTA's other warps: two floats unless they cannot
+// hold it (`wide`).
+template <typename T, int D>
+__device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, int b, int h, int j,
+                                                         int i, float S, bool wide) {
+    const int lane = threadIdx.x & 31;
+    const int group = a.n_q_heads / a.n_kv_heads;
+    const int page = a.table[(long long)b * a.table_stride + j];
+    if (page < 0 || page >= a.num_pages) return key_of(-(double)INFINITY);
+    if (S == 0.f) return key_of(0.0);  // every product is a zero
+    const T* row = static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D;
+    const T* q = static_cast<const T*>(a.q) + ((long long)b * a.n_q_heads + h * group + i) * D;
+    float x[D / 32], lo[D / 32], hi[D / 32];
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        const int d = u * 32 + lane;
+        x[u] = (float)q[d], lo[u] = (float)row[d], hi[u] = (float)row[D + d];
+    }
+    if (wide) {
+        double sum = 0.0;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+            // as the product does it: both halves, one of them with a zero
+            const bool neg = signbit(x[u]);
+            sum += (double)(neg ? x[u] : 0.f) * (double)lo[u] + (double)(neg ? 0.f : x[u]) * (double)hi[u];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        return key_of(sum);
+    }
+    Two sum = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u)  // (exact products; nothing is infinite here)
+        sum = add(sum, {__fmul_rn(x[u], signbit(x[u]) ? lo[u] : hi[u]), 0.f});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        // the same order in every lane: the lower lane's sum first
+        const Two other = {__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)};
+        sum = lane & o ? add(other, sum) : add(sum, other);
+    }
+    return key_of((double)sum.hi + (double)sum.lo);
+}
+
+// What a tile of scores leaves for the choice.
+struct ScoreScratch {
+    uint32_t big[16], top[16], low[16];
+    float sum[16];
+};
+
+// Scores of pages first .. end - 1 (by the CTA), and of them the largest |bound|, the keys of
+// the largest and the smallest score of a page of the pool, and the largest sum of a
+// query's |q|.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, int b, int h, int first, int end,
+                                            uint8_t* s_q, ScoreScratch& sh, uint4* stat) {
+    constexpr int kSegs = 2 * D / 32;      // 64-byte pieces of a row: two k-steps each
+    constexpr int kRowBytes = 4 * D + 64;  // a query's [q- | q+], rows 64 bytes apart mod 128
+    constexpr int kWarps = THREADS / 32, kStep = kWarps * 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = a.n_q_heads / a.n_kv_heads;
+    const int rows8 = (group + 7) / 8 * 8;
+    const int32_t* table = a.table + (long long)b * a.table_stride;
+    const T* bounds = static_cast<const T*>(a.bounds) + (long long)h * 2 * D;
+    const long long page_step = (long long)a.n_kv_heads * 2 * D;
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t bits = 0;
+    // lanes 0 .. 15 (and again 16 .. 31) find the pages, every lane then takes rows g, g + 8
+    auto page_at = [&](int j0) {
+        const int j = j0 + (lane & 15);
+        if (j >= end) return -1;
+        const int page = table[j];
+        if (page >= 0 && page < a.num_pages) return page;
+        bits |= PKV_DEV_BAD_PAGE;
+        return -1;
+    };
+    uint4 x[kSegs], y[kSegs];
+    bool use0, use1;
+    auto load = [&](int page) {
+        const int page0 = __shfl_sync(kFull, page, g), page1 = __shfl_sync(kFull, page, g + 8);
+        use0 = page0 >= 0, use1 = page1 >= 0;
+        const uint4* r0 = reinterpret_cast<const uint4*>(bounds + page0 * page_step);
+        const uint4* r1 = reinterpret_cast<const uint4*>(bounds + page1 * page_step);
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) {
+            x[s] = use0 ? r0[s * 4 + t] : make_uint4(0, 0, 0, 0);
+            y[s] = use1 ? r1[s * 4 + t] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    int j0 = first + warp * 16;
+    load(page_at(j0));  // in flight while the queries come
+    int next = page_at(j0 + kStep);
+
+    // [q- | q+] of the head's queries; rows behind the group are zeros and not used
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                    ((long long)b * a.n_q_heads + h * group) * D);
+    for (int i = threadIdx.x; i < rows8 * (D / 8); i += THREADS) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < group) v = q[i];
+        uint32_t w[4] = {v.x, v.y, v.z, v.w}, neg[4], pos[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // by the sign bit; a NaN goes to one of the two and makes the score NaN
+            const uint32_t mask = ((w[e] & 0x80008000u) >> 15) * 0xffffu;
+            neg[e] = w[e] & mask;
+            pos[e] = w[e] & ~mask;
+        }
+        uint8_t* at = s_q + r * kRowBytes + c * 16;
+        *reinterpret_cast<uint4*>(at) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+        *reinterpret_cast<uint4*>(at + 2 * D) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+    }
+    __syncthreads();
+
+    const long long unit = (long long)b * a.n_kv_heads + h;
+    uint32_t big = 0, top = 0, low = 0xffffffffu;
+    for (; j0 < end; j0 += kStep) {
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) {
+            big = max_abs2<T>(max_abs2<T>(big, x[s].x), x[s].y);
+            big = max_abs2<T>(max_abs2<T>(big, x[s].z), x[s].w);
+            big = max_abs2<T>(max_abs2<T>(big, y[s].x), y[s].y);
+            big = max_abs2<T>(max_abs2<T>(big, y[s].z), y[s].w);
+        }
+        float best0 = -INFINITY, best1 = -INFINITY;
+        for (int q0 = 0; q0 < group; q0 += 8) {
+            float c[2][4] = {};  // even and odd k-steps in chains of their own
+            const uint8_t* qrow = s_q + (q0 + g) * kRowBytes + t * 16;
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s) {
+                const uint4 v = *reinterpret_cast<const uint4*>(qrow + s * 64);
+                const uint32_t a0[4] = {x[s].x, y[s].x, x[s].y, y[s].y};
+                const uint32_t a1[4] = {x[s].z, y[s].z, x[s].w, y[s].w};
+                Mma<T>::run(c[0], a0, v.x, v.y);
+                Mma<T>::run(c[1], a1, v.z, v.w);
+            }
+            if (q0 + 2 * t < group) {
+                best0 = fmaxf(best0, c[0][0] + c[1][0]);
+                best1 = fmaxf(best1, c[0][2] + c[1][2]);
+            }
+            if (q0 + 2 * t + 1 < group) {
+                best0 = fmaxf(best0, c[0][1] + c[1][1]);
+                best1 = fmaxf(best1, c[0][3] + c[1][3]);
+            }
+        }
+        const bool in0 = use0, in1 = use1;
+        if (j0 + kStep < end) {
+            load(next);
+            next = page_at(j0 + 2 * kStep);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, o));
+            best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, o));
+        }
+        if (t == 0) {
+            float* out = a.scores + unit * a.table_stride + j0;
+            if (j0 + g < end) out[g] = in0 ? best0 : -INFINITY;
+            if (j0 + g + 8 < end) out[g + 8] = in1 ? best1 : -INFINITY;
+            if (in0) top = max(top, key_of(best0)), low = min(low, key_of(best0));
+            if (in1) top = max(top, key_of(best1)), low = min(low, key_of(best1));
+        }
+    }
+    if (bits) set_status(a.status, bits);
+    // the sums of |q|: [q- | q+] holds each element once, beside a zero
+    float most = 0.f;
+    for (int r = warp; r < group; r += kWarps) {
+        const uint4* row = reinterpret_cast<const uint4*>(s_q + r * kRowBytes);
+        float sum = 0.f;
+        if (lane < D / 4) {
+            float f[8];
+            Cvt<T>::unpack8(row[lane], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += fabsf(f[e]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        most = sum > most || sum != sum ? sum : most;
+    }
+    big = __reduce_max_sync(kFull, max(big & 0xffffu, big >> 16));
+    top = __reduce_max_sync(kFull, top);
+    low = __reduce_min_sync(kFull, low);
+    if (lane == 0) {
+        sh.big[warp] = big;
+        sh.top[warp] = top;
+        sh.low[warp] = low;
+        sh.sum[warp] = most;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            big = max(big, sh.big[w]);
+            top = max(top, sh.top[w]);
+            low = min(low, sh.low[w]);
+            most = sh.sum[w] > most || sh.sum[w] != sh.sum[w] ? sh.sum[w] : most;
+        }
+        *stat = make_uint4(big, top, low, __float_as_uint(most));
+    }
+}
+
+// Sum over the CTA, to every thread.  buf: an int a warp; callers alternate two.
+template <int THREADS>
 __device__ __forceinline__ int cta_sum(int x, int* buf) {
     x = __reduce_add_sync(kFull, x);
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    return __reduce_add_sync(kFull, lane < kPickWarps ? buf[lane] : 0);
+    return __reduce_add_sync(kFull, lane < THREADS / 32 ? buf[lane] : 0);
 }
 
-// 64-bit score of a page, worked out by a warp (every lane gets it).
-template <typename T, int D>
-__device__ __forceinline__ double score64(const SelectArgs& a, int b, int h, int j) {
-    const int lane = threadIdx.x & 31;
-    const int group = a.n_q_heads / a.n_kv_heads;
-    const int page = a.table[(long long)b * a.table_stride + j];
-    if (page < 0 || page >= a.num_pages) return -INFINITY;
-    const T* row = static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D;
-    const T* q = static_cast<const T*>(a.q) + ((long long)b * a.n_q_heads + h * group) * D;
-    double best = -INFINITY;
-    for (int i = 0; i < group; ++i) {
-        double sum = 0.0;
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
-            const int d = u * 32 + lane;
-            const float x = (float)q[i * D + d], lo = (float)row[d], hi = (float)row[D + d];
-            // as the product does it: both halves, one of them with a zero
-            const bool neg = signbit(x);
-            sum += (double)(neg ? x : 0.f) * (double)lo + (double)(neg ? 0.f : x) * (double)hi;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (sum != sum) return sum;  // every lane has the same sum
-        best = fmax(best, sum);
+struct PickScratch {
+    uint32_t chosen[kMaxSelectPages / 32];
+    int hist[kBins];
+    int buf[2][16];
+    int few_at[kFew];              // pages that are not settled, the keys of their scores,
+    uint32_t few[kFew];
+    unsigned long long far[kFew];  // and of their 64-bit scores
+    int open_n, bin, above;
+    uint32_t kth;
+};
+
+// The want-th largest of `key_at(i)` over i < cn, bit by bit from the top (any number of
+// candidates and equals).
+template <int THREADS, typename K, typename F>
+__device__ __forceinline__ K kth_key(int (*buf)[16], int& turn, int cn, int want, F key_at) {
+    K key = 0;
+    for (int bit = 8 * sizeof(K) - 1; bit >= 0; --bit) {
+        const K probe = key | ((K)1 << bit);
+        int count = 0;
+        for (int i = threadIdx.x; i < cn; i += THREADS) count += key_at(i) >= probe;
+        if (cta_sum<THREADS>(count, buf[turn ^= 1]) >= want) key = probe;
     }
-    return best;
+    return key;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a) {
-    __shared__ uint32_t s_chosen[kMaxSelectPages / 32];
-    __shared__ int s_buf[2][kPickWarps + 1];
-    __shared__ double s_sum[kPickWarps];
-    __shared__ uint32_t s_big;
-    __shared__ double s_few[kFew];
-    __shared__ int s_few_at[kFew];
-    __shared__ int s_few_n;
+// The choice among pages c0 .. c0 + cn - 1: the `want` of the highest scores, into out[c0 ..].
+// stats: the unit's tiles'.  sh.hist and sh.open_n are 0.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, int cn, int want,
+                                     int32_t* out, const uint4* stats, int tiles, float* s_sc,
+                                     int cache, PickScratch& sh) {
+    constexpr int kWarps = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x, b = blockIdx.y;
+    const int group = a.n_q_heads / a.n_kv_heads;
     const long long unit = (long long)b * a.n_kv_heads + h;
-    int32_t* out = a.selected + unit * a.max_pages;
-    pdl_wait();
-    pdl_trigger();
-    uint32_t bits = 0;
-    const int n = pages_of(a, b, &bits);  // (flagged by the scores' kernel)
-    const int K = a.max_pages;
-    if (n <= K) {
-        for (int i = threadIdx.x; i < K; i += kPickThreads) out[i] = i < n ? i : -1;
-        return;
-    }
-    // candidates: pages keep_first .. n - keep_last - 1, `want` of them are taken
-    const int c0 = a.keep_first, cn = n - a.keep_first - a.keep_last;
-    const int want = K - a.keep_first - a.keep_last;
-    for (int i = threadIdx.x; i < a.keep_first; i += kPickThreads) out[i] = i;
-    for (int i = threadIdx.x; i < a.keep_last; i += kPickThreads)
-        out[K - a.keep_last + i] = n - a.keep_last + i;
-    if (want == 0) return;
-    const float* sc = a.scores + unit * a.table_stride + c0;
-    double* sc64 = a.scores64 + unit * a.table_stride + c0;
+    const float* far = a.scores + unit * a.table_stride + c0;
+    unsigned long long* keys64 = a.keys64 + unit * a.table_stride + c0;
     const int words = (cn + 31) / 32;
-    if (threadIdx.x == 0) {
-        s_big = 0;
-        s_few_n = 0;
-    }
-    __syncthreads();
-
-    // S = the largest sum of |q| times the largest |bound|
-    {
-        const int group = a.n_q_heads / a.n_kv_heads;
-        const T* q = static_cast<const T*>(a.q) + ((long long)b * a.n_q_heads + h * group) * D;
-        double most = 0.0;
-        for (int i = warp; i < group; i += kPickWarps) {
-            float sum = 0.f;
-#pragma unroll
-            for (int u = 0; u < D / 32; ++u) sum += fabsf((float)q[i * D + u * 32 + lane]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            most = sum > most || sum != sum ? (double)sum : most;
-        }
-        if (lane == 0) s_sum[warp] = most;
-        uint32_t big = 0;
-        for (int i = threadIdx.x; i < (n + kSelectTile - 1) / kSelectTile; i += kPickThreads)
-            big = max(big, a.tile_max[unit * a.tiles + i]);
-        big = __reduce_max_sync(kFull, big);
-        if (lane == 0) atomicMax(&s_big, big);
-    }
-    __syncthreads();
-    double most = 0.0;
-#pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) {
-        const double x = s_sum[w];
-        most = x > most || x != x ? x : most;
-    }
-    const uint16_t big16 = (uint16_t)s_big;
-    const double S = most * (double)(float)(*reinterpret_cast<const T*>(&big16));
-    // beyond fp32 (or not a number): no fp32 score says anything
-    const bool blind = !(S < 1e38);
-    // (2^-126: what a product below fp32's normal range may lose, 256 times)
-    const double e2 = 2.0 * (S * 3.0517578125e-05 + (S > 0.0 ? 256.0 * 1.1754943508222875e-38 : 0.0));
-
-    // T: the want-th largest fp32 score, bit by bit from the top
-    double upper = INFINITY, lower = -INFINITY;
     int turn = 0;
-    if (!blind) {
-        uint32_t key = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t probe = key | (1u << bit);
-            int count = 0;
-            for (int i = threadIdx.x; i < cn; i += kPickThreads) count += key_of(sc[i]) >= probe;
-            if (cta_sum(count, s_buf[turn ^= 1]) >= want) key = probe;
-        }
-        const float kth = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-        upper = (double)kth + e2;
-        lower = (double)kth - e2;
-        // (e2 infinite cannot be; kth = -inf: bad pages fill up the list, lower = upper = -inf)
-    }
-    // pages that are chosen for certain, and how many are not settled
-    int sure = 0, open = 0;
-    for (int w = warp; w < words; w += kPickWarps) {
-        const int i = w * 32 + lane;
-        const double s = i < cn ? (double)sc[i] : 0.0;
-        const bool yes = i < cn && !blind && s > upper;
-        const bool may = i < cn && !yes && (blind || s >= lower);
-        const uint32_t m = __ballot_sync(kFull, yes);
-        if (lane == 0) s_chosen[w] = m;
-        sure += yes;
-        open += may;
-    }
-    sure = cta_sum(sure, s_buf[turn ^= 1]);
-    open = cta_sum(open, s_buf[turn ^= 1]);
-    const int left = want - sure;  // >= 1: at most want - 1 scores are above the want-th
-    __syncthreads();
 
-    if (open == left) {  // all of them
-        for (int w = warp; w < words; w += kPickWarps) {
-            const int i = w * 32 + lane;
-            const bool may = i < cn && (blind || ((double)sc[i] >= lower && (double)sc[i] <= upper));
-            const uint32_t m = __ballot_sync(kFull, may);
-            if (lane == 0) s_chosen[w] |= m;
+    for (int i = threadIdx.x; i < min(cn, cache); i += THREADS) s_sc[i] = far[i];
+    uint32_t big = 0, top = 0, low = 0xffffffffu;
+    float most = 0.f;
+    for (int i = lane; i < tiles; i += 32) {
+        const uint4 st = stats[i];
+        big = max(big, st.x);
+        top = max(top, st.y);
+        low = min(low, st.z);
+        most = __uint_as_float(st.w);  // the same for every tile
+    }
+    big = __reduce_max_sync(kFull, big);
+    top = __reduce_max_sync(kFull, top);
+    low = __reduce_min_sync(kFull, low);
+    most = __shfl_sync(kFull, most, 0);
+    const uint16_t big16 = (uint16_t)big;
+    // S and twice the error bound, rounded up
+    const float S = __fmul_ru(most, (float)(*reinterpret_cast<const T*>(&big16)));
+    // beyond fp32 (or not a number): no fp32 score says anything
+    const bool blind = !(S < 1e38f);
+    // (the second part: what products below fp32's normal range may lose, 256 of them, twice)
+    const float e2 = S > 0.f ? __fadd_ru(__fmul_ru(S, 6.103515625e-05f), 6.1e-36f) : 0.f;
+    // two fp32 values hold a sum of products to 2^-47 of S, where none of them is so small
+    // that its last bits are lost; else fp64
+    const bool wide = blind || S < 8.7e-19f;
+    auto score = [&](int i) { return i < cache ? s_sc[i] : far[i]; };
+
+    // Where the border lies: the want-th largest fp32 score is in the bin that the counts
+    // reach it in.  (A bin's number grows with the score, whatever the rounding.  A page
+    // outside the pool, -inf, falls into bin 0.)
+    float upper = INFINITY, lower = -INFINITY;  // above / below is settled
+    const float mx = score_of(top), mn = low > top ? mx : score_of(low);
+    const float inv = top != 0 && mx > mn ? (float)(kBins - 1) / (mx - mn) : 0.f;
+    auto bin_of = [&](float s) { return min(max((int)((s - mn) * inv), 0), kBins - 1); };
+    if (!blind) {
+        for (int i = threadIdx.x; i < cn; i += THREADS)  // (the thread's own copies)
+            atomicAdd(&sh.hist[bin_of(score(i))], 1);
+        __syncthreads();
+        constexpr int kPer = kBins / THREADS;
+        int own[kPer], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            mine += own[e] = sh.hist[kBins - 1 - (threadIdx.x * kPer + e)];
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += v;
         }
-    } else {
-        const bool few = open <= kFew;
-        for (int w = warp; w < words; w += kPickWarps) {
-            const int i = w * 32 + lane;
-            const bool may = i < cn && (blind || ((double)sc[i] >= lower && (double)sc[i] <= upper));
-            uint32_t m = __ballot_sync(kFull, may);
-            while (m) {
-                const int at = w * 32 + __ffs(m) - 1;
-                m &= m - 1;
-                // S = 0: every product is a zero
-                const double s = S == 0.0 ? 0.0 : score64<T, D>(a, b, h, c0 + at);
-                if (lane == 0) {
-                    if (few) {
-                        const int k = atomicAdd(&s_few_n, 1);
-                        s_few[k] = s;
-                        s_few_at[k] = at;
-                    } else {
-                        sc64[at] = s;
-                    }
-                }
+        int* buf = sh.buf[turn ^= 1];
+        if (lane == 31) buf[warp] = upto;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) upto += w < warp ? buf[w] : 0;
+        int above = upto - mine;
+        if (above < want && want <= upto) {  // one thread
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                if (above < want && want <= above + own[e])
+                    sh.bin = kBins - 1 - (threadIdx.x * kPer + e);
+                above += own[e];
             }
         }
         __syncthreads();
-        if (few) {
-            for (int k = threadIdx.x; k < open; k += kPickThreads) {
-                const unsigned long long mine = key_of(s_few[k]);
-                const int at = s_few_at[k];
+        const int bin = sh.bin;
+        // all that may be within 2 e of a score of that bin: the bin's ends (a few roundings
+        // of their size further apart) and e2.  One bin for all (inv = 0) has no ends.
+        const float slack = __fadd_ru(e2, fmaxf(fabsf(mn), fabsf(mx)) * 2e-6f);
+        if (inv > 0.f && bin < kBins - 1) upper = mn + (float)(bin + 1) * (1.0f / inv) + slack;
+        if (inv > 0.f && bin > 0) lower = mn + (float)bin * (1.0f / inv) - slack;
+    }
+    // pages that are chosen for certain, and those that are not settled
+    int sure = 0;
+    for (int w = warp; w < words; w += kWarps) {
+        const int i = w * 32 + lane;
+        const float s = i < cn ? score(i) : 0.f;
+        const bool yes = i < cn && !blind && s > upper;
+        const bool may = i < cn && !yes && (blind || s >= lower);
+        const uint32_t m = __ballot_sync(kFull, yes);
+        if (lane == 0) sh.chosen[w] = m;
+        sure += __popc(m);
+        if (may) {
+            const int k = atomicAdd(&sh.open_n, 1);
+            if (k < kFew) {
+                sh.few_at[k] = i;
+                sh.few[k] = key_of(s);
+            }
+        }
+    }
+    sure = cta_sum<THREADS>(lane == 0 ? sure : 0, sh.buf[turn ^= 1]);
+    const int open = sh.open_n;
+    int left = want - sure;  // >= 1
+    if (open <= kFew && !blind) {
+        // the left-th of the few by fp32: those more than e2 from it are settled too.  The
+        // others' keys become 64-bit ones
+        for (int k = threadIdx.x; k < open; k += THREADS) {
+            const uint32_t s = sh.few[k];
+            int more = 0, same = 0;
+            for (int o = 0; o < open; ++o) {
+                more += sh.few[o] > s;
+                same += sh.few[o] == s;
+            }
+            if (more < left && left <= more + same) sh.kth = s;
+        }
+        __syncthreads();
+        const float kth = score_of(sh.kth);
+        upper = __fadd_ru(kth, e2);
+        lower = __fadd_rd(kth, -e2);
+        int yes = 0, may = 0;
+        for (int k = lane; k < open; k += 32) {  // every warp counts for itself
+            const float s = score_of(sh.few[k]);
+            yes += s > upper;
+            may += s <= upper && s >= lower;
+        }
+        yes = __reduce_add_sync(kFull, yes);
+        may = __reduce_add_sync(kFull, may);
+        if (may == left - yes) {
+            for (int k = threadIdx.x; k < open; k += THREADS)
+                if (score_of(sh.few[k]) >= lower)
+                    atomicOr(&sh.chosen[sh.few_at[k] >> 5], 1u << (sh.few_at[k] & 31));
+        } else {
+            // settled ones get the ends of the keys' range
+            for (int k = threadIdx.x; k < open; k += THREADS)
+                sh.far[k] = score_of(sh.few[k]) > upper ? ~0ull : 0ull;
+            __syncthreads();
+            for (int x = warp; x < open * group; x += kWarps) {
+                const int k = x / group;
+                const float s = score_of(sh.few[k]);
+                if (s > upper || s < lower) continue;
+                const unsigned long long key =
+                    long_score<T, D>(a, b, h, c0 + sh.few_at[k], x - k * group, S, wide);
+                if (lane == 0) atomicMax(&sh.far[k], key);
+            }
+            __syncthreads();
+            for (int k = threadIdx.x; k < open; k += THREADS) {
+                const unsigned long long mine = sh.far[k];
+                const int at = sh.few_at[k];
                 int above = 0;
                 for (int o = 0; o < open; ++o) {
-                    const unsigned long long other = key_of(s_few[o]);
-                    above += other > mine || (other == mine && s_few_at[o] < at);
+                    const unsigned long long other = sh.far[o];
+                    above += other > mine || (other == mine && sh.few_at[o] < at);
                 }
-                if (above < left) atomicOr(&s_chosen[at >> 5], 1u << (at & 31));
+                if (above < left) atomicOr(&sh.chosen[at >> 5], 1u << (at & 31));
             }
-        } else {
-            // the left-th largest of the 64-bit scores, bit by bit, then the lowest indexes
-            // among its equals
-            auto is_open = [&](int i) {
-                return blind || ((double)sc[i] >= lower && (double)sc[i] <= upper);
-            };
-            unsigned long long key = 0;
-            for (int bit = 63; bit >= 0; --bit) {
-                const unsigned long long probe = key | (1ull << bit);
-                int count = 0;
-                for (int i = threadIdx.x; i < cn; i += kPickThreads)
-                    if (is_open(i)) count += key_of(sc64[i]) >= probe;
-                if (cta_sum(count, s_buf[turn ^= 1]) >= left) key = probe;
+        }
+    } else {
+        // many (scores that crowd into a bin, equal pages, or scores beyond fp32): the
+        // exact border of the fp32 scores bit by bit, the 64-bit scores around it into the
+        // workspace, the left-th largest of those, then the lowest indexes among its equals
+        if (!blind) {
+            const float kth = score_of(kth_key<THREADS, uint32_t>(
+                sh.buf, turn, cn, want, [&](int i) { return key_of(score(i)); }));
+            upper = __fadd_ru(kth, e2);
+            lower = __fadd_rd(kth, -e2);
+        }
+        auto is_open = [&](int i) {
+            const float s = score(i);
+            return blind || (s >= lower && s <= upper);
+        };
+        sure = 0;
+        for (int w = warp; w < words; w += kWarps) {
+            const int i = w * 32 + lane;
+            const uint32_t yes = __ballot_sync(kFull, i < cn && !blind && score(i) > upper);
+            if (lane == 0) sh.chosen[w] = yes;
+            sure += __popc(yes);
+            uint32_t m = __ballot_sync(kFull, i < cn && is_open(i));
+            while (m) {
+                const int at = w * 32 + __ffs(m) - 1;
+                m &= m - 1;
+                unsigned long long key = 0;
+                for (int x = 0; x < group; ++x)
+                    key = max(key, long_score<T, D>(a, b, h, c0 + at, x, S, wide));
+                if (lane == 0) keys64[at] = key;
             }
-            int above = 0;
-            for (int i = threadIdx.x; i < cn; i += kPickThreads)
-                if (is_open(i)) above += key_of(sc64[i]) > key;
-            above = cta_sum(above, s_buf[turn ^= 1]);
-            int equal = left - above;  // of the equals, the first so many
-            for (int w0 = 0; w0 < words; w0 += kPickWarps) {
-                const int w = w0 + warp, i = w * 32 + lane;
-                const bool may = i < cn && is_open(i);
-                const unsigned long long k = may ? key_of(sc64[i]) : 0ull;
-                const uint32_t yes = __ballot_sync(kFull, may && k > key);
-                uint32_t tie = __ballot_sync(kFull, may && k == key);
-                int* buf = s_buf[turn ^= 1];
-                if (lane == 0) buf[warp] = __popc(tie);
-                __syncthreads();
-                int before = 0, all = 0;
+        }
+        left = want - cta_sum<THREADS>(lane == 0 ? sure : 0, sh.buf[turn ^= 1]);
+        const unsigned long long key = kth_key<THREADS, unsigned long long>(
+            sh.buf, turn, cn, left, [&](int i) { return is_open(i) ? keys64[i] : 0ull; });
+        int above = 0;
+        for (int i = threadIdx.x; i < cn; i += THREADS) above += is_open(i) && keys64[i] > key;
+        int equal = left - cta_sum<THREADS>(above, sh.buf[turn ^= 1]);  // the first so many
+        for (int w0 = 0; w0 < words; w0 += kWarps) {
+            const int w = w0 + warp, i = w * 32 + lane;
+            const bool may = i < cn && is_open(i);
+            const unsigned long long k = may ? keys64[i] : 0ull;
+            uint32_t take = __ballot_sync(kFull, may && k > key);
+            uint32_t tie = __ballot_sync(kFull, may && k == key);
+            int* buf = sh.buf[turn ^= 1];
+            if (lane == 0) buf[warp] = __popc(tie);
+            __syncthreads();
+            int before = 0, all = 0;
 #pragma unroll
-                for (int x = 0; x < kPickWarps; ++x) {
-                    before += x < warp ? buf[x] : 0;
-                    all += buf[x];
-                }
-                int room = equal - before;
-                uint32_t take = yes;
-                while (tie && room > 0) {
-                    take |= tie & -tie;
-                    tie &= tie - 1;
-                    --room;
-                }
-                if (lane == 0 && w < words) s_chosen[w] |= take;
-                equal -= min(all, max(equal, 0));
+            for (int v = 0; v < kWarps; ++v) {
+                before += v < warp ? buf[v] : 0;
+                all += buf[v];
             }
+            for (int room = equal - before; tie && room > 0; --room) {
+                take |= tie & -tie;
+                tie &= tie - 1;
+            }
+            if (lane == 0 && w < words) sh.chosen[w] |= take;
+            equal -= min(all, max(equal, 0));
         }
     }
     __syncthreads();
 
     // the chosen in ascending order
     int done = 0;
-    for (int w0 = 0; w0 < words; w0 += kPickThreads) {
+    for (int w0 = 0; w0 < words; w0 += THREADS) {
         const int w = w0 + threadIdx.x;
-        uint32_t m = w < words ? s_chosen[w] : 0;
+        uint32_t m = w < words ? sh.chosen[w] : 0;
         const int mine = __popc(m);
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o) upto += x;
+            const int v = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += v;
         }
-        int* buf = s_buf[turn ^= 1];
+        int* buf = sh.buf[turn ^= 1];
         if (lane == 31) buf[warp] = upto;
         __syncthreads();
         int before = 0, all = 0;
 #pragma unroll
-        for (int x = 0; x < kPickWarps; ++x) {
-            before += x < warp ? buf[x] : 0;
-            all += buf[x];
+        for (int v = 0; v < kWarps; ++v) {
+            before += v < warp ? buf[v] : 0;
+            all += buf[v];
         }
         int at = done + before + upto - mine;
         while (m) {
@@ -426,20 +574,120 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a) 
     }
 }
 
-template <typename T, int D>
-cudaError_t launch(const SelectArgs& a, cudaStream_t stream) {
-    const int group = a.n_q_heads / a.n_kv_heads;
-    const size_t smem = (size_t)((group + 7) / 8 * 8) * (4 * D + 64);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            score_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+// What needs no scores: every page where there are no more than max_pages, and the pages that
+// are always kept.  True where nothing is left to choose.
+__device__ __forceinline__ bool list_kept(const SelectArgs& a, int n, int32_t* out, int threads,
+                                          bool write) {
+    const int K = a.max_pages;
+    if (n <= K) {
+        for (int i = threadIdx.x; write && i < K; i += threads) out[i] = i < n ? i : -1;
+        return true;
     }
-    cudaError_t e = launch_pdl(score_kernel<T, D>, dim3(a.n_kv_heads, a.tiles, a.batch),
-                               dim3(kScoreWarps * 32), smem, stream, a);
+    for (int i = threadIdx.x; write && i < a.keep_first; i += threads) out[i] = i;
+    for (int i = threadIdx.x; write && i < a.keep_last; i += threads)
+        out[K - a.keep_last + i] = n - a.keep_last + i;
+    return a.keep_first + a.keep_last == K;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectArgs a) {
+    extern __shared__ __align__(16) uint8_t s_q[];
+    __shared__ ScoreScratch sh;
+    const int h = blockIdx.x, tile = blockIdx.y, b = blockIdx.z;
+    pdl_wait();
+    pdl_trigger();
+    uint32_t bits = 0;
+    const int n = pages_of(a, b, &bits);
+    if (bits && h == 0 && tile == 0 && threadIdx.x == 0) set_status(a.status, bits);
+    const int first = tile * a.tile_pages;
+    if (first >= n || list_kept(a, n, nullptr, kScoreThreads, false)) return;
+    score_pages<T, D, kScoreThreads>(a, b, h, first, min(first + a.tile_pages, n), s_q, sh,
+                                     a.stats + ((long long)b * a.n_kv_heads + h) * a.tiles + tile);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a, int cache) {
+    extern __shared__ float s_sc[];  // [cache]
+    __shared__ PickScratch sh;
+    const int h = blockIdx.x, b = blockIdx.y;
+    const long long unit = (long long)b * a.n_kv_heads + h;
+    int32_t* out = a.selected + unit * a.max_pages;
+    for (int i = threadIdx.x; i < kBins; i += kPickThreads) sh.hist[i] = 0;
+    if (threadIdx.x == 0) sh.open_n = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    uint32_t bits = 0;
+    const int n = pages_of(a, b, &bits);  // (flagged by the scores' kernel)
+    if (list_kept(a, n, out, kPickThreads, true)) return;
+    pick<T, D, kPickThreads>(a, b, h, a.keep_first, n - a.keep_first - a.keep_last,
+                             a.max_pages - a.keep_first - a.keep_last, out, a.stats + unit * a.tiles,
+                             (n + a.tile_pages - 1) / a.tile_pages, s_sc, cache, sh);
+}
+
+// Both in one CTA.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSmallThreads) select_small_kernel(const SelectArgs a, int cache,
+                                                                     int q_bytes) {
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    __shared__ ScoreScratch score_sh;
+    __shared__ PickScratch sh;
+    const int h = blockIdx.x, b = blockIdx.y;
+    const long long unit = (long long)b * a.n_kv_heads + h;
+    int32_t* out = a.selected + unit * a.max_pages;
+    for (int i = threadIdx.x; i < kBins; i += kSmallThreads) sh.hist[i] = 0;
+    if (threadIdx.x == 0) sh.open_n = 0;
+    pdl_wait();
+    pdl_trigger();
+    uint32_t bits = 0;
+    const int n = pages_of(a, b, &bits);
+    if (bits && h == 0 && threadIdx.x == 0) set_status(a.status, bits);
+    if (list_kept(a, n, out, kSmallThreads, true)) return;
+    uint4* stat = a.stats + unit * a.tiles;
+    score_pages<T, D, kSmallThreads>(a, b, h, 0, n, s_dyn, score_sh, stat);
+    __syncthreads();
+    pick<T, D, kSmallThreads>(a, b, h, a.keep_first, n - a.keep_first - a.keep_last,
+                              a.max_pages - a.keep_first - a.keep_last, out, stat, 1,
+                              reinterpret_cast<float*>(s_dyn + q_bytes), cache, sh);
+}
+
+template <typename T, int D>
+cudaError_t launch(SelectArgs a, cudaStream_t stream) {
+    const int group = a.n_q_heads / a.n_kv_heads;
+    const int q_bytes = (group + 7) / 8 * 8 * (4 * D + 64);
+    const int cache = a.table_stride < kScoreCache ? a.table_stride : kScoreCache;
+    const long long units = (long long)a.batch * a.n_kv_heads;
+    // Short rows: one launch, a CTA a unit.  us a call (bf16, D 128), one / two launches: 32
+    // units of 128 pages 8.0 / 9.5, 256 pages 9.3 / 9.9, 512 pages 12.1 / 10.1; 128 units of
+    // 512 pages 12.5 / 14.9.  Longer rows of unequal requests want their pages shared out.
+    if (a.table_stride <= 256 || (a.table_stride <= 512 && 2 * units >= sm_count())) {
+        a.tiles = 1;
+        static SmemLimit limit;
+        const cudaError_t e = limit.set(reinterpret_cast<const void*>(select_small_kernel<T, D>),
+                                        kMaxSelectGroup * (4 * D + 64) + kScoreCache * 4);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(select_small_kernel<T, D>, dim3(a.n_kv_heads, a.batch),
+                          dim3(kSmallThreads), q_bytes + cache * 4, stream, a, cache, q_bytes);
+    }
+    // a few steps a CTA (its start is a chain of loads: length, table, bounds), as long as
+    // the CTAs make a wave
+    a.tile_pages = kSelectTile;
+    const long long wave = 4LL * sm_count();
+    while (a.tile_pages < 16 * kSelectTile &&
+           units * ((a.table_stride + 2 * a.tile_pages - 1) / (2 * a.tile_pages)) >= wave)
+        a.tile_pages *= 2;
+    a.tiles = (a.table_stride + a.tile_pages - 1) / a.tile_pages;
+    static SmemLimit score_limit, pick_limit;
+    cudaError_t e = score_limit.set(reinterpret_cast<const void*>(score_kernel<T, D>),
+                                    kMaxSelectGroup * (4 * D + 64));
+    if (e == cudaSuccess)
+        e = pick_limit.set(reinterpret_cast<const void*>(pick_kernel<T, D>), kScoreCache * 4);
+    if (e == cudaSuccess)
+        e = launch_pdl(score_kernel<T, D>, dim3(a.n_kv_heads, a.tiles, a.batch),
+                       dim3(kScoreThreads), q_bytes, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(pick_kernel<T, D>, dim3(a.n_kv_heads, a.batch), dim3(kPickThreads), 0,
-                      stream, a);
+    return launch_pdl(pick_kernel<T, D>, dim3(a.n_kv_heads, a.batch), dim3(kPickThreads),
+                      cache * 4, stream, a, cache);
 }
 
 }  // namespace

@@ -6,13 +6,62 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace pkv {
 
+// The dynamic shared memory that a kernel may ask for, set once a device.
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};  // bit per device
+    cudaError_t set(const void* fn, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+
+// SMs of the current device (at least 1).
+inline int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 constexpr int kMaxTableBatch = 16384;    // requests of one paged_tables_build
+constexpr int kMaxAppendRows = 4096;     // rows of a token (q, k, v) of one kv_append_tokens
 constexpr int kMaxSelectPages = 131072;  // table columns of one paged_select_pages
-constexpr int kMaxSelectGroup = 256;     // query heads of a KV head: their rows in shared memory
+constexpr int kSelectTile = 64;          // the fewest pages of a score CTA of paged_select_pages
+constexpr int kMaxSelectGroup = 192;     // query heads of a KV head: their rows in shared memory
+
+// Thread-block clusters.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 struct TablesArgs {
     const int32_t* cached;      // [B]
@@ -75,14 +124,12 @@ struct SelectArgs {
     int batch, n_q_heads, n_kv_heads, page_size, num_pages;
     int keep_first, keep_last, max_pages;
     int32_t* selected;   // [B][Hkv][max_pages]
-    double* scores64;    // workspace [B][Hkv][stride]
+    unsigned long long* keys64;  // workspace [B][Hkv][stride]: 64-bit scores, as ordered keys
     float* scores;       // workspace [B][Hkv][stride]
-    uint32_t* tile_max;  // workspace [B][Hkv][tiles]: bits of the largest |bound| of a tile
-    int tiles;
+    uint4* stats;        // workspace [B][Hkv][tiles]: what a tile of scores leaves for the choice
+    int tiles, tile_pages;  // a score CTA takes tile_pages pages (set by the launch)
     uint32_t* status;
 };
-// pages of one score CTA
-constexpr int kSelectTile = 128;
 cudaError_t launch_select(const SelectArgs& a, bool bf16, int head_dim, cudaStream_t stream);
 
 struct SelectedParams {

@@ -169,11 +169,12 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
-    const int ctas = a.n_tokens > 0 ? (a.n_tokens + kTokensPerCta - 1) / kTokensPerCta : 1;
+    const int ctas = a.n_tokens > 0 ? 1 + (a.n_tokens - 1) / kTokensPerCta : 1;
     const size_t smem = (size_t)(2 * a.batch + 1) * 4;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxTableBatch + 1) * 4);
+        static SmemLimit limit;
+        const cudaError_t e = limit.set(reinterpret_cast<const void*>(tables_kernel),
+                                        (2 * kMaxTableBatch + 1) * 4);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(tables_kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
