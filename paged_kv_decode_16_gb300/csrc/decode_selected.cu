@@ -443,7 +443,7 @@ cudaError_t launch(const SelectedParams& p, const CUtensorMap& kmap, const CUten
                    cudaStream_t stream) {
     const long long units = (long long)p.batch * p.n_kv_heads * p.head_blocks;
     const int sms = sm_count();
-    if (units > sms) return launch_clusters<T, D, HT, 4, 2>(p, kmap, vmap, 1, stream);
+    if (units > sms) return launch_clusters<T, D, HT, 6, 2>(p, kmap, vmap, 1, stream);
     const long long pages = p.max_pages < p.table_stride ? p.max_pages : p.table_stride;
     const long long chunks = pages * (p.page_size / kChunk);
     // steps of a warp, and the cluster's merge, which costs about as much as one
