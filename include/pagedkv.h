@@ -754,7 +754,8 @@ pkv_status paged_decode_step_kv8(const void* k_new, const void* v_new, const int
  * its tokens do not fit the table row or the n_tokens rows (PKV_DEV_BAD_LEN;
  * a negative length counts as 0), or when the free pages run out before all
  * that it needs (PKV_DEV_NO_PAGES); later requests that need no page, or, in
- * the first case, whose own tokens fit, still get theirs.  A page id outside
+ * the first case, whose own tokens fit, still get theirs.  A free_begin outside
+ * [0, n_free_pages] leaves no pages (PKV_DEV_NO_PAGES).  A page id outside
  * [0, num_pages) gives its tokens slot -1 (PKV_DEV_BAD_PAGE).  query_starts
  * stops at n_tokens.  batch at most 16384 (UNSUPPORTED), outputs must not
  * overlap inputs or one another (ALIAS).  One launch. */
@@ -819,8 +820,8 @@ pkv_status pkv_rope_init(pkv_rope* out, int rotary_dim, double theta, int interl
  * rope NULL: k_new is copied bit for bit; q, q_out, positions and the norm
  * weights must be NULL.
  *
- * Strides: multiples of 8 elements, at least a token's heads * head_dim
- * (INVALID_ARG).  8-bit pool, rotary_dim above head_dim, or more than 4096 rows a
+ * Strides: multiples of 8 elements, at least a token's heads * head_dim, at most
+ * 2^30 (INVALID_ARG).  8-bit pool, rotary_dim above head_dim, or more than 4096 rows a
  * token (n_q_heads + 2 n_kv_heads): UNSUPPORTED.  q_out
  * or the pools over an input: ALIAS.  n_tokens = 0 launches nothing, else one
  * launch. */
@@ -842,8 +843,8 @@ pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_s
  * it behind the append of the same slots; a page's tokens have to be one run,
  * in ascending order, in one call (else the page's bounds are those of one of
  * its runs).  Rows behind x are not read; a page whose tokens are taken back
- * keeps its (then wider) bounds until a row of it is written again.  8-bit pool: UNSUPPORTED; bounds over
- * the pool or the slots: ALIAS.  One launch. */
+ * keeps its (then wider) bounds until a row of it is written again.  8-bit
+ * pool: UNSUPPORTED; bounds over the pool or the slots: ALIAS.  One launch. */
 pkv_status kv_page_bounds(const pkv_pool* pool, const int64_t* slots, int n_tokens, void* bounds,
                           uint32_t* dev_status, pkv_stream stream);
 
@@ -860,9 +861,10 @@ pkv_status paged_select_workspace_size(int batch, int n_kv_heads, int table_stri
  * (lo, hi: kv_page_bounds of the page), which no q . k of the page exceeds.
  * Equal scores: the lower index first; a NaN score is the highest.  selected
  * int32 [batch][n_kv_heads][max_pages] (device): the indexes into the request's
- * table row in ascending order, -1 behind them.  The choice is that of scores
- * in 64 bits: pages whose 32-bit scores are too close to the border to tell are
- * scored again in 64.
+ * table row in ascending order, -1 behind them.  The choice does not depend on
+ * how a sum is rounded to 32 bits: pages whose 32-bit scores are too close to the
+ * border to tell are scored again to 47 bits of the sum of its terms' sizes, and in
+ * 64-bit floats where 32-bit ones would overflow or lose the terms.
  *
  * q [batch][n_q_heads][head_dim] and bounds in dtype; page_table, context_lens
  * as for the decode (device).  A page id outside [0, num_pages) scores -inf

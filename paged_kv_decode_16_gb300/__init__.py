@@ -1092,8 +1092,6 @@ def _on(dev, *tensors) -> bool:
 
 
 def _status_word(dev_status, dev):
-    if dev_status is None:
-        return None
     if not (dev_status.get_device() == dev and dev_status.dtype is _I32
             and dev_status.numel() >= 1 and dev_status.is_contiguous()):
         _dev(dev_status, "dev_status", _I32)
@@ -1145,12 +1143,14 @@ def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
         raise ValueError("positions, seq_ids and slots must be [tokens]")
     if free_end.numel() != 1 or (free_begin is not None and free_begin.numel() != 1):
         raise ValueError("free_begin and free_end must hold one int32")
-    _check(load_library().paged_tables_build(
+    code = (_lib or load_library()).paged_tables_build(
         cached_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
-        _ptr(free_begin), free_end.data_ptr(), int(page_size), int(num_pages),
-        page_table.data_ptr(), cols, context_lens.data_ptr(), query_starts.data_ptr(), N,
-        positions.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(), _status_word(dev_status, dev),
-        _current(stream, dev)), "paged_tables_build")
+        _ptr(free_begin), free_end.data_ptr(), page_size, num_pages, page_table.data_ptr(), cols,
+        context_lens.data_ptr(), query_starts.data_ptr(), N, positions.data_ptr(),
+        seq_ids.data_ptr(), slots.data_ptr(),
+        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    if code:
+        _check(code, "paged_tables_build")
 
 
 class _RopeStruct(ctypes.Structure):
@@ -1255,11 +1255,12 @@ def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots
             if q is None and q_norm_weight is not None:
                 raise ValueError("q_norm_weight needs q")
             _norm_weights(q_norm_weight, k_norm_weight, dt, D)
-    _check(load_library().kv_append_tokens(
+    code = (_lib or load_library()).kv_append_tokens(
         pool.handle, k_new.data_ptr(), ks, v_new.data_ptr(), vs, slots.data_ptr(), N, qp, qs, Hq,
         _ptr(positions), None if rope is None else rope._p, _ptr(q_norm_weight),
-        _ptr(k_norm_weight), float(norm_eps), op, os_, _status_word(dev_status, dev),
-        _current(stream, dev)), "kv_append_tokens")
+        _ptr(k_norm_weight), norm_eps, op, os_, None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    if code:
+        _check(code, "kv_append_tokens")
     return q_out
 
 
@@ -1275,9 +1276,11 @@ def kv_page_bounds(pool: Pool, slots: torch.Tensor, bounds: torch.Tensor,
         raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
     if bounds.shape != (pool.num_pages, pool.n_kv_heads, 2, pool.head_dim):
         raise ValueError("bounds must be [num_pages, Hkv, 2, D] matching the pool")
-    _check(load_library().kv_page_bounds(pool.handle, slots.data_ptr(), slots.shape[0],
-                                         bounds.data_ptr(), _status_word(dev_status, dev),
-                                         _current(stream, dev)), "kv_page_bounds")
+    code = (_lib or load_library()).kv_page_bounds(
+        pool.handle, slots.data_ptr(), slots.shape[0], bounds.data_ptr(),
+        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    if code:
+        _check(code, "kv_page_bounds")
     return bounds
 
 
@@ -1346,11 +1349,13 @@ def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
     NP, Hkv, two, D2 = bounds.shape
     if two != 2 or D2 != D or heads != Hkv:
         raise ValueError("bounds must be [num_pages, Hkv, 2, D] and selected [B, Hkv, max_pages]")
-    _check(load_library().paged_select_pages(
+    code = (_lib or load_library()).paged_select_pages(
         q.data_ptr(), bounds.data_ptr(), page_table.data_ptr(), cols, context_lens.data_ptr(), B,
-        Hq, Hkv, D, int(page_size), NP, dt, int(keep_first), int(keep_last), keep,
+        Hq, Hkv, D, page_size, NP, dt, keep_first, keep_last, keep,
         selected.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _status_word(dev_status, dev), _current(stream, dev)), "paged_select_pages")
+        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    if code:
+        _check(code, "paged_select_pages")
     return selected
 
 
@@ -1372,11 +1377,13 @@ def paged_decode_attention_selected(q: torch.Tensor, k_pool: torch.Tensor, v_poo
         raise ValueError("q/out [B, Hq, D] and pools [NP, Hkv, P, D] disagree")
     if heads != Hkv:
         raise ValueError("selected must be [B, Hkv, max_pages]")
-    _check(load_library().paged_decode_attention_selected(
+    code = (_lib or load_library()).paged_decode_attention_selected(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), cols,
         context_lens.data_ptr(), selected.data_ptr(), keep, B, Hq, Hkv, D, P, NP, dt,
-        float(scale), out.data_ptr(), _status_word(dev_status, dev), _current(stream, dev)),
-        "paged_decode_attention_selected")
+        scale, out.data_ptr(), None if dev_status is None else _status_word(dev_status, dev),
+        _current(stream, dev))
+    if code:
+        _check(code, "paged_decode_attention_selected")
     return out
 
 

@@ -239,7 +239,7 @@ pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_s
     if (!k_new || !v_new || !slots || (rope && !positions)) return PKV_ERR_INVALID_ARG;
     const int64_t kv_row = (int64_t)pool->n_kv_heads * D, q_row = (int64_t)n_q_heads * D;
     auto bad_stride = [](int64_t s, int64_t row) {
-        return s < row || s % 8 != 0 || s > (int64_t(1) << 40);
+        return s < row || s % 8 != 0 || s > (int64_t(1) << 30);
     };
     if (bad_stride(k_stride, kv_row) || bad_stride(v_stride, kv_row) ||
         (q && (bad_stride(q_stride, q_row) || bad_stride(q_out_stride, q_row))))

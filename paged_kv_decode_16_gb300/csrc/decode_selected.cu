@@ -83,7 +83,7 @@ __device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint
 }
 
 template <typename T, int D, int HT, int kWarps, int kStages>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 1 : 2)
 selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
     using Lay = SelLayout<D, HT, kWarps, kStages>;
@@ -106,8 +106,10 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
         for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
         fence_barrier_init();
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap))
+                     : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap))
+                     : "memory");
     }
     __syncwarp();
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
@@ -160,13 +162,14 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
         *row = (int)(((long long)page * p.n_kv_heads + h) * P + part * kChunk);
         *used = (int)min(left, (long long)kChunk);
     };
-    int row_a, used_a, row_b, used_b;  // chunks base .. base + 31 and the 32 behind them
+    int row_a, used_a, row_b, used_b;  // the 32 chunks from `at` on and the 32 behind them
     describe(lane, &row_a, &used_a);
     describe(32 + lane, &row_b, &used_b);
 
     uint32_t qb[HT][KSTEPS][2];  // B fragments of Q^T: heads as columns
     {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + q_row * D);
+        const uint32_t* q =
+            reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + q_row * D);
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
@@ -179,13 +182,24 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     }
 
     const uint64_t policy = l2_evict_first_policy();
-    int base_i = 0;  // row_a is of chunks base_i .. base_i + 31
-    auto issue = [&](int i) {
-        const int at = i - base_i;  // < 64
-        const int ra = __shfl_sync(kFull, row_a, at & 31), rb = __shfl_sync(kFull, row_b, at & 31);
-        const int y = at < 32 ? ra : rb;
-        if (lane == 0 && y >= 0) {
-            const int st = i % kStages;
+    int at = 0, issued = 0;
+    uint32_t todo = __ballot_sync(kFull, row_a >= 0);  // chunks of row_a not on their way yet
+    uint32_t used_st = 0;                              // tokens in use of each stage, 5 bits each
+    // Bring in the next chunk that has tokens; false when there is none.
+    auto issue = [&]() {
+        while (todo == 0) {
+            at += 32;
+            if (at >= mine) return false;
+            row_a = row_b;
+            used_a = used_b;
+            todo = __ballot_sync(kFull, row_a >= 0);
+            describe(at + 32 + lane, &row_b, &used_b);
+        }
+        const int from = __ffs(todo) - 1, st = issued % kStages;
+        todo &= todo - 1;
+        const int y = __shfl_sync(kFull, row_a, from), used = __shfl_sync(kFull, used_a, from);
+        used_st = (used_st & ~(31u << 5 * st)) | (uint32_t)used << 5 * st;
+        if (lane == 0) {
             uint8_t* stage = ring + st * Lay::kStageBytes;
             fence_proxy_async_smem();
             mbar_arrive_expect_tx(&bar[st], Lay::kStageBytes);
@@ -195,12 +209,12 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
                 tma_load_2d_hint(stage + (Lay::kBoxes + bx) * Lay::kBoxBytes, &vmap, bx * 64, y,
                                  &bar[st], policy);
             }
-        } else if (lane == 0) {
-            mbar_arrive(&bar[i % kStages]);
         }
+        ++issued;
+        return true;
     };
-    int issued = 0;
-    while (issued < kStages && issued < mine) issue(issued++);
+    while (issued < kStages && issue()) {
+    }
 
     // O^T: rows d = 16 dt + g_lo and + 8, columns heads 8 ht + tq and + 1.  m: the maxima of
     // those two heads, l: this lane's part of their sums.
@@ -216,9 +230,9 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     }
     const int mi = lane >> 3, rr = lane & 7;
 
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0; i < issued; ++i) {
         const int st = i % kStages;
-        const int used = __shfl_sync(kFull, used_a, i - base_i);
+        const int used = (int)(used_st >> 5 * st & 31u);
         if (!mbar_wait_bounded(&bar[st], (uint32_t)((i / kStages) & 1))) {
             // a copy never landed: report it, wait (bounded) for those in flight
             if (lane == 0) set_status(p.status, PKV_DEV_TIMEOUT);
@@ -226,96 +240,88 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
                 mbar_wait_bounded(&bar[j % kStages], (uint32_t)((j / kStages) & 1));
             break;
         }
-        if (used > 0) {
-            const uint32_t kst = ring_u32 + st * Lay::kStageBytes;
-            const uint32_t vst = kst + Lay::kBoxes * Lay::kBoxBytes;
-            if (used < kChunk) {
-                // V rows behind the sequence's end may hold anything
-                uint4* v = reinterpret_cast<uint4*>(ring + st * Lay::kStageBytes +
-                                                    Lay::kBoxes * Lay::kBoxBytes);
-                for (int z = lane; z < (kChunk - used) * 8 * Lay::kBoxes; z += 32) {
-                    const int bx = z / ((kChunk - used) * 8), rem = z - bx * (kChunk - used) * 8;
-                    v[(bx * Lay::kBoxBytes + (used + rem / 8) * 128) / 16 + (rem & 7)] =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                __syncwarp();
+        const uint32_t kst = ring_u32 + st * Lay::kStageBytes;
+        const uint32_t vst = kst + Lay::kBoxes * Lay::kBoxBytes;
+        if (used < kChunk) {
+            // V rows behind the sequence's end may hold anything
+            uint4* v = reinterpret_cast<uint4*>(ring + st * Lay::kStageBytes +
+                                                Lay::kBoxes * Lay::kBoxBytes);
+            for (int z = lane; z < (kChunk - used) * 8 * Lay::kBoxes; z += 32) {
+                const int bx = z / ((kChunk - used) * 8), rem = z - bx * (kChunk - used) * 8;
+                v[(bx * Lay::kBoxBytes + (used + rem / 8) * 128) / 16 + (rem & 7)] =
+                    make_uint4(0u, 0u, 0u, 0u);
             }
-            // S^T = K Q^T: tokens are the rows, even and odd k-steps in chains of their own
-            float s[HT][2][4] = {};
+            __syncwarp();
+        }
+        // S^T = K Q^T: tokens are the rows, even and odd k-steps in chains of their own
+        float s[HT][2][4] = {};
 #pragma unroll
-            for (int kk = 0; kk < KSTEPS; ++kk) {
-                const int d = kk * 16 + (mi >> 1) * 8;
-                uint32_t ka[4];
-                ldsm_x4(kst + (d / 64) * Lay::kBoxBytes + swz128((mi & 1) * 8 + rr, (d % 64) / 8), ka);
+        for (int kk = 0; kk < KSTEPS; ++kk) {
+            const int d = kk * 16 + (mi >> 1) * 8;
+            uint32_t ka[4];
+            ldsm_x4(kst + (d / 64) * Lay::kBoxBytes + swz128((mi & 1) * 8 + rr, (d % 64) / 8), ka);
 #pragma unroll
-                for (int ht = 0; ht < HT; ++ht)
-                    Mma<T>::run(s[ht][kk & 1], ka, qb[ht][kk][0], qb[ht][kk][1]);
+            for (int ht = 0; ht < HT; ++ht)
+                Mma<T>::run(s[ht][kk & 1], ka, qb[ht][kk][0], qb[ht][kk][1]);
+        }
+        uint32_t pb[HT][2], pl[HT][2];  // B fragments of P^T (and of what its bf16s leave)
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+            float e[4], alpha[2];  // e: (token g_lo, heads tq, tq + 1), (token g_lo + 8, ..)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float v = (s[ht][0][x] + s[ht][1][x]) * p.scale_log2;
+                e[x] = g_lo + (x & 2) * 4 < used ? v : -INFINITY;
             }
-            uint32_t pb[HT][2], pl[HT][2];  // B fragments of P^T (and of what its bf16s leave)
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht) {
-                float e[4], alpha[2];  // e: (token g_lo, heads tq, tq + 1), (token g_lo + 8, ..)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float v = (s[ht][0][x] + s[ht][1][x]) * p.scale_log2;
-                    e[x] = g_lo + (x & 2) * 4 < used ? v : -INFINITY;
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(e[c], e[2 + c]);
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                    const float m_new = fmaxf(m[ht][c], mx);
-                    const float ref = m_new == -INFINITY ? 0.f : m_new;
-                    alpha[c] = fast_exp2(m[ht][c] - ref);
-                    e[c] = fast_exp2(e[c] - ref);
-                    e[2 + c] = fast_exp2(e[2 + c] - ref);
-                    l[ht][c] = fmaf(l[ht][c], alpha[c], e[c] + e[2 + c]);
-                    m[ht][c] = m_new;
-                }
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    o[ht][dt][0] *= alpha[0];
-                    o[ht][dt][1] *= alpha[1];
-                    o[ht][dt][2] *= alpha[0];
-                    o[ht][dt][3] *= alpha[1];
-                }
-                if constexpr (kSplitP) {
-                    split_bf16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
-                    split_bf16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
-                } else {
-                    split_f16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
-                    split_f16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    pb[ht][x] = transpose8(pb[ht][x]);
-                    pl[ht][x] = transpose8(pl[ht][x]);
-                }
+            for (int c = 0; c < 2; ++c) {
+                float mx = fmaxf(e[c], e[2 + c]);
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                const float m_new = fmaxf(m[ht][c], mx);
+                const float ref = m_new == -INFINITY ? 0.f : m_new;
+                alpha[c] = fast_exp2(m[ht][c] - ref);
+                e[c] = fast_exp2(e[c] - ref);
+                e[2 + c] = fast_exp2(e[2 + c] - ref);
+                l[ht][c] = fmaf(l[ht][c], alpha[c], e[c] + e[2 + c]);
+                m[ht][c] = m_new;
             }
-            // O^T += V^T P^T, P as a high part and the rest: two products
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
-                const int d = dt * 16 + (mi & 1) * 8;
-                uint32_t va[4];
-                ldsm_x4_trans(vst + (d / 64) * Lay::kBoxBytes + swz128((mi >> 1) * 8 + rr, (d % 64) / 8),
-                              va);
+                o[ht][dt][0] *= alpha[0];
+                o[ht][dt][1] *= alpha[1];
+                o[ht][dt][2] *= alpha[0];
+                o[ht][dt][3] *= alpha[1];
+            }
+            if constexpr (kSplitP) {
+                split_bf16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
+                split_bf16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
+            } else {
+                split_f16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
+                split_f16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
+            }
 #pragma unroll
-                for (int ht = 0; ht < HT; ++ht) {
-                    Mma<T>::run(o[ht][dt], va, pb[ht][0], pb[ht][1]);
-                    Mma<T>::run(o[ht][dt], va, pl[ht][0], pl[ht][1]);
-                }
+            for (int x = 0; x < 2; ++x) {
+                pb[ht][x] = transpose8(pb[ht][x]);
+                pl[ht][x] = transpose8(pl[ht][x]);
+            }
+        }
+        // O^T += V^T P^T, P as a high part and the rest: two products
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+            const int d = dt * 16 + (mi & 1) * 8;
+            uint32_t va[4];
+            const int tok = (mi >> 1) * 8 + rr;
+            ldsm_x4_trans(vst + (d / 64) * Lay::kBoxBytes + swz128(tok, (d % 64) / 8), va);
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) {
+                Mma<T>::run(o[ht][dt], va, pb[ht][0], pb[ht][1]);
+                Mma<T>::run(o[ht][dt], va, pl[ht][0], pl[ht][1]);
             }
         }
         __syncwarp();
-        if (issued < mine) issue(issued++);
-        if (i + 1 - base_i == 32) {
-            base_i += 32;
-            row_a = row_b;
-            used_a = used_b;
-            describe(base_i + 32 + lane, &row_b, &used_b);
-        }
+        issue();
     }
     if (bits) set_status(p.status, bits);
 
@@ -344,6 +350,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     }
     __syncthreads();
     T* out = static_cast<T*>(p.out) + q_row * D;
+    float* s_cta = s_o + kWarps * Lay::kStateFloats;  // the CTA's state
     auto weight = [](float m, float top) {  // of a state with maximum m among maxima up to top
         return m == -INFINITY ? 0.f : fast_exp2(m - top);
     };
@@ -357,8 +364,8 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = weight(s_m[w * 32 + g], top);
-            const float4 x =
-                *reinterpret_cast<const float4*>(s_o + w * Lay::kStateFloats + g * Lay::kRowFloats + c);
+            const float4 x = *reinterpret_cast<const float4*>(s_o + w * Lay::kStateFloats +
+                                                              g * Lay::kRowFloats + c);
             sum = fmaf(f, s_m[w * 32 + 16 + g], sum);
             acc.x = fmaf(f, x.x, acc.x);
             acc.y = fmaf(f, x.y, acc.y);
@@ -370,7 +377,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
             *reinterpret_cast<uint2*>(out + g * D + c) = make_uint2(
                 Cvt<T>::pack2(acc.x * inv, acc.y * inv), Cvt<T>::pack2(acc.z * inv, acc.w * inv));
         } else {
-            *reinterpret_cast<float4*>(s_o + kWarps * Lay::kStateFloats + g * Lay::kRowFloats + c) = acc;
+            *reinterpret_cast<float4*>(s_cta + g * Lay::kRowFloats + c) = acc;
             if (c == 0) {
                 s_m[kWarps * 32 + g] = top;
                 s_m[kWarps * 32 + 16 + g] = sum;
@@ -381,7 +388,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     // ---- the CTAs' states: each CTA writes its share of the outputs ----
     cluster_arrive();
     cluster_wait();
-    const uint32_t my_o = smem_u32(s_o + kWarps * Lay::kStateFloats);
+    const uint32_t my_o = smem_u32(s_cta);
     const uint32_t my_m = smem_u32(s_m + kWarps * 32);
     for (int z = rank * kWarps * 32 + threadIdx.x; z < rows * (D / 4);
          z += ranks * kWarps * 32) {
@@ -434,10 +441,11 @@ cudaError_t launch_clusters(const SelectedParams& p, const CUtensorMap& kmap,
 
 // Up to a CTA an SM, the time is that of a warp's chunks one after another: eight warps a
 // CTA with three stages each (all of an SM's shared memory), and as many CTAs a unit as fit.
-// Beyond it, bytes in flight count, and a second wave costs: four warps with two stages,
-// three CTAs an SM.  us a call, bf16, D 128, group 4, eight warps / four (best cluster size
-// of each): 8 units of 256 chunks 7.7 / 9.4, 64 units 20.0 / 24.6, 152 units 46.2 / 48.9,
-// 192 units 66.5 / 58.5; 152 units of 16 chunks 4.7 / 5.6, 192 units 8.5 / 6.2.
+// Beyond it, bytes in flight count, and a second wave costs: six warps with two stages, two
+// CTAs an SM.  us a call, bf16, D 128, group 4, eight warps / six: 192 units of 64 chunks
+// 19.5 / 18.0, of 16 chunks 8.5 / 6.1; 256 units of 64 chunks 22.2 / 20.0; and against four
+// warps (the cluster size that suits each): 8 units of 256 chunks 7.7 / 9.4, 64 units 20.0 /
+// 24.6, 152 units 46.2 / 48.9.
 template <typename T, int D, int HT>
 cudaError_t launch(const SelectedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t stream) {

@@ -53,7 +53,8 @@ struct Abs2<__half> {
 template <typename T>
 __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
     using V = typename Abs2<T>::V;
-    const V r = __hmax2_nan(*reinterpret_cast<const V*>(&m), __habs2(*reinterpret_cast<const V*>(&x)));
+    const V a = __habs2(*reinterpret_cast<const V*>(&x));
+    const V r = __hmax2_nan(*reinterpret_cast<const V*>(&m), a);
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -113,7 +114,8 @@ __device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, in
         for (int u = 0; u < D / 32; ++u) {
             // as the product does it: both halves, one of them with a zero
             const bool neg = signbit(x[u]);
-            sum += (double)(neg ? x[u] : 0.f) * (double)lo[u] + (double)(neg ? 0.f : x[u]) * (double)hi[u];
+            sum += (double)(neg ? x[u] : 0.f) * (double)lo[u];
+            sum += (double)(neg ? 0.f : x[u]) * (double)hi[u];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
@@ -621,8 +623,9 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a, 
     const int n = pages_of(a, b, &bits);  // (flagged by the scores' kernel)
     if (list_kept(a, n, out, kPickThreads, true)) return;
     pick<T, D, kPickThreads>(a, b, h, a.keep_first, n - a.keep_first - a.keep_last,
-                             a.max_pages - a.keep_first - a.keep_last, out, a.stats + unit * a.tiles,
-                             (n + a.tile_pages - 1) / a.tile_pages, s_sc, cache, sh);
+                             a.max_pages - a.keep_first - a.keep_last, out,
+                             a.stats + unit * a.tiles, (n + a.tile_pages - 1) / a.tile_pages, s_sc,
+                             cache, sh);
 }
 
 // Both in one CTA.

@@ -25,7 +25,8 @@ def close(got, ref, bound, what=""):
     if bad.any():
         i = tuple(int(x) for x in bad.nonzero()[0])
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {i}: "
-                             f"{got[i].item()!r} for {ref[i].item()!r}, bound {bound[i].item():.3g}")
+                             f"{got[i].item()!r} for {ref[i].item()!r}, bound "
+                             f"{bound[i].item():.3g}")
 
 
 def tables(cached, new, free, begin, table, page, num_pages, n_tokens):

@@ -811,3 +811,199 @@ def test_binding_refusals():
                dict(cached_lens=n.cpu()), dict(free_begin=n)):
         with pytest.raises((ValueError, TypeError)):
             pkv.paged_tables_build(**dict(good, **kw))
+
+
+# ---------------------------------------------------------------------------
+# the ends of the ranges
+# ---------------------------------------------------------------------------
+def test_offsets_beyond_32_bits():
+    """A pool of 2.4e9 elements a side: rows of its last pages are written, bounded,
+    selected and attended to at their own places."""
+    NP, hkv, page, d = 9200, 8, 256, 128
+    assert NP * hkv * page * d > 2 ** 31
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    k_pool = torch.empty(NP, hkv, page, d, dtype=BF16, device=DEV)
+    v_pool = torch.empty_like(k_pool)
+    pool = pkv.kv_pool_create(NP, page, hkv, d, BF16, k_pool, v_pool)
+    table = [[NP - 1, 3, NP - 2, NP - 5, NP - 9]]
+    n = 4 * page + 100
+    slots = [table[0][t // page] * page + t % page for t in range(n)]
+    k, v = rand(gen, n, hkv, d, dtype=BF16), rand(gen, n, hkv, d, dtype=BF16)
+    q = rand(gen, n, 16, d, dtype=BF16)
+    q_out = torch.empty_like(q)
+    st = status_word()
+    pkv.kv_append_tokens(pool, k, v, i64(slots), q=q, positions=i32(list(range(n))),
+                         rope=pkv.Rope(d), q_out=q_out, dev_status=st)
+    want, err = ref.turned(k, torch.arange(n), ref.frequencies(d, 10000.0), False)
+    at = torch.tensor(slots)
+    got = k_pool[at // page, :, at % page]
+    ref.close(got, want, ref.rounded(want, err, BF16))
+    assert torch.equal(v_pool[at // page, :, at % page], v)
+    bounds = torch.zeros(NP, hkv, 2, d, dtype=BF16, device=DEV)
+    pkv.kv_page_bounds(pool, i64(slots), bounds, dev_status=st)
+    for j, p in enumerate(table[0]):
+        rows = k_pool[p, :, :min(page, n - j * page)]
+        assert torch.equal(bounds[p, :, 0], rows.amin(1))
+        assert torch.equal(bounds[p, :, 1], rows.amax(1))
+    ask = q_out[-1:]
+    sel = run_select(ask, bounds, i32(table), i32([n]), page, 3, 0, 1, st)
+    lists, _ = ref.select(ask, bounds, table, [n], page, 3, 0, 1)
+    assert sel.tolist() == lists
+    out = run_attend(ask, k_pool, v_pool, i32(table), i32([n]), sel, 0.09, st)
+    small = [[0, 1, 2, 3, 4]]  # the same pages in a small pool for the plain form
+    w, b = ref.attend(ask, k_pool[table[0]], v_pool[table[0]], small, [n], lists, 0.09)
+    ref.close(out, w, b)
+    assert st.item() == 0
+
+
+def test_append_many_tokens_and_rows():
+    """Several groups a CTA, and tokens of more rows than a group's."""
+    check_append(9001, 8, 2, 128, 16, BF16, 128, False, "none", 1.0, True, True, 21)
+    check_append(3, 900, 62, 64, 16, F16, 32, True, "none", 1.0, False, False, 22)
+    check_append(2, 2000, 1000, 64, 16, F16, 64, False, "none", 1.0, False, False, 23)
+
+
+def test_append_norm_of_one_side():
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    q, k, v = token_rows(gen, 20, 6, 2, 128, F16, True)
+    w = (1 + 0.2 * rand(gen, 128, dtype=torch.float32)).half()
+    pos = list(range(5, 25))
+    for qw, kw in ((w, None), (None, w)):
+        pool, k_pool, _ = make_pool(2, 16, 2, 128, F16)
+        q_out = torch.empty(20, 6, 128, dtype=F16, device=DEV)
+        pkv.kv_append_tokens(pool, k, v, i64(list(range(20))), q=q, positions=i32(pos),
+                             rope=pkv.Rope(64), q_out=q_out, q_norm_weight=qw, k_norm_weight=kw,
+                             norm_eps=1e-5)
+        f = ref.frequencies(64, 10000.0)
+        for got, x, weight in ((q_out, q, qw),
+                               (k_pool.transpose(1, 2).reshape(32, 2, 128)[:20], k, kw)):
+            y, err = ref.turned(x, torch.tensor(pos), f, False, 1.0, weight, 1e-5)
+            ref.close(got, y, ref.rounded(y, err, F16))
+
+
+def test_append_one_slot_twice():
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    pool, k_pool, v_pool = make_pool(1, 16, 1, 64, F16)
+    k, v = rand(gen, 2, 1, 64, dtype=F16), rand(gen, 2, 1, 64, dtype=F16)
+    pkv.kv_append_tokens(pool, k, v, i64([3, 3]))
+    vecs = k_pool[0, 0, 3].reshape(8, 8)
+    assert all(torch.equal(vecs[i], k[0, 0].reshape(8, 8)[i])
+               or torch.equal(vecs[i], k[1, 0].reshape(8, 8)[i]) for i in range(8))
+    v_pool[0, 0, 3] = -7.0
+    assert (v_pool == -7.0).all()
+
+
+def test_calls_with_no_tokens_or_requests():
+    pool, k_pool, v_pool = make_pool(4, 16, 2, 64, BF16)
+    k = torch.empty(0, 2, 64, dtype=BF16, device=DEV)
+    none = i64([])
+    pkv.kv_append_tokens(pool, k, k, none)
+    q = torch.empty(0, 4, 64, dtype=BF16, device=DEV)
+    pkv.kv_append_tokens(pool, k, k, none, q=q, positions=i32([]), rope=pkv.Rope(64), q_out=q)
+    pkv.kv_page_bounds(pool, none, torch.zeros(4, 2, 2, 64, dtype=BF16, device=DEV))
+    t, n = i32([]).reshape(0, 3), i32([])
+    sel = torch.empty(0, 2, 5, dtype=torch.int32, device=DEV)
+    pkv.paged_select_pages(q, torch.zeros(4, 2, 2, 64, dtype=BF16, device=DEV), t, n, 16, sel,
+                           pkv.alloc_select_workspace(0, 2, 3))
+    pkv.paged_decode_attention_selected(q, k_pool, v_pool, t, n, sel, 0.1, torch.empty_like(q))
+    torch.cuda.synchronize()
+    assert (k_pool == 7.0).all() and (v_pool == -7.0).all()
+
+
+def test_select_largest_group():
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    rng = random.Random(8)
+    bounds = rand(gen, 300, 1, 2, 128, dtype=BF16).sort(2).values
+    table = page_table(rng, [16 * 300], 16, 300, 300)
+    check_select(rand(gen, 1, 192, 128, dtype=BF16), bounds, table, [16 * 300], 16, 20, 1, 1)
+    table = page_table(rng, [16 * 100], 16, 300, 100)
+    check_select(rand(gen, 1, 192, 128, dtype=BF16), bounds, table, [16 * 100], 16, 20, 1, 1)
+
+
+@pytest.mark.parametrize("cols", [40, 600, 2000])
+def test_select_many_requests(cols):
+    """Both forms of the selection over a whole grid of uneven requests."""
+    gen = torch.Generator(device=DEV).manual_seed(cols)
+    rng = random.Random(cols)
+    lens = [rng.randrange(0, 16 * cols + 1) for _ in range(12)] + [16 * cols]
+    NP = sum(-(-n // 16) for n in lens) + 2
+    bounds = rand(gen, NP, 2, 2, 64, dtype=F16).sort(2).values
+    check_select(rand(gen, 13, 8, 64, dtype=F16), bounds, page_table(rng, lens, 16, NP, cols),
+                 lens, 16, 24, 1, 2)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,dtype", [(8, 1, 128, 64, BF16), (12, 1, 64, 256, F16),
+                                                 (16, 1, 128, 128, F16), (2, 1, 64, 64, BF16)])
+def test_attend_of_few_units_over_clusters(hq, hkv, d, page, dtype):
+    """Long lists of a single request: eight CTAs merge, also in a captured call."""
+    gen = torch.Generator(device=DEV).manual_seed(hq)
+    rng = random.Random(hq)
+    n = page * 60 - 7
+    table = page_table(rng, [n], page, 62, 64)
+    k_pool, v_pool = (rand(gen, 62, hkv, page, d, dtype=dtype) for _ in range(2))
+    q = rand(gen, 1, hq, d, dtype=dtype)
+    sel = [[sorted(rng.sample(range(60), 50)) + [-1] * 3]]
+    got = check_attend(q, k_pool, v_pool, table, [n], sel, d ** -0.5)
+    t, ln, s, out = i32(table), i32([n]), i32(sel), torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.paged_decode_attention_selected(q, k_pool, v_pool, t, ln, s, d ** -0.5, out)
+    graph.replay()
+    assert torch.equal(out, got)
+    short = [[rng.sample(range(60), 1) + [-1] * 52]]
+    s.copy_(i32(short))
+    graph.replay()
+    w, b = ref.attend(q, k_pool, v_pool, table, [n], short, d ** -0.5)
+    ref.close(out, w, b)
+
+
+def test_attend_lists_that_are_mostly_empty():
+    """A list as wide as the table, with its few entries far apart."""
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    k_pool, v_pool = (rand(gen, 40, 2, 16, 64, dtype=BF16) for _ in range(2))
+    rng = random.Random(2)
+    cols = 5000
+    table = [[rng.randrange(40) for _ in range(cols)] for _ in range(2)]
+    sel = [[[-1] * cols for _ in range(2)] for _ in range(2)]
+    for b in range(2):
+        for h in range(2):
+            for j in rng.sample(range(cols), 3 * (b + h)):
+                sel[b][h][j] = j
+    q = rand(gen, 2, 8, 64, dtype=BF16)
+    check_attend(q, k_pool, v_pool, table, [16 * cols, 16 * cols - 3], sel, 0.125)
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces and outputs of their own on two streams."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    rng = random.Random(3)
+    lens = [16 * 700, 16 * 650 - 5]
+    table = page_table(rng, lens, 16, 1400, 700)
+    bounds = rand(gen, 1400, 2, 2, 128, dtype=BF16).sort(2).values
+    k_pool, v_pool = (rand(gen, 1400, 2, 16, 128, dtype=BF16) for _ in range(2))
+    qs = [rand(gen, 2, 8, 128, dtype=BF16) for _ in range(2)]
+    t, n = i32(table), i32(lens)
+    want = [ref.select(q, bounds, table, lens, 16, 40, 1, 1)[0] for q in qs]
+    sels = [torch.empty(2, 2, 40, dtype=torch.int32, device=DEV) for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    works = [pkv.alloc_select_workspace(2, 2, 700) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s, q, sel, out, ws in zip(streams, qs, sels, outs, works):
+            pkv.paged_select_pages(q, bounds, t, n, 16, sel, ws, stream=s)
+            pkv.paged_decode_attention_selected(q, k_pool, v_pool, t, n, sel, 0.09, out, stream=s)
+    torch.cuda.synchronize()
+    for q, sel, out, lists in zip(qs, sels, outs, want):
+        assert sel.tolist() == lists
+        w, b = ref.attend(q, k_pool, v_pool, table, lens, lists, 0.09)
+        ref.close(out, w, b)
+
+
+def test_selected_pool_of_8_bits_is_refused():
+    pool = pkv.kv8_pool_create(4, 16, 2, 64)
+    k = torch.zeros(1, 2, 64, dtype=BF16, device=DEV)
+    with pytest.raises(ValueError, match="16-bit"):
+        pkv.kv_append_tokens(pool, k, k, i64([0]))
+    with pytest.raises(ValueError, match="16-bit"):
+        pkv.kv_page_bounds(pool, i64([0]), torch.zeros(4, 2, 2, 64, dtype=BF16, device=DEV))

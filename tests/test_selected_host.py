@@ -121,7 +121,7 @@ def test_rope_frequencies(scaling, rdim, theta, factor, low, high, ctx):
     got = np.array(r.turns())
     # a few roundings of 2^-53 relative each, whole turns dropped
     d = (got - want) % 1.0
-    assert np.all(np.minimum(d, 1 - d) <= 16 * 2.0 ** -53 * np.maximum(want, 2.0 ** -11)), (got, want)
+    assert np.all(np.minimum(d, 1 - d) <= 16 * 2.0 ** -53 * np.maximum(want, 2.0 ** -11))
 
 
 def test_rope_scalings_keep_the_ends():
@@ -130,7 +130,8 @@ def test_rope_scalings_keep_the_ends():
     for scaling, high in (("turns", 4.0), ("index", 32.0)):
         x = np.array(pkv.Rope(128, 500000.0, scaling=scaling, factor=8.0, high_turns=high).turns())
         assert x[0] == plain[0] and abs(x[-1] * 8 / plain[-1] - 1) < 1e-12
-        assert np.all(np.diff(x) < 0) and np.all(x <= plain) and np.all(x >= plain / 8 * (1 - 1e-12))
+        assert np.all(np.diff(x) < 0)
+        assert np.all(x <= plain) and np.all(x >= plain / 8 * (1 - 1e-12))
 
 
 def _append(lib, pool, rope=True, rdim=128, **kw):
