@@ -2,7 +2,8 @@
 
 Every function here has the name of the C-ABI entry point it calls
 (``include/pagedkv.h``) and only marshals arguments: torch tensors are
-checked for device, dtype and contiguity and passed as raw device pointers;
+checked for device, dtype and contiguity and passed as raw device pointers
+(through ctypes, or for the calls with selected pages by a small native module);
 the current torch CUDA stream is passed as the stream.  All computation runs
 in the library's CUDA kernels.  There is no fallback: if the library was not
 built, or a call fails, an exception is raised.
@@ -12,6 +13,7 @@ PyTorch is used only to own device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -232,6 +234,8 @@ class Pool:
     def __init__(self, handle: int, k: torch.Tensor | None, v: torch.Tensor | None,
                  num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype):
         self._h = ctypes.c_void_p(handle)
+        self._address = handle  # of the pool (None once destroyed)
+        self.device = None
         self._keep = (k, v)
         self.num_pages, self.page_size = num_pages, page_size
         self.n_kv_heads, self.head_dim, self.dtype = n_kv_heads, head_dim, dtype
@@ -277,6 +281,7 @@ class Pool:
         if self._h:
             code = load_library().kv_pool_destroy(self._h)
             self._h = ctypes.c_void_p(None)
+            self._address = None
             self._keep = (None, None)
             _check(code, "kv_pool_destroy")
 
@@ -1078,25 +1083,26 @@ def paged_decode_step_kv8(k_new: torch.Tensor, v_new: torch.Tensor, positions: t
 
 # ---------------------------------------------------------------------------
 # Serving with selected pages: tables, appends of any tokens, page bounds, the
-# selection and the attention over it
+# selection and the attention over it.  Their arguments are checked by the
+# binding's native part (binding/calls.cpp), which raises ValueError or TypeError
+# for what it refuses and calls the entry point of the same name.
 # ---------------------------------------------------------------------------
-_I64 = torch.int64
+_calls = None
 
 
-def _on(dev, *tensors) -> bool:
-    """Contiguous tensors on device `dev` (None entries pass)."""
-    for t in tensors:
-        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
-            return False
-    return True
-
-
-def _status_word(dev_status, dev):
-    if not (dev_status.get_device() == dev and dev_status.dtype is _I32
-            and dev_status.numel() >= 1 and dev_status.is_contiguous()):
-        _dev(dev_status, "dev_status", _I32)
-        raise ValueError("dev_status must hold an int32")
-    return dev_status.data_ptr()
+def load_binding():
+    """The binding's native part (built first when missing)."""
+    global _calls
+    if _calls is None:
+        load_library()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            _build.build()
+        spec = importlib.util.spec_from_file_location("_pagedkv_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls = module
+    return _calls
 
 
 def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
@@ -1109,48 +1115,14 @@ def paged_tables_build(cached_lens: torch.Tensor, new_lens: torch.Tensor,
     their new pages in page_table [B, cols] (taken in order from free_pages,
     from entry free_begin[0] on; free_end[0] is where the next call goes on),
     context_lens [B], query_starts [B + 1], and each token row's positions,
-    seq_ids and slots [tokens] (-1 behind the last request's)."""
-    dev = -1
-    try:
-        dev = cached_lens.get_device()
-        ok = dev >= 0 and dev == _get_device() and page_table.dim() == 2
-        if ok:
-            for t in (cached_lens, new_lens, free_pages, free_end, page_table, context_lens,
-                      query_starts, positions, seq_ids):
-                if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
-                    ok = False
-            ok = (ok and slots.dtype is _I64 and slots.get_device() == dev
-                  and slots.is_contiguous()
-                  and (free_begin is None or (free_begin.dtype is _I32
-                                              and free_begin.get_device() == dev)))
-    except AttributeError:
-        ok = False
-    if not ok:
-        if free_begin is not None:
-            _dev(free_begin, "free_begin", _I32, 1)
-        _kv8_explain((cached_lens, "cached_lens", _I32, 1), (new_lens, "new_lens", _I32, 1),
-                     (free_pages, "free_pages", _I32, 1), (free_end, "free_end", _I32, 1),
-                     (page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
-                     (query_starts, "query_starts", _I32, 1), (positions, "positions", _I32, 1),
-                     (seq_ids, "seq_ids", _I32, 1), (slots, "slots", _I64, 1))
-    B, cols = page_table.shape
-    N = slots.numel()
-    if (cached_lens.numel() != B or new_lens.numel() != B or context_lens.numel() != B
-            or query_starts.numel() != B + 1):
-        raise ValueError("cached_lens, new_lens, context_lens must be [B] and query_starts "
-                         "[B + 1] for page_table [B, cols]")
-    if positions.numel() != N or seq_ids.numel() != N:
-        raise ValueError("positions, seq_ids and slots must be [tokens]")
-    if free_end.numel() != 1 or (free_begin is not None and free_begin.numel() != 1):
-        raise ValueError("free_begin and free_end must hold one int32")
-    code = (_lib or load_library()).paged_tables_build(
-        cached_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
-        _ptr(free_begin), free_end.data_ptr(), page_size, num_pages, page_table.data_ptr(), cols,
-        context_lens.data_ptr(), query_starts.data_ptr(), N, positions.data_ptr(),
-        seq_ids.data_ptr(), slots.data_ptr(),
-        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    seq_ids and slots [tokens] (-1 behind the last request's).  Everything is
+    int32 but slots (int64)."""
+    code = (_calls or load_binding()).paged_tables_build(
+        cached_lens, new_lens, free_pages, free_begin, free_end, page_table, page_size, num_pages,
+        context_lens, query_starts, positions, seq_ids, slots, dev_status,
+        None if stream is None else stream.cuda_stream)
     if code:
-        _check(code, "paged_tables_build")
+        raise PagedKVError(code, "paged_tables_build")
 
 
 class _RopeStruct(ctypes.Structure):
@@ -1190,29 +1162,6 @@ class Rope:
         return [self._s.turns[i] / 2.0 ** 64 for i in range(self._s.rotary_dim // 2)]
 
 
-def _token_rows(t, name, dev, dtype, tokens, heads, head_dim):
-    """The stride between tokens of t [tokens, heads, head_dim] on `dev`, whose
-    heads are contiguous (a slice of a fused projection may be passed)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (tokens, heads, head_dim):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] = "
-                         f"{(tokens, heads, head_dim)}, got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != head_dim and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if tokens > 1 else heads * head_dim
-
-
-def _selected_pool(pool):
-    if pool.dtype not in _DT:
-        raise ValueError("pool must be a 16-bit pool (kv_pool_create)")
-
-
 def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
                      q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
                      rope: Rope | None = None, q_out: torch.Tensor | None = None,
@@ -1223,44 +1172,12 @@ def kv_append_tokens(pool: Pool, k_new: torch.Tensor, v_new: torch.Tensor, slots
     written); with a rope, turn q [tokens, Hq, D] at positions [tokens] into
     q_out and k_new on its way, after the optional per-head RMS norms.  Rows may
     be slices of a wider tensor; q_out may be q."""
-    _selected_pool(pool)
-    _dev(slots, "slots", _I64, 1)
-    dev = slots.get_device()
-    if pool.device is not None and pool.device != dev:
-        raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
-    dt, N, D, Hkv = pool.dtype, slots.shape[0], pool.head_dim, pool.n_kv_heads
-    ks = _token_rows(k_new, "k_new", dev, dt, N, Hkv, D)
-    vs = _token_rows(v_new, "v_new", dev, dt, N, Hkv, D)
-    qs = os_ = Hq = 0
-    qp = op = None
-    if rope is None:
-        if q is not None or q_out is not None or positions is not None:
-            raise ValueError("q, q_out and positions need a rope")
-        if q_norm_weight is not None or k_norm_weight is not None:
-            raise ValueError("the norm weights need a rope")
-    else:
-        if positions is None:
-            raise ValueError("a rope needs positions")
-        _dev(positions, "positions", _I32, 1)
-        if positions.shape[0] != N:
-            raise ValueError("positions must have one entry per token")
-        if (q is None) != (q_out is None):
-            raise ValueError("give q and q_out, or neither")
-        if q is not None:
-            Hq = q.shape[1] if q.dim() == 3 else 0
-            qs = _token_rows(q, "q", dev, dt, N, Hq, D)
-            os_ = _token_rows(q_out, "q_out", dev, dt, N, Hq, D)
-            qp, op = q.data_ptr(), q_out.data_ptr()
-        if q_norm_weight is not None or k_norm_weight is not None:
-            if q is None and q_norm_weight is not None:
-                raise ValueError("q_norm_weight needs q")
-            _norm_weights(q_norm_weight, k_norm_weight, dt, D)
-    code = (_lib or load_library()).kv_append_tokens(
-        pool.handle, k_new.data_ptr(), ks, v_new.data_ptr(), vs, slots.data_ptr(), N, qp, qs, Hq,
-        _ptr(positions), None if rope is None else rope._p, _ptr(q_norm_weight),
-        _ptr(k_norm_weight), norm_eps, op, os_, None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    code = (_calls or load_binding()).kv_append_tokens(
+        pool._address, pool.device, k_new, v_new, slots, q, positions,
+        None if rope is None else rope._p, q_out, q_norm_weight, k_norm_weight, norm_eps,
+        dev_status, None if stream is None else stream.cuda_stream)
     if code:
-        _check(code, "kv_append_tokens")
+        raise PagedKVError(code, "kv_append_tokens")
     return q_out
 
 
@@ -1268,19 +1185,11 @@ def kv_page_bounds(pool: Pool, slots: torch.Tensor, bounds: torch.Tensor,
                    dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The smallest and largest key, element by element, of every page that holds
     one of slots [tokens], into bounds [num_pages, Hkv, 2, D]."""
-    _selected_pool(pool)
-    _dev(slots, "slots", _I64, 1)
-    _dev(bounds, "bounds", pool.dtype, 4)
-    dev = slots.get_device()
-    if pool.device is not None and pool.device != dev:
-        raise ValueError(f"pool is on cuda:{pool.device} but slots is on cuda:{dev}")
-    if bounds.shape != (pool.num_pages, pool.n_kv_heads, 2, pool.head_dim):
-        raise ValueError("bounds must be [num_pages, Hkv, 2, D] matching the pool")
-    code = (_lib or load_library()).kv_page_bounds(
-        pool.handle, slots.data_ptr(), slots.shape[0], bounds.data_ptr(),
-        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    code = (_calls or load_binding()).kv_page_bounds(
+        pool._address, pool.device, slots, bounds, dev_status,
+        None if stream is None else stream.cuda_stream)
     if code:
-        _check(code, "kv_page_bounds")
+        raise PagedKVError(code, "kv_page_bounds")
     return bounds
 
 
@@ -1299,37 +1208,6 @@ def alloc_select_workspace(batch: int, n_kv_heads: int, table_cols: int,
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def _selected_call(q, page_table, context_lens, selected, others, names):
-    """(current device, B, Hq, D, table columns, dtype code) of checked arguments;
-    others: the call's other tensors, of q's dtype, as named."""
-    dev = -1
-    try:
-        dev = q.get_device()
-        dtype = q.dtype
-        ok = (dev >= 0 and dev == _get_device() and dtype in _DT and q.is_contiguous()
-              and q.dim() == 3 and page_table.dim() == 2 and selected.dim() == 3)
-        if ok:
-            for t in (page_table, context_lens, selected):
-                if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
-                    ok = False
-            for t in others:
-                if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-                    ok = False
-    except AttributeError:
-        ok = False
-    if not ok:
-        _dev(q, "q", None, 3)
-        _dtype_code(q)
-        _kv8_explain((page_table, "page_table", _I32, 2), (context_lens, "context_lens", _I32, 1),
-                     (selected, "selected", _I32, 3),
-                     *((t, n, q.dtype) for t, n in zip(others, names)))
-    B, Hq, D = q.shape
-    rows, cols = page_table.shape
-    if rows != B or context_lens.numel() != B or selected.shape[0] != B:
-        raise ValueError("page_table rows, context_lens or selected != batch")
-    return dev, B, Hq, D, cols, _DT[dtype]
-
-
 def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor,
                        context_lens: torch.Tensor, page_size: int, selected: torch.Tensor,
                        workspace: torch.Tensor, keep_first: int = 1, keep_last: int = 1,
@@ -1338,24 +1216,11 @@ def paged_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
     keep_first, the last keep_last and those of the highest score by bounds
     [num_pages, Hkv, 2, D], into selected [B, Hkv, max_pages] (indexes into the
     rows of page_table, ascending, -1 behind them)."""
-    dev, B, Hq, D, cols, dt = _selected_call(q, page_table, context_lens, selected, (bounds,),
-                                             ("bounds",))
-    if (workspace.dtype is not torch.uint8 or workspace.get_device() != dev
-            or not workspace.is_contiguous()):
-        _kv8_explain((workspace, "workspace", torch.uint8))
-    _, heads, keep = selected.shape
-    if bounds.dim() != 4:
-        _kv8_explain((bounds, "bounds", q.dtype, 4))
-    NP, Hkv, two, D2 = bounds.shape
-    if two != 2 or D2 != D or heads != Hkv:
-        raise ValueError("bounds must be [num_pages, Hkv, 2, D] and selected [B, Hkv, max_pages]")
-    code = (_lib or load_library()).paged_select_pages(
-        q.data_ptr(), bounds.data_ptr(), page_table.data_ptr(), cols, context_lens.data_ptr(), B,
-        Hq, Hkv, D, page_size, NP, dt, keep_first, keep_last, keep,
-        selected.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        None if dev_status is None else _status_word(dev_status, dev), _current(stream, dev))
+    code = (_calls or load_binding()).paged_select_pages(
+        q, bounds, page_table, context_lens, page_size, selected, workspace, keep_first, keep_last,
+        dev_status, None if stream is None else stream.cuda_stream)
     if code:
-        _check(code, "paged_select_pages")
+        raise PagedKVError(code, "paged_select_pages")
     return selected
 
 
@@ -1366,24 +1231,11 @@ def paged_decode_attention_selected(q: torch.Tensor, k_pool: torch.Tensor, v_poo
                                     stream=None) -> torch.Tensor:
     """Decode attention of q [B, Hq, D] over the pages selected[b][h] (indexes into
     the rows of page_table; negative entries are skipped) into out."""
-    dev, B, Hq, D, cols, dt = _selected_call(q, page_table, context_lens, selected,
-                                             (k_pool, v_pool, out), ("k_pool", "v_pool", "out"))
-    ks = k_pool.shape
-    if len(ks) != 4:
-        _kv8_explain((k_pool, "k_pool", q.dtype, 4))
-    NP, Hkv, P, D2 = ks
-    _, heads, keep = selected.shape
-    if D2 != D or v_pool.shape != ks or out.shape != q.shape:
-        raise ValueError("q/out [B, Hq, D] and pools [NP, Hkv, P, D] disagree")
-    if heads != Hkv:
-        raise ValueError("selected must be [B, Hkv, max_pages]")
-    code = (_lib or load_library()).paged_decode_attention_selected(
-        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), cols,
-        context_lens.data_ptr(), selected.data_ptr(), keep, B, Hq, Hkv, D, P, NP, dt,
-        scale, out.data_ptr(), None if dev_status is None else _status_word(dev_status, dev),
-        _current(stream, dev))
+    code = (_calls or load_binding()).paged_decode_attention_selected(
+        q, k_pool, v_pool, page_table, context_lens, selected, scale, out, dev_status,
+        None if stream is None else stream.cuda_stream)
     if code:
-        _check(code, "paged_decode_attention_selected")
+        raise PagedKVError(code, "paged_decode_attention_selected")
     return out
 
 

@@ -1,4 +1,5 @@
-"""Build the CUDA library (libpagedkv.so) in-tree with nvcc for sm_103a.
+"""Build the CUDA library (libpagedkv.so) in-tree with nvcc for sm_103a, and the
+Python binding's native part (binding/calls.cpp) with g++ against this torch.
 
 Each translation unit is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and the objects are
@@ -16,9 +17,11 @@ import contextlib
 import fcntl
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -26,6 +29,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpagedkv.so")
+BINDING = os.path.join(HERE, "binding", "calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,11 +53,50 @@ def _inputs() -> list[str]:
         os.path.join(CSRC, "*.hpp")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
+def binding_path() -> str:
+    """The native module of the Python binding; its name holds the torch and Python
+    versions that it was built against."""
+    import torch
+    tag = re.sub(r"[^0-9A-Za-z]+", "_", f"{torch.__version__}_py{sysconfig.get_python_version()}")
+    return os.path.join(OUT_DIR, f"_pagedkv_calls_{tag}.so")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    calls = binding_path()
+    if not os.path.exists(LIB) or not os.path.exists(calls):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    header = os.path.join(INCLUDE, "pagedkv.h")
+    return all(os.path.getmtime(f) <= t for f in _inputs()) and all(
+        os.path.getmtime(f) <= os.path.getmtime(calls) for f in (BINDING, header, __file__))
+
+
+def _compile_binding(out: str) -> subprocess.CompletedProcess:
+    """g++ of binding/calls.cpp into an object (a C++ file against torch's headers)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    cmd = ["g++", "-c", BINDING, "-o", out, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    return subprocess.run(cmd, capture_output=True, text=True)
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    out = binding_path()
+    tmp = f"{out}.tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lpagedkv", "-L", libs,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stderr)
+    os.replace(tmp, out)
 
 
 @contextlib.contextmanager
@@ -96,15 +139,19 @@ def _build_locked(verbose: bool, ptxas_verbose: bool) -> str:
 
     objs = []
     errors = []
+    calls_obj = os.path.join(obj_dir, "calls.o")
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(_compile_binding, calls_obj)
         for src, obj, r in ex.map(compile_one, sources()):
             if verbose or ptxas_verbose:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
                 errors.append(f"{os.path.basename(src)}:\n{r.stderr}")
             objs.append(obj)
+        if calls.result().returncode != 0:
+            errors.append(f"calls.cpp:\n{calls.result().stderr}")
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
     # the temporary name keeps the .so suffix: nvcc picks the link step from it
     tmp = os.path.join(OUT_DIR, f"libpagedkv.tmp{os.getpid()}.so")
     cmd = [nvcc, "-shared", *ARCH, "-o", tmp, *objs]
@@ -112,6 +159,7 @@ def _build_locked(verbose: bool, ptxas_verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB)
+    _link_binding(calls_obj)
     shutil.rmtree(obj_dir, ignore_errors=True)
     return LIB
 
