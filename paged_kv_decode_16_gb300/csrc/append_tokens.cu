@@ -187,9 +187,11 @@ append_tokens_kernel(const AppendTokensArgs a, const GroupShape gs) {
 
     fill_src(blockIdx.x, 0);
     fill_src(blockIdx.x + gridDim.x, 1);
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     read_token(blockIdx.x);
+    for (int u = 0; u < depth; ++u) load();
     if (normed && tid < 2 * kTasks) {
         const T* w = static_cast<const T*>(tid < kTasks ? a.q_norm : a.k_norm);
         float f[8], h[8];
@@ -205,7 +207,6 @@ append_tokens_kernel(const AppendTokensArgs a, const GroupShape gs) {
     }
     keep_token(0);
     __syncthreads();
-    for (int u = 0; u < depth; ++u) load();
     fill(blockIdx.x, 0);
     read_token(blockIdx.x + gridDim.x);
     keep_token(1);

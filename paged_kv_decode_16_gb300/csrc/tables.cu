@@ -10,63 +10,71 @@
 // itself, in shared memory, rather than wait for another launch that does it once: the
 // lengths of 256 requests are 2 KB from L2.  No CTA reads what another one writes
 // (a request's old entries are below its new ones), so there is nothing to wait for.
+// One scan serves both sums, although a request without token rows takes no pages: the
+// requests that have rows all come before the first that has none.
 #include "selected.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokensPerCta = 1024;
 constexpr int kWarps = kThreads / 32;
 
 // Exclusive sums over the CTA of one (tokens, pages) pair a thread; totals in *all_*.
-__device__ __forceinline__ void scan2(long long& t, long long& g, long long* all_t,
-                                      long long* all_g, longlong2* s_warp) {
+template <typename S>
+__device__ __forceinline__ void scan2(S& t, S& g, S* all_t, S* all_g, S (*s_warp)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = t, y = g;
+    S x = t, y = g;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(kFull, x, o), b = __shfl_up_sync(kFull, y, o);
+        const S a = __shfl_up_sync(kFull, x, o), b = __shfl_up_sync(kFull, y, o);
         if (lane >= o) {
             x += a;
             y += b;
         }
     }
-    if (lane == 31) s_warp[warp] = make_longlong2(x, y);
+    if (lane == 31) {
+        s_warp[warp][0] = x;
+        s_warp[warp][1] = y;
+    }
     __syncthreads();
-    long long pt = 0, pg = 0, st = 0, sg = 0;
+    S pt = 0, pg = 0, st = 0, sg = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const longlong2 v = s_warp[w];
+        const S a = s_warp[w][0], b = s_warp[w][1];
         if (w < warp) {
-            pt += v.x;
-            pg += v.y;
+            pt += a;
+            pg += b;
         }
-        st += v.x;
-        sg += v.y;
+        st += a;
+        sg += b;
     }
     t = pt + x - t;
     g = pg + y - g;
     *all_t = st;
     *all_g = sg;
-    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
+// S: holds the sums of kThreads requests, each of which counts for at most n_tokens + 1 tokens
+// and as many pages.
+template <typename S>
+__global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a, int per_cta) {
     extern __shared__ int32_t smem[];
-    int32_t* s_start = smem;                 // [B + 1] first token row
-    int32_t* s_page = smem + a.batch + 1;    // [B] pages taken before the request; -1: refused
-    __shared__ longlong2 s_warp[kWarps];
+    const int B = a.batch, P = a.page_size;
+    int32_t* s_start = smem;               // [B + 1] first token row
+    int32_t* s_page = smem + B + 1;        // [B] pages taken before the request; -1: refused
+    int32_t* s_cached = s_page + B;        // [B]
+    __shared__ S s_warp[2][kWarps][2];
     __shared__ uint32_t s_status;
     __shared__ int s_taken;
-    const int B = a.batch, P = a.page_size;
     if (threadIdx.x == 0) {
         s_status = 0;
         s_taken = 0;
     }
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
-    int begin = a.free_begin ? *a.free_begin : 0;
+    const int begin = a.free_begin ? *a.free_begin : 0;
     int avail = a.n_free - begin;
     uint32_t bits = 0;
     if (begin < 0 || avail < 0) {  // no such entry: nothing is left
@@ -75,10 +83,10 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
     }
     // positions are int32: a request may end at 2^31 - 1 at most
     const long long cap = min((long long)a.table_stride * P, 0x7fffffffLL);
-    __syncthreads();
 
     long long base_t = 0, base_g = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
+    int turn = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads, turn ^= 1) {
         const int b = b0 + threadIdx.x;
         int c = 0, n = 0;
         if (b < B) {
@@ -88,34 +96,35 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
         const bool bad = c < 0 || n < 0;
         c = max(c, 0);
         n = max(n, 0);
-        const bool fits_row = (long long)c + n <= cap;
-        long long t = n, all_t, all_g;
-        const long long need_row = ((long long)c + n + P - 1) / P - ((long long)c + P - 1) / P;
-        // whether its rows exist depends on the token sum alone: sum that first
-        long long g = 0;
-        scan2(t, g, &all_t, &all_g, s_warp);
-        const long long start = base_t + t, end = start + n;
-        const bool fits = !bad && fits_row && end <= a.n_tokens;
-        const long long need = fits ? need_row : 0;
-        long long none = 0, unused;
-        g = need;
-        scan2(none, g, &unused, &all_g, s_warp);
-        const long long before = base_g + g, upto = before + need;
+        const bool fits_row = !bad && (long long)c + n <= cap;
+        // a request that is too long for the rows counts as just too long.  Its pages and
+        // those behind it may count or not: no request behind it has rows left
+        const int tokens = min(n, a.n_tokens < 0x7fffffff ? a.n_tokens + 1 : a.n_tokens);
+        // (c and n fit a row here, whose pages are an int)
+        const int need = fits_row ? (int)(((unsigned)c + (unsigned)n + P - 1) / P -
+                                          ((unsigned)c + P - 1) / P)
+                                  : 0;
+        S t = tokens, g = min(need, tokens), all_t, all_g;
+        scan2<S>(t, g, &all_t, &all_g, s_warp[turn]);
+        const long long start = base_t + (long long)t, end = start + n;
+        const long long upto = base_g + (long long)g + need;
+        const bool fits = fits_row && end <= a.n_tokens;
         const bool paid = need == 0 || upto <= avail;
         if (b < B) {
             if (!fits) bits |= PKV_DEV_BAD_LEN;
-            if (!paid) bits |= PKV_DEV_NO_PAGES;
+            else if (!paid) bits |= PKV_DEV_NO_PAGES;
             if (fits && paid && need > 0) atomicMax(&s_taken, (int)upto);
             s_start[b] = (int)min(start, (long long)a.n_tokens);
             // (a request that needs no page has no use for the count)
-            s_page[b] = fits && paid ? (need ? (int)before : 0) : -1;
+            s_page[b] = fits && paid ? (need ? (int)(upto - need) : 0) : -1;
+            s_cached[b] = c;
             if (blockIdx.x == 0) {
                 a.lens[b] = fits && paid ? c + n : c;
                 a.starts[b] = s_start[b];
             }
         }
-        base_t += all_t;
-        base_g += all_g;
+        base_t += (long long)all_t;
+        base_g += (long long)all_g;
     }
     const int total = (int)min(base_t, (long long)a.n_tokens);
     if (threadIdx.x == 0) s_start[B] = total;
@@ -125,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
         *a.free_end = begin + s_taken;
     }
 
-    const int first = blockIdx.x * kTokensPerCta;
-    const int last = min(first + kTokensPerCta, a.n_tokens);
-    for (int i = first + threadIdx.x; i < last; i += kThreads) {
+    const long long first = (long long)blockIdx.x * per_cta;
+    const int last = (int)min(first + per_cta, (long long)a.n_tokens);
+    for (int i = (int)first + threadIdx.x; i < last; i += kThreads) {
         int pos = -1, seq = -1;
         long long slot = -1;
         if (i < total) {
@@ -141,10 +150,10 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
             seq = lo;
             const int pages = s_page[seq];
             if (pages >= 0) {
-                const int c = a.cached[seq];
-                pos = c + (i - s_start[seq]);
+                const unsigned c = s_cached[seq];
+                pos = (int)c + (i - s_start[seq]);
                 const int j = pos / P, off = pos - j * P;
-                const int have = (int)(((long long)c + P - 1) / P);
+                const int have = (int)((c + P - 1) / P);
                 int32_t* entry = a.table + (long long)seq * a.table_stride + j;
                 int page;
                 if (j < have) {
@@ -169,15 +178,22 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
-    const int ctas = a.n_tokens > 0 ? 1 + (a.n_tokens - 1) / kTokensPerCta : 1;
-    const size_t smem = (size_t)(2 * a.batch + 1) * 4;
+    // a token a thread while that is a wave of four CTAs an SM, more beyond it
+    const long long tiles = a.n_tokens > 0 ? 1 + ((long long)a.n_tokens - 1) / kThreads : 1;
+    const long long wave = 4LL * sm_count();
+    const int per_cta = (int)((tiles + wave - 1) / wave) * kThreads;
+    const int ctas = a.n_tokens > 0 ? (int)(1 + ((long long)a.n_tokens - 1) / per_cta) : 1;
+    const size_t smem = (size_t)(3 * a.batch + 1) * 4;
+    // sums of kThreads requests in 32 bits
+    const bool narrow = a.n_tokens < 0x7fffffff / kThreads - 1;
+    auto kernel = narrow ? tables_kernel<int> : tables_kernel<long long>;
     if (smem > 48 * 1024) {
-        static SmemLimit limit;
-        const cudaError_t e = limit.set(reinterpret_cast<const void*>(tables_kernel),
-                                        (2 * kMaxTableBatch + 1) * 4);
+        static SmemLimit limits[2];
+        const cudaError_t e = limits[narrow].set(reinterpret_cast<const void*>(kernel),
+                                                 (3 * kMaxTableBatch + 1) * 4);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(tables_kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, per_cta);
 }
 
 }  // namespace pkv

@@ -127,6 +127,36 @@ def test_tables_largest_batch():
     assert check_tables(cached, new, ids[3 * B:], 0, table, 16, 5 * B, sum(new) + 3) == 0
 
 
+def test_tables_of_millions_of_tokens():
+    """Token sums of one round of the CTA beyond 32 bits' guard, many tokens a CTA."""
+    new, page, cols = [4000001, 0, 1, 4900000], 256, 20000
+    B, N = len(new), 9000000
+    need = [-(-n // page) for n in new]
+    order = torch.randperm(sum(need), device=DEV).to(torch.int32)
+    table = torch.full((B, cols), -1, dtype=torch.int32, device=DEV)
+    out = dict(lens=i32([0] * B), starts=i32([0] * (B + 1)), end=i32([0]),
+               pos=torch.zeros(N, dtype=torch.int32, device=DEV),
+               seq=torch.zeros(N, dtype=torch.int32, device=DEV),
+               slots=torch.zeros(N, dtype=torch.int64, device=DEV))
+    st = status_word()
+    pkv.paged_tables_build(i32([0] * B), i32(new), order, None, out["end"], table, page,
+                           sum(need), out["lens"], out["starts"], out["pos"], out["seq"],
+                           out["slots"], dev_status=st)
+    assert st.item() == 0 and out["end"].item() == sum(need) and out["lens"].tolist() == new
+    assert out["starts"].tolist() == [0, 4000001, 4000001, 4000002, sum(new)]
+    row = at = 0
+    for b, n in enumerate(new):
+        p = torch.arange(n, device=DEV)
+        pages = order[at:at + need[b]].long()
+        assert torch.equal(table[b, :need[b]].long(), pages) and (table[b, need[b]:] == -1).all()
+        assert torch.equal(out["pos"][row:row + n].long(), p)
+        assert (out["seq"][row:row + n] == b).all()
+        assert torch.equal(out["slots"][row:row + n], pages[p // page] * page + p % page)
+        row, at = row + n, at + need[b]
+    for name in ("pos", "seq", "slots"):
+        assert (out[name][row:] == -1).all()
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
