@@ -803,7 +803,7 @@ pkv_status pkv_rope_init(pkv_rope* out, int rotary_dim, double theta, int interl
  * not written; beyond the pool: PKV_DEV_BAD_PAGE and not written).  k_new, v_new
  * [n_tokens][n_kv_heads][head_dim] in the pool's dtype, tokens k_stride /
  * v_stride elements apart, heads contiguous (slices of a fused projection).
- * Two tokens with one slot leave it with either's rows.
+ * Two tokens with one slot leave it with pieces of either's rows.
  *
  * With rope non-NULL (host), q [n_tokens][n_q_heads][head_dim] (q_stride) is
  * turned at positions (int32 [n_tokens], device) into q_out (q_out_stride), and

@@ -499,6 +499,8 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
             const float s = score(i);
             return blind || (s >= lower && s <= upper);
         };
+        // (S = 0, a query or bounds of zeros: what is open is all equal)
+        auto long_key = [&](int i) { return S != 0.f ? keys64[i] : 1ull; };
         sure = 0;
         for (int w = warp; w < words; w += kWarps) {
             const int i = w * 32 + lane;
@@ -506,7 +508,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
             if (lane == 0) sh.chosen[w] = yes;
             sure += __popc(yes);
             uint32_t m = __ballot_sync(kFull, i < cn && is_open(i));
-            while (m) {
+            while (m && S != 0.f) {
                 const int at = w * 32 + __ffs(m) - 1;
                 m &= m - 1;
                 unsigned long long key = 0;
@@ -517,14 +519,14 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
         }
         left = want - cta_sum<THREADS>(lane == 0 ? sure : 0, sh.buf[turn ^= 1]);
         const unsigned long long key = kth_key<THREADS, unsigned long long>(
-            sh.buf, turn, cn, left, [&](int i) { return is_open(i) ? keys64[i] : 0ull; });
+            sh.buf, turn, cn, left, [&](int i) { return is_open(i) ? long_key(i) : 0ull; });
         int above = 0;
-        for (int i = threadIdx.x; i < cn; i += THREADS) above += is_open(i) && keys64[i] > key;
+        for (int i = threadIdx.x; i < cn; i += THREADS) above += is_open(i) && long_key(i) > key;
         int equal = left - cta_sum<THREADS>(above, sh.buf[turn ^= 1]);  // the first so many
         for (int w0 = 0; w0 < words; w0 += kWarps) {
             const int w = w0 + warp, i = w * 32 + lane;
             const bool may = i < cn && is_open(i);
-            const unsigned long long k = may ? keys64[i] : 0ull;
+            const unsigned long long k = may ? long_key(i) : 0ull;
             uint32_t take = __ballot_sync(kFull, may && k > key);
             uint32_t tie = __ballot_sync(kFull, may && k == key);
             int* buf = sh.buf[turn ^= 1];

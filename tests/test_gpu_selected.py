@@ -1030,6 +1030,28 @@ def test_two_streams_at_once():
         ref.close(out, w, b)
 
 
+def test_destroyed_pool_is_refused():
+    pool, _, _ = make_pool(4, 16, 2, 64, BF16)
+    pool.destroy()
+    k = torch.zeros(1, 2, 64, dtype=BF16, device=DEV)
+    with pytest.raises(ValueError, match="destroyed"):
+        pkv.kv_append_tokens(pool, k, k, i64([0]))
+    with pytest.raises(ValueError, match="destroyed"):
+        pkv.kv_page_bounds(pool, i64([0]), torch.zeros(4, 2, 2, 64, dtype=BF16, device=DEV))
+
+
+def test_pool_that_owns_its_memory():
+    pool = pkv.kv_pool_create(4, 16, 2, 64, BF16)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    k, v = rand(gen, 20, 2, 64, dtype=BF16), rand(gen, 20, 2, 64, dtype=BF16)
+    pkv.kv_append_tokens(pool, k, v, i64(list(range(20, 40))))
+    got = [torch.zeros(1, 2, 40, 64, dtype=BF16, device=DEV) for _ in range(2)]
+    pkv.kv_gather(pool, i32([[0, 1, 2]]), i32([40]), 40, *got)
+    assert torch.equal(got[0][0, :, 20:], k.transpose(0, 1))
+    assert torch.equal(got[1][0, :, 20:], v.transpose(0, 1))
+    pool.destroy()
+
+
 def test_selected_pool_of_8_bits_is_refused():
     pool = pkv.kv8_pool_create(4, 16, 2, 64)
     k = torch.zeros(1, 2, 64, dtype=BF16, device=DEV)

@@ -294,6 +294,19 @@ def test_attend_checks(lib, kw, code):
     assert _attend(lib, **kw) == code
 
 
+def test_native_binding_checks_its_arguments():
+    """The native part of the binding has the five calls; each wants its own number of
+    arguments and, without a GPU, raises instead of calling anything."""
+    calls = pkv.load_binding()
+    for name, n in (("paged_tables_build", 15), ("kv_append_tokens", 14), ("kv_page_bounds", 6),
+                    ("paged_select_pages", 11), ("paged_decode_attention_selected", 10)):
+        fn = getattr(calls, name)
+        with pytest.raises(TypeError, match=f"expected {n} arguments"):
+            fn(None)
+        with pytest.raises((RuntimeError, TypeError, ValueError)):
+            fn(*[None] * n)
+
+
 def test_reference_table_builder_by_hand():
     """The reference of the GPU tests on a case worked out by hand: P 16, request 0 with 15
     + 2 tokens (old page 7, new page 3), 1 idle, 2 refused (no room in its row), 3 new."""
