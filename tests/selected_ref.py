@@ -166,8 +166,8 @@ def select(q, bounds, table, lens, page, max_pages, first, last):
             if n <= max_pages:
                 take = list(range(n))
             else:
-                if any(not 0 <= p < NP for p in table[b][:n]):
-                    status |= BAD_PAGE
+                if max_pages > first + last and any(not 0 <= p < NP for p in table[b][:n]):
+                    status |= BAD_PAGE  # (looked at only where there is something to choose)
                 sc = scores(q[b, h * G:h * G + G], bounds[:, h], table[b][first:n - last], NP)
                 order = sorted(range(len(sc)),
                                key=lambda i: (0 if math.isnan(sc[i]) else 1,
