@@ -8,7 +8,8 @@
 // the contraction's order is free, so a lane takes 16 contiguous bytes of a row as its
 // fragments of two k-steps.  What bounds it: memory, 4 D bytes a page and head (256 units of
 // 8192 pages, 1.07 GB: 139 us with the choice), and for less the grid's start and the choice's
-// phases (256 uneven units of 256 to 2048 pages, 113 MB: 29.7 us, of which 8 the choice).
+// phases (256 uneven units of 256 to 2048 pages, 113 MB: 29.6 us, of which 7 the choice;
+// 256 units of 64 pages 7.6 us, of which 1.5 where scores near the border are told apart).
 //
 // The choice is that of exact scores, so that it does not depend on how a product is
 // summed.  A product of two 16-bit values is exact in fp32; each of the 2 D / 16 steps adds 16
@@ -27,6 +28,7 @@ namespace {
 constexpr int kScoreThreads = 128;
 constexpr int kPickThreads = 512;
 constexpr int kSmallThreads = 256;  // of the kernel that does both
+constexpr int kSmallPages = 512;    // and the most table columns it takes
 constexpr int kFew = 256;           // pages that are ranked by comparing all pairs
 constexpr int kBins = 1024;         // of the histogram that finds the border
 // Up to so many candidates are all ranked instead: 60 candidates 4.7 against 5.1 us a call,
@@ -79,64 +81,68 @@ __device__ __forceinline__ float score_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// A sum in two floats: hi + lo, |lo| at most half a step of hi.
-struct Two {
-    float hi, lo;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-    const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
-    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-    const Two s = two_sum(a.hi, b.hi);
-    const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
-    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
-}
-
-// The score of a page for one query head to more than 32 bits, as a key, worked out by a
-// warp (every lane gets it).  fp64 runs at a 64th of fp32's rate on this part, and a warp's
-// 8 D products of it cost 6 us beside the CTA's other warps: two floats unless they cannot
-// hold it (`wide`).
+// The score of a page for one query head to more than 32 bits, as a key, worked out by D / 8
+// lanes side by side (each gets it; page < 0: the key of -inf).  S: at least the sum of the
+// products' sizes.  fp64 runs at a 64th of fp32's rate on this part, so it serves only where
+// fp32 cannot hold the products (`wide`).  Else a product, exact in fp32, is cut at two fixed
+// bits, by adding and taking away 1.5 times a power of two: with 2^k above 2 S, the parts
+// down to 2^(k-23) add up without rounding, and so do those from there to 2^(k-39); what is
+// left is below 2^(k-40), so its rounded sum is off by 2^(k-50), 2^-48 S, at most.
 template <typename T, int D>
-__device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, int b, int h, int j,
-                                                         int i, float S, bool wide) {
-    const int lane = threadIdx.x & 31;
-    const int group = a.n_q_heads / a.n_kv_heads;
-    const int page = a.table[(long long)b * a.table_stride + j];
-    if (page < 0 || page >= a.num_pages) return key_of(-(double)INFINITY);
-    if (S == 0.f) return key_of(0.0);  // every product is a zero
-    const T* row = static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D;
-    const T* q = static_cast<const T*>(a.q) + ((long long)b * a.n_q_heads + h * group + i) * D;
-    float x[D / 32], lo[D / 32], hi[D / 32];
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-        const int d = u * 32 + lane;
-        x[u] = (float)q[d], lo[u] = (float)row[d], hi[u] = (float)row[D + d];
+__device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, int b, int h,
+                                                         int page, int head, float S, bool wide) {
+    constexpr int kLanes = D / 8;
+    const int l = threadIdx.x % kLanes;
+    const bool real = page >= 0 && page < a.num_pages;
+    uint4 xv = make_uint4(0, 0, 0, 0), lov = xv, hiv = xv;
+    if (real) {
+        const int group = a.n_q_heads / a.n_kv_heads;
+        const T* row =
+            static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D;
+        const T* q = static_cast<const T*>(a.q) +
+                     ((long long)b * a.n_q_heads + h * group + head) * D;
+        xv = reinterpret_cast<const uint4*>(q)[l];
+        lov = reinterpret_cast<const uint4*>(row)[l];
+        hiv = reinterpret_cast<const uint4*>(row + D)[l];
     }
+    float x[8], lo[8], hi[8];
+    Cvt<T>::unpack8(xv, x);
+    Cvt<T>::unpack8(lov, lo);
+    Cvt<T>::unpack8(hiv, hi);
+    double sum = 0.0;
     if (wide) {
-        double sum = 0.0;
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
+        for (int e = 0; e < 8; ++e) {
             // as the product does it: both halves, one of them with a zero
-            const bool neg = signbit(x[u]);
-            sum += (double)(neg ? x[u] : 0.f) * (double)lo[u];
-            sum += (double)(neg ? 0.f : x[u]) * (double)hi[u];
+            const bool neg = signbit(x[e]);
+            sum += (double)(neg ? x[e] : 0.f) * (double)lo[e];
+            sum += (double)(neg ? 0.f : x[e]) * (double)hi[e];
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        return key_of(sum);
-    }
-    Two sum = {0.f, 0.f};
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    } else {
+        const uint32_t top = (__float_as_uint(S) >> 23) + 2;  // 2^k: above 2 S
+        const float cut1 = __uint_as_float(top << 23 | 0x400000u);
+        const float cut2 = __uint_as_float((top - 16) << 23 | 0x400000u);
+        float s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u)  // (exact products; nothing is infinite here)
-        sum = add(sum, {__fmul_rn(x[u], signbit(x[u]) ? lo[u] : hi[u]), 0.f});
+        for (int e = 0; e < 8; ++e) {
+            const float p = __fmul_rn(x[e], signbit(x[e]) ? lo[e] : hi[e]);
+            const float p1 = __fsub_rn(__fadd_rn(p, cut1), cut1), r = __fsub_rn(p, p1);
+            const float p2 = __fsub_rn(__fadd_rn(r, cut2), cut2);
+            s1 = __fadd_rn(s1, p1);
+            s2 = __fadd_rn(s2, p2);
+            s3 = __fadd_rn(s3, __fsub_rn(r, p2));
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        // the same order in every lane: the lower lane's sum first
-        const Two other = {__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)};
-        sum = lane & o ? add(other, sum) : add(sum, other);
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+            s1 += __shfl_xor_sync(kFull, s1, o);
+            s2 += __shfl_xor_sync(kFull, s2, o);
+            s3 += __shfl_xor_sync(kFull, s3, o);
+        }
+        sum = (double)s1 + ((double)s2 + (double)s3);
     }
-    return key_of((double)sum.hi + (double)sum.lo);
+    return key_of(real ? sum : -(double)INFINITY);
 }
 
 // 16 bytes of a row.  A row is 512 bytes (D 128) somewhere in memory, which its four lanes
@@ -159,10 +165,11 @@ struct ScoreScratch {
 
 // Scores of pages first .. end - 1 (by the CTA), and of them the largest |bound|, the keys of
 // the largest and the smallest score of a page of the pool, and the largest sum of a
-// query's |q|.
+// query's |q|.  ids (nullable): receives the pages (-1: not one of the pool's).
 template <typename T, int D, int THREADS>
 __device__ __forceinline__ void score_pages(const SelectArgs& a, int b, int h, int first, int end,
-                                            uint8_t* s_q, ScoreScratch& sh, uint4* stat) {
+                                            uint8_t* s_q, ScoreScratch& sh, uint4* stat,
+                                            int* ids = nullptr) {
     constexpr int kSegs = 2 * D / 32;      // 64-byte pieces of a row: two k-steps each
     constexpr int kRowBytes = 4 * D + 64;  // a query's [q- | q+], rows 64 bytes apart mod 128
     constexpr int kWarps = THREADS / 32, kStep = kWarps * 16;
@@ -178,10 +185,13 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, int b, int h, i
     auto page_at = [&](int j0) {
         const int j = j0 + (lane & 15);
         if (j >= end) return -1;
-        const int page = table[j];
-        if (page >= 0 && page < a.num_pages) return page;
-        bits |= PKV_DEV_BAD_PAGE;
-        return -1;
+        int page = table[j];
+        if (page < 0 || page >= a.num_pages) {
+            bits |= PKV_DEV_BAD_PAGE;
+            page = -1;
+        }
+        if (ids && lane < 16) ids[j] = page;
+        return page;
     };
     uint4 x[kSegs], y[kSegs];
     bool use0, use1;
@@ -345,12 +355,13 @@ __device__ __forceinline__ K kth_key(int (*buf)[16], int& turn, int cn, int want
 }
 
 // The choice among pages c0 .. c0 + cn - 1: the `want` of the highest scores, into out[c0 ..].
-// stats: the unit's tiles'.  sh.hist and sh.open_n are 0.
+// stats: the unit's tiles'.  ids (nullable): the unit's pages.  sh.hist and sh.open_n are 0.
 template <typename T, int D, int THREADS>
 __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, int cn, int want,
                                      int32_t* out, const uint4* stats, int tiles, float* s_sc,
-                                     int cache, PickScratch& sh) {
+                                     int cache, PickScratch& sh, const int* ids = nullptr) {
     constexpr int kWarps = THREADS / 32;
+    constexpr int kLanes = D / 8, kTeams = 32 / kLanes;  // of a long score
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = a.n_q_heads / a.n_kv_heads;
     const long long unit = (long long)b * a.n_kv_heads + h;
@@ -377,12 +388,15 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
     // S and twice the error bound, rounded up
     const float S = __fmul_ru(most, (float)(*reinterpret_cast<const T*>(&big16)));
     // beyond fp32 (or not a number): no fp32 score says anything
-    const bool blind = !(S < 1e38f);
+    const bool blind = !(S < 1e36f);
     // (the second part: what products below fp32's normal range may lose, 256 of them, twice)
     const float e2 = S > 0.f ? __fadd_ru(__fmul_ru(S, 6.103515625e-05f), 6.1e-36f) : 0.f;
-    // two fp32 values hold a sum of products to 2^-47 of S, where none of them is so small
-    // that its last bits are lost; else fp64
+    // 2^-60: below it fp32 may lose the last bits of what counts
     const bool wide = blind || S < 8.7e-19f;
+    const int team = lane / kLanes;
+    auto page_of = [&](int i) {
+        return ids ? ids[c0 + i] : a.table[(long long)b * a.table_stride + c0 + i];
+    };
     auto score = [&](int i) { return i < cache ? s_sc[i] : far[i]; };
 
     // Where the border lies: for few candidates by their ranks; else the want-th largest fp32
@@ -465,6 +479,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
             if (k < kFew) {
                 sh.few_at[k] = i;
                 sh.few[k] = key_of(s);
+                sh.far[k] = 0ull;
             }
         }
     }
@@ -475,45 +490,49 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
         for (int k = threadIdx.x; k < open; k += THREADS)
             atomicOr(&sh.chosen[sh.few_at[k] >> 5], 1u << (sh.few_at[k] & 31));
     } else if (open <= kFew && !blind) {
-        // the left-th of the few by fp32: those more than e2 from it are settled too.  The
-        // others' keys become 64-bit ones
-        for (int k = threadIdx.x; k < open; k += THREADS) {
-            const uint32_t s = sh.few[k];
-            int more = 0, same = 0;
-            for (int o = 0; o < open; ++o) {
-                more += sh.few[o] > s;
-                same += sh.few[o] == s;
+        bool told = false;
+        if (!ranked) {
+            // the left-th of the few by fp32: those more than e2 from it are settled too
+            for (int k = threadIdx.x; k < open; k += THREADS) {
+                const uint32_t s = sh.few[k];
+                int more = 0, same = 0;
+                for (int o = 0; o < open; ++o) {
+                    more += sh.few[o] > s;
+                    same += sh.few[o] == s;
+                }
+                if (more < left && left <= more + same) sh.kth = s;
             }
-            if (more < left && left <= more + same) sh.kth = s;
-        }
-        __syncthreads();
-        const float kth = score_of(sh.kth);
-        upper = __fadd_ru(kth, e2);
-        lower = __fadd_rd(kth, -e2);
-        int yes = 0, may = 0;
-        for (int k = lane; k < open; k += 32) {  // every warp counts for itself
-            const float s = score_of(sh.few[k]);
-            yes += s > upper;
-            may += s <= upper && s >= lower;
-        }
-        yes = __reduce_add_sync(kFull, yes);
-        may = __reduce_add_sync(kFull, may);
-        if (may == left - yes) {
-            for (int k = threadIdx.x; k < open; k += THREADS)
-                if (score_of(sh.few[k]) >= lower)
-                    atomicOr(&sh.chosen[sh.few_at[k] >> 5], 1u << (sh.few_at[k] & 31));
-        } else {
-            // settled ones get the ends of the keys' range
-            for (int k = threadIdx.x; k < open; k += THREADS)
-                sh.far[k] = score_of(sh.few[k]) > upper ? ~0ull : 0ull;
             __syncthreads();
-            for (int x = warp; x < open * group; x += kWarps) {
-                const int k = x / group;
+            const float kth = score_of(sh.kth);
+            upper = __fadd_ru(kth, e2);
+            lower = __fadd_rd(kth, -e2);
+            int yes = 0, may = 0;
+            for (int k = lane; k < open; k += 32) {  // every warp counts for itself
                 const float s = score_of(sh.few[k]);
-                if (s > upper || s < lower) continue;
+                yes += s > upper;
+                may += s <= upper && s >= lower;
+            }
+            yes = __reduce_add_sync(kFull, yes);
+            may = __reduce_add_sync(kFull, may);
+            told = may == left - yes;
+            for (int k = threadIdx.x; k < open; k += THREADS) {
+                const float s = score_of(sh.few[k]);
+                if (told && s >= lower)
+                    atomicOr(&sh.chosen[sh.few_at[k] >> 5], 1u << (sh.few_at[k] & 31));
+                if (s > upper) sh.far[k] = ~0ull;  // settled: the end of the keys' range
+            }
+            __syncthreads();
+        }
+        if (!told) {
+            // the others' 64-bit keys, a team of lanes a (page, head)
+            for (int x0 = warp * kTeams; x0 < open * group; x0 += kWarps * kTeams) {
+                const int x = x0 + team, k = min(x / group, open - 1);
+                const float s = score_of(sh.few[k]);
+                const bool mine = x < open * group && s <= upper && s >= lower;
+                const int page = mine ? page_of(sh.few_at[k]) : -1;
                 const unsigned long long key =
-                    long_score<T, D>(a, b, h, c0 + sh.few_at[k], x - k * group, S, wide);
-                if (lane == 0) atomicMax(&sh.far[k], key);
+                    long_score<T, D>(a, b, h, page, x - k * group, S, wide);
+                if (mine && lane % kLanes == 0) atomicMax(&sh.far[k], key);
             }
             __syncthreads();
             for (int k = threadIdx.x; k < open; k += THREADS) {
@@ -553,9 +572,14 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
             while (m && S != 0.f) {
                 const int at = w * 32 + __ffs(m) - 1;
                 m &= m - 1;
+                const int page = page_of(at);
                 unsigned long long key = 0;
-                for (int x = 0; x < group; ++x)
-                    key = max(key, long_score<T, D>(a, b, h, c0 + at, x, S, wide));
+                for (int x = 0; x < group; x += kTeams)  // (the last head again for idle teams)
+                    key = max(key, long_score<T, D>(a, b, h, page, min(x + team, group - 1), S,
+                                                    wide));
+#pragma unroll
+                for (int o = kLanes; o < 32; o <<= 1)
+                    key = max(key, __shfl_xor_sync(kFull, key, o));
                 if (lane == 0) keys64[at] = key;
             }
         }
@@ -679,6 +703,7 @@ __global__ void __launch_bounds__(kSmallThreads) select_small_kernel(const Selec
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ ScoreScratch score_sh;
     __shared__ PickScratch sh;
+    __shared__ int s_ids[kSmallPages];
     const int h = blockIdx.x, b = blockIdx.y;
     const long long unit = (long long)b * a.n_kv_heads + h;
     int32_t* out = a.selected + unit * a.max_pages;
@@ -691,11 +716,11 @@ __global__ void __launch_bounds__(kSmallThreads) select_small_kernel(const Selec
     if (bits && h == 0 && threadIdx.x == 0) set_status(a.status, bits);
     if (list_kept(a, n, out, kSmallThreads, true)) return;
     uint4* stat = a.stats + unit * a.tiles;
-    score_pages<T, D, kSmallThreads>(a, b, h, 0, n, s_dyn, score_sh, stat);
+    score_pages<T, D, kSmallThreads>(a, b, h, 0, n, s_dyn, score_sh, stat, s_ids);
     __syncthreads();
     pick<T, D, kSmallThreads>(a, b, h, a.keep_first, n - a.keep_first - a.keep_last,
                               a.max_pages - a.keep_first - a.keep_last, out, stat, 1,
-                              reinterpret_cast<float*>(s_dyn + q_bytes), cache, sh);
+                              reinterpret_cast<float*>(s_dyn + q_bytes), cache, sh, s_ids);
 }
 
 template <typename T, int D>
@@ -705,10 +730,11 @@ cudaError_t launch(SelectArgs a, cudaStream_t stream) {
     const int cache = a.table_stride < kScoreCache ? a.table_stride : kScoreCache;
     const int cache_bytes = cache * 4 + 16;
     const long long units = (long long)a.batch * a.n_kv_heads;
-    // Short rows: one launch, a CTA a unit.  us a call (bf16, D 128), one / two launches: 32
-    // units of 128 pages 8.0 / 9.5, 256 pages 9.3 / 9.9, 512 pages 12.1 / 10.1; 128 units of
-    // 512 pages 12.5 / 14.9.  Longer rows of unequal requests want their pages shared out.
-    if (a.table_stride <= 256 || (a.table_stride <= 512 && 2 * units >= sm_count())) {
+    // Short rows: one launch, a CTA a unit.  us a call (bf16, D 128), one / two launches, as
+    // both were measured: 32 units of 128 pages 8.0 / 9.5, 256 pages 9.3 / 9.9, 512 pages
+    // 12.1 / 10.1; 128 units of 512 pages 12.5 / 14.9.  Longer rows of unequal requests want
+    // their pages shared out.
+    if (a.table_stride <= 256 || (a.table_stride <= kSmallPages && 2 * units >= sm_count())) {
         a.tiles = 1;
         static SmemLimit limit;
         const cudaError_t e = limit.set(reinterpret_cast<const void*>(select_small_kernel<T, D>),
