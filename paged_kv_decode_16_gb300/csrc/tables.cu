@@ -189,12 +189,11 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
     // sums of kThreads requests in 32 bits
     const bool narrow = a.n_tokens < 0x7fffffff / kThreads - 1;
     auto kernel = narrow ? tables_kernel<int> : tables_kernel<long long>;
-    if (smem > 48 * 1024) {
-        static SmemLimit limits[2];
-        const cudaError_t e = limits[narrow].set(reinterpret_cast<const void*>(kernel),
-                                                 (3 * kMaxTableBatch + 1) * 4);
-        if (e != cudaSuccess) return e;
-    }
+    // (the 48 KB that a launch has unasked hold the kernel's static shared memory too)
+    static SmemLimit limits[2];
+    const cudaError_t e = limits[narrow].set(reinterpret_cast<const void*>(kernel),
+                                             (3 * kMaxTableBatch + 1) * 4);
+    if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, per_cta);
 }
 
