@@ -136,9 +136,11 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a, in
         *a.free_end = begin + s_taken;
     }
 
+    // (counted from the CTA's first row: a row's number may be up to 2^31 - 2)
     const long long first = (long long)blockIdx.x * per_cta;
-    const int last = (int)min(first + per_cta, (long long)a.n_tokens);
-    for (int i = (int)first + threadIdx.x; i < last; i += kThreads) {
+    const int rows = (int)min((long long)per_cta, a.n_tokens - first);
+    for (int x = threadIdx.x; x < rows; x += kThreads) {
+        const int i = (int)first + x;
         int pos = -1, seq = -1;
         long long slot = -1;
         if (i < total) {

@@ -4,6 +4,10 @@ import subprocess
 import sys
 
 import pytest
+import torch
+
+import paged_kv_decode_16_gb300 as pkv
+from test_gpu_selected import DEV, i32, status_word
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -40,3 +44,39 @@ def test_tables_of_batches_about_the_default_shared_memory(tokens):
                         *map(str, (4072, 4073, 4074, 4083, 4084, 4090, 4095, 4096, 4500))],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stdout + r.stderr
+
+
+def same(x, first, want, step=1 << 26):
+    """x[i] == want(i) for i from `first` on, in pieces."""
+    for a in range(first, x.numel(), step):
+        i = torch.arange(a, min(a + step, x.numel()), device=DEV)
+        if not torch.equal(x[a:a + step].long(), want(i)):
+            return False
+    return True
+
+
+def test_tables_of_the_most_token_rows():
+    """2^31 - 1 rows: a row's number plus a stride of the grid is beyond 32 bits."""
+    N, page = 2 ** 31 - 1, 256
+    new = [3, N - 100 - 3]
+    need = [1, -(-new[1] // page)]
+    free = torch.randperm(sum(need), device=DEV).to(torch.int32)
+    table = torch.full((2, need[1]), -1, dtype=torch.int32, device=DEV)
+    lens, starts, end, st = i32([0, 0]), i32([0] * 3), i32([0]), status_word()
+    pos, seq = (torch.full((N,), 7, dtype=torch.int32, device=DEV) for _ in range(2))
+    slots = torch.full((N,), 7, dtype=torch.int64, device=DEV)
+    pkv.paged_tables_build(i32([0, 0]), i32(new), free, None, end, table, page, sum(need), lens,
+                           starts, pos, seq, slots, dev_status=st)
+    assert st.item() == 0 and end.item() == sum(need)
+    assert lens.tolist() == new and starts.tolist() == [0, 3, N - 100]
+    assert torch.equal(table[1], free[1:]) and table[0, 0] == free[0]
+    assert (table[0, 1:] == -1).all()
+    pages = free.long()
+    assert pos[:3].tolist() == [0, 1, 2] and (seq[:3] == 0).all()
+    assert torch.equal(slots[:3], pages[0] * page + torch.arange(3, device=DEV))
+    none = N - 100
+    assert same(seq[:none], 3, torch.ones_like)
+    assert same(pos[:none], 3, lambda i: i - 3)
+    assert same(slots[:none], 3, lambda i: pages[1 + (i - 3) // page] * page + (i - 3) % page)
+    for x in (pos, seq, slots):
+        assert (x[none:] == -1).all()
