@@ -44,7 +44,9 @@ __global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const BoundsAr
     pdl_wait();
     pdl_trigger();
     __syncthreads();
-    for (int i = first + threadIdx.x; i < min(first + tile, a.n_tokens); i += kWarps * 32) {
+    // (counted from the tile's start: a token's number may be up to 2^31 - 2)
+    for (int x = threadIdx.x; x < min(tile, a.n_tokens - first); x += kWarps * 32) {
+        const int i = first + x;
         const long long s = a.slots[i];
         if (s < 0) continue;
         if (s >= a.n_slots) {

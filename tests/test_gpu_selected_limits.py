@@ -80,3 +80,24 @@ def test_tables_of_the_most_token_rows():
     assert same(slots[:none], 3, lambda i: pages[1 + (i - 3) // page] * page + (i - 3) % page)
     for x in (pos, seq, slots):
         assert (x[none:] == -1).all()
+
+
+def test_bounds_of_the_most_slots():
+    """2^31 - 1 slots, of which the last ones, and those around a tile's ends, hold rows."""
+    N, NP, page, hkv, d = 2 ** 31 - 1, 90, 16, 2, 64
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    k_pool = torch.randn(NP, hkv, page, d, generator=gen, device=DEV).to(torch.bfloat16)
+    pool = pkv.kv_pool_create(NP, page, hkv, d, torch.bfloat16, k_pool, torch.empty_like(k_pool))
+    slots = torch.full((N,), -1, dtype=torch.int64, device=DEV)
+    pages = torch.randperm(NP, generator=gen, device=DEV)
+    at = torch.arange(NP, device=DEV) % page
+    slots[N - 80:] = (pages * page + at)[10:]      # a page each
+    slots[:10] = (pages * page + at)[:10]
+    bounds = torch.full((NP, hkv, 2, d), 55.0, dtype=torch.bfloat16, device=DEV)
+    st = status_word()
+    pkv.kv_page_bounds(pool, slots, bounds, dev_status=st)
+    assert st.item() == 0
+    for p, x in zip(pages.tolist(), at.tolist()):
+        rows = k_pool[p, :, :x + 1]
+        assert torch.equal(bounds[p, :, 0], rows.amin(1))
+        assert torch.equal(bounds[p, :, 1], rows.amax(1))
