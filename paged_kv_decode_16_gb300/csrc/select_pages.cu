@@ -649,8 +649,9 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
 __device__ __forceinline__ bool list_kept(const SelectArgs& a, int n, int32_t* out, int threads,
                                           bool write) {
     const int K = a.max_pages;
-    if (n <= K) {
-        for (int i = threadIdx.x; write && i < K; i += threads) out[i] = i < n ? i : -1;
+    if (n <= K) {  // (K may be close to 2^31: 32 bits without a sign hold the loop's last sum)
+        for (uint32_t i = threadIdx.x; write && i < (uint32_t)K; i += threads)
+            out[i] = i < (uint32_t)n ? (int)i : -1;
         return true;
     }
     for (int i = threadIdx.x; write && i < a.keep_first; i += threads) out[i] = i;

@@ -101,3 +101,21 @@ def test_bounds_of_the_most_slots():
         rows = k_pool[p, :, :x + 1]
         assert torch.equal(bounds[p, :, 0], rows.amin(1))
         assert torch.equal(bounds[p, :, 1], rows.amax(1))
+
+
+def test_select_into_the_longest_list():
+    """max_pages 2^31 - 1: every page is listed, -1 behind them to the list's end."""
+    K, n = 2 ** 31 - 1, 700
+    sel = torch.full((1, 1, K), 7, dtype=torch.int32, device=DEV)
+    q = torch.ones(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    bounds = torch.ones(n, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[None]
+    st = status_word()
+    for cols, ws in ((n, pkv.alloc_select_workspace(1, 1, n)),       # two launches
+                     (200, pkv.alloc_select_workspace(1, 1, 200))):  # one
+        sel.fill_(7)
+        pkv.paged_select_pages(q, bounds, table[:, :cols].contiguous(), i32([16 * cols - 3]), 16,
+                               sel, ws, dev_status=st)
+        assert st.item() == 0
+        assert torch.equal(sel[0, 0, :cols].long(), torch.arange(cols, device=DEV))
+        assert (sel[0, 0, cols:] == -1).all()
