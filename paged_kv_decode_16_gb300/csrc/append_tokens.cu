@@ -75,7 +75,7 @@ append_tokens_kernel(const AppendTokensArgs a, const GroupShape gs) {
     uint64_t* s_dst = s_src + 3 * pad;                                              // [2][pad]
 
     const int tid = threadIdx.x;
-    const int groups = (a.n_tokens + gs.tokens - 1) / gs.tokens;
+    const int groups = 1 + (a.n_tokens - 1) / gs.tokens;
     const bool rope = a.positions != nullptr;
     const bool normed = a.q_norm || a.k_norm;
     const int pairs = rope ? a.rope.rotary_dim >> 1 : 0;
