@@ -35,6 +35,8 @@ constexpr int kBins = 1024;         // of the histogram that finds the border
 // 125 the same, 253 11.1 against 9.4.
 constexpr int kRankAll = 64;
 constexpr int kScoreCache = 16384;  // scores kept in shared memory
+// 2^-60: products that add up to less may have lost, in fp32, last bits that count
+constexpr float kSmallSum = 8.673617379884035e-19f;
 
 __device__ __forceinline__ int pages_of(const SelectArgs& a, int b, uint32_t* bits) {
     int len = a.lens[b];
@@ -81,36 +83,63 @@ __device__ __forceinline__ float score_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
+// 16 bytes of a row.  A row is 512 bytes (D 128) somewhere in memory, which its four lanes
+// walk 64 bytes at a time: the hint brings 256 into L2 at the first touch (32 requests of
+// up to 32768 tokens 33.3 -> 31.5 us a call).
+__device__ __forceinline__ uint4 load_row(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // The score of a page for one query head to more than 32 bits, as a key, worked out by D / 8
-// lanes side by side (each gets it; page < 0: the key of -inf).  S: at least the sum of the
-// products' sizes.  fp64 runs at a 64th of fp32's rate on this part, so it serves only where
-// fp32 cannot hold the products (`wide`).  Else a product, exact in fp32, is cut at two fixed
-// bits, by adding and taking away 1.5 times a power of two: with 2^k above 2 S, the parts
-// down to 2^(k-23) add up without rounding, and so do those from there to 2^(k-39); what is
-// left is below 2^(k-40), so its rounded sum is off by 2^(k-50), 2^-48 S, at most.
+// lanes side by side (each gets it; page < 0: the key of -inf).  fp64 runs at a 64th of fp32's
+// rate on this part, so it serves only where fp32 cannot hold the products: where those of any
+// page may be too large (`wide`), or where this page's are too small (for the whole warp then).
+// Else a product, exact in fp32, is cut at two bits that go by S, the sum of this page's
+// products' sizes, by adding and taking away 1.5 times a power of two: with 2^k above 2 S, the
+// parts down to 2^(k-23) add up without rounding, and so do those from there to 2^(k-39); what
+// is left is below 2^(k-40), so its rounded sum is off by 2^(k-50), 2^-48 S, at most.
 template <typename T, int D>
 __device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, int b, int h,
-                                                         int page, int head, float S, bool wide) {
+                                                         int page, int head, bool wide) {
     constexpr int kLanes = D / 8;
     const int l = threadIdx.x % kLanes;
     const bool real = page >= 0 && page < a.num_pages;
-    uint4 xv = make_uint4(0, 0, 0, 0), lov = xv, hiv = xv;
-    if (real) {
-        const int group = a.n_q_heads / a.n_kv_heads;
-        const T* row =
-            static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D;
-        const T* q = static_cast<const T*>(a.q) +
-                     ((long long)b * a.n_q_heads + h * group + head) * D;
-        xv = reinterpret_cast<const uint4*>(q)[l];
-        lov = reinterpret_cast<const uint4*>(row)[l];
-        hiv = reinterpret_cast<const uint4*>(row + D)[l];
-    }
-    float x[8], lo[8], hi[8];
-    Cvt<T>::unpack8(xv, x);
-    Cvt<T>::unpack8(lov, lo);
-    Cvt<T>::unpack8(hiv, hi);
+    const int group = a.n_q_heads / a.n_kv_heads;
+    const uint4* row = reinterpret_cast<const uint4*>(
+        static_cast<const T*>(a.bounds) + ((long long)page * a.n_kv_heads + h) * 2 * D) + l;
+    const uint4* q = reinterpret_cast<const uint4*>(
+        static_cast<const T*>(a.q) + ((long long)b * a.n_q_heads + h * group + head) * D) + l;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     double sum = 0.0;
-    if (wide) {
+    float p[8], S = 0.f;
+    if (!wide) {
+        float x[8], lo[8], hi[8];
+        Cvt<T>::unpack8(real ? *q : zero, x);
+        Cvt<T>::unpack8(real ? *row : zero, lo);
+        Cvt<T>::unpack8(real ? row[kLanes] : zero, hi);
+        bool some = false;  // a product that is not 0
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float y = signbit(x[e]) ? lo[e] : hi[e];
+            p[e] = __fmul_rn(x[e], y);
+            S += fabsf(p[e]);
+            some = some || (x[e] != 0.f && y != 0.f);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
+        wide = __any_sync(kFull, some && S < kSmallSum);
+        S = fmaxf(S, kSmallSum);
+    }
+    if (wide) {  // (rare: the rows are read again rather than kept)
+        float x[8], lo[8], hi[8];
+        Cvt<T>::unpack8(real ? load_row(q) : zero, x);
+        Cvt<T>::unpack8(real ? load_row(row) : zero, lo);
+        Cvt<T>::unpack8(real ? load_row(row + kLanes) : zero, hi);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             // as the product does it: both halves, one of them with a zero
@@ -127,8 +156,7 @@ __device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, in
         float s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float p = __fmul_rn(x[e], signbit(x[e]) ? lo[e] : hi[e]);
-            const float p1 = __fsub_rn(__fadd_rn(p, cut1), cut1), r = __fsub_rn(p, p1);
+            const float p1 = __fsub_rn(__fadd_rn(p[e], cut1), cut1), r = __fsub_rn(p[e], p1);
             const float p2 = __fsub_rn(__fadd_rn(r, cut2), cut2);
             s1 = __fadd_rn(s1, p1);
             s2 = __fadd_rn(s2, p2);
@@ -143,18 +171,6 @@ __device__ __forceinline__ unsigned long long long_score(const SelectArgs& a, in
         sum = (double)s1 + ((double)s2 + (double)s3);
     }
     return key_of(real ? sum : -(double)INFINITY);
-}
-
-// 16 bytes of a row.  A row is 512 bytes (D 128) somewhere in memory, which its four lanes
-// walk 64 bytes at a time: the hint brings 256 into L2 at the first touch (32 requests of
-// up to 32768 tokens 33.3 -> 31.5 us a call).
-__device__ __forceinline__ uint4 load_row(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
 }
 
 // What a tile of scores leaves for the choice.
@@ -391,8 +407,6 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
     const bool blind = !(S < 1e36f);
     // (the second part: what products below fp32's normal range may lose, 256 of them, twice)
     const float e2 = S > 0.f ? __fadd_ru(__fmul_ru(S, 6.103515625e-05f), 6.1e-36f) : 0.f;
-    // 2^-60: below it fp32 may lose the last bits of what counts
-    const bool wide = blind || S < 8.7e-19f;
     const int team = lane / kLanes;
     auto page_of = [&](int i) {
         return ids ? ids[c0 + i] : a.table[(long long)b * a.table_stride + c0 + i];
@@ -531,7 +545,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
                 const bool mine = x < open * group && s <= upper && s >= lower;
                 const int page = mine ? page_of(sh.few_at[k]) : -1;
                 const unsigned long long key =
-                    long_score<T, D>(a, b, h, page, x - k * group, S, wide);
+                    long_score<T, D>(a, b, h, page, x - k * group, blind);
                 if (mine && lane % kLanes == 0) atomicMax(&sh.far[k], key);
             }
             __syncthreads();
@@ -575,8 +589,8 @@ __device__ __forceinline__ void pick(const SelectArgs& a, int b, int h, int c0, 
                 const int page = page_of(at);
                 unsigned long long key = 0;
                 for (int x = 0; x < group; x += kTeams)  // (the last head again for idle teams)
-                    key = max(key, long_score<T, D>(a, b, h, page, min(x + team, group - 1), S,
-                                                    wide));
+                    key = max(key,
+                              long_score<T, D>(a, b, h, page, min(x + team, group - 1), blind));
 #pragma unroll
                 for (int o = kLanes; o < 32; o <<= 1)
                     key = max(key, __shfl_xor_sync(kFull, key, o));
