@@ -179,12 +179,14 @@ struct ScoreScratch {
     float sum[16];
 };
 
-// Scores of pages first .. end - 1 (by the CTA), and of them the largest |bound|, the keys of
-// the largest and the smallest score of a page of the pool, and the largest sum of a
-// query's |q|.  ids (nullable): receives the pages (-1: not one of the pool's).
+// Scores of pages first .. end - 1 of n (by the CTA), and of them the largest |bound|, the keys
+// of the largest and the smallest score of a page of the pool, and the largest sum of a
+// query's |q|.  The pages that are listed anyway are not read, and have no part in these (what
+// they hold must not widen the border of the others).  ids (nullable): receives the pages
+// (-1: not one of the pool's, or listed anyway).
 template <typename T, int D, int THREADS>
 __device__ __forceinline__ void score_pages(const SelectArgs& a, int b, int h, int first, int end,
-                                            uint8_t* s_q, ScoreScratch& sh, uint4* stat,
+                                            int n, uint8_t* s_q, ScoreScratch& sh, uint4* stat,
                                             int* ids = nullptr) {
     constexpr int kSegs = 2 * D / 32;      // 64-byte pieces of a row: two k-steps each
     constexpr int kRowBytes = 4 * D + 64;  // a query's [q- | q+], rows 64 bytes apart mod 128
@@ -206,6 +208,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, int b, int h, i
             bits |= PKV_DEV_BAD_PAGE;
             page = -1;
         }
+        if (j < a.keep_first || j >= n - a.keep_last) page = -1;
         if (ids && lane < 16) ids[j] = page;
         return page;
     };
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectArgs a
     if (bits && h == 0 && tile == 0 && threadIdx.x == 0) set_status(a.status, bits);
     const int first = tile * a.tile_pages;
     if (first >= n || list_kept(a, n, nullptr, kScoreThreads, false)) return;
-    score_pages<T, D, kScoreThreads>(a, b, h, first, min(first + a.tile_pages, n), s_q, sh,
+    score_pages<T, D, kScoreThreads>(a, b, h, first, min(first + a.tile_pages, n), n, s_q, sh,
                                      a.stats + ((long long)b * a.n_kv_heads + h) * a.tiles + tile);
 }
 
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(kSmallThreads) select_small_kernel(const Selec
     if (bits && h == 0 && threadIdx.x == 0) set_status(a.status, bits);
     if (list_kept(a, n, out, kSmallThreads, true)) return;
     uint4* stat = a.stats + unit * a.tiles;
-    score_pages<T, D, kSmallThreads>(a, b, h, 0, n, s_dyn, score_sh, stat, s_ids);
+    score_pages<T, D, kSmallThreads>(a, b, h, 0, n, n, s_dyn, score_sh, stat, s_ids);
     __syncthreads();
     pick<T, D, kSmallThreads>(a, b, h, a.keep_first, n - a.keep_first - a.keep_last,
                               a.max_pages - a.keep_first - a.keep_last, out, stat, 1,

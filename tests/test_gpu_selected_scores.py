@@ -1,11 +1,14 @@
 """paged_select_pages on bounds of very unequal sizes: the choice stays that of the 64-bit
-scores."""
+scores, and pages that are listed anyway have no part in it."""
+import math
 import random
 
 import pytest
 import torch
 
-from test_gpu_selected import BF16, DEV, check_select, page_table, rand
+import paged_kv_decode_16_gb300 as pkv
+import selected_ref as ref
+from test_gpu_selected import BF16, DEV, F16, check_select, i32, page_table, rand, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +44,39 @@ def test_select_beside_a_page_of_ordinary_keys(n):
     bounds[table[0][n // 2]] = 2.0 ** 30
     bounds[table[0][n // 4]] = 0.0
     check_select(q, bounds, table, [16 * n], 16, n // 5, 1, 1)
+
+
+@pytest.mark.parametrize("n,cols", [(40, 60), (120, 200), (200, 600)])
+@pytest.mark.parametrize("first,last", [(1, 1), (3, 0), (0, 5)])
+@pytest.mark.parametrize("x", [math.nan, math.inf, 2.0 ** 100])
+def test_select_listed_pages_have_no_part_in_the_choice(n, cols, first, last, x):
+    """Whatever the pages that are always listed hold, no score of another page is looked
+    at a second time in 64 bits: their place in the workspace stays as it was."""
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    rng = random.Random(n)
+    table = page_table(rng, [16 * n], 16, n, cols)
+    q = rand(gen, 1, 4, 64, dtype=BF16)
+    bounds = rand(gen, n, 2, 2, 64, dtype=BF16).sort(2).values
+    if first:
+        bounds[table[0][first - 1], :, 1, 9] = x
+    if last:
+        bounds[table[0][n - last], :, 0, 8] = x
+    sel = torch.full((1, 2, 12), 77, dtype=torch.int32, device=DEV)
+    ws = pkv.alloc_select_workspace(1, 2, cols).fill_(165)
+    st = status_word()
+    pkv.paged_select_pages(q, bounds, i32(table), i32([16 * n]), 16, sel, ws, keep_first=first,
+                           keep_last=last, dev_status=st)
+    want, _ = ref.select(q, bounds, table, [16 * n], 16, 12, first, last)
+    assert sel.tolist() == want and st.item() == 0
+    assert (ws[:2 * cols * 8] == 165).all()
+
+
+def test_select_flags_listed_pages_outside_the_pool():
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    rng = random.Random(1)
+    q = rand(gen, 1, 4, 64, dtype=F16)
+    bounds = rand(gen, 90, 2, 2, 64, dtype=F16).sort(2).values
+    for at in (0, 88, 89):
+        table = page_table(rng, [16 * 90], 16, 90, 90)
+        table[0][at] = 90
+        assert check_select(q, bounds, table, [16 * 90], 16, 12, 1, 2) == ref.BAD_PAGE
