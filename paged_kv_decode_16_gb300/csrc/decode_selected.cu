@@ -14,7 +14,9 @@
 // of the head) fill the 16 rows of an instruction and 8 query heads its 8 columns: half the
 // instructions of the form with the heads as rows, of which a group of 8 or less leaves
 // half empty.  P^T comes from S^T's accumulators by an 8 x 8 transpose (movmatrix).  P enters
-// in two 16-bit pieces, so that it keeps 16 (bf16) or 22 (fp16) significant bits.
+// in two 16-bit pieces, so that it keeps 16 (bf16) or 22 (fp16) significant bits.  fp16's
+// range ends at steps of 2^-24, so its weights are taken 2^15 times: the largest, 1, still fits,
+// and what is lost of any is below 2^-39 of the largest.
 //
 // What bounds it: memory, 4 D bytes a token and KV head (256 units of 512 tokens, 134 MB:
 // 24 us, 5.6 TB/s, of which 4 are the chain below; 1024 units, 455 MB: 70 us, 6.5 TB/s); a
@@ -74,8 +76,12 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
     return v;
 }
 
-// P in two fp16 pieces, as split_bf16x2: what the first leaves keeps 11 bits more.
+// P in two fp16 pieces, as split_bf16x2: what the first leaves keeps 11 bits more.  Both are
+// kHalfScale times P.
+constexpr float kHalfScale = 32768.f;
 __device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    a *= kHalfScale;
+    b *= kHalfScale;
     const __half2 h = __floats2half2_rn(a, b);
     const float2 f = __half22float2(h);
     hi = *reinterpret_cast<const uint32_t*>(&h);
@@ -333,10 +339,11 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float* dst = s_o + warp * Lay::kStateFloats + (g + c) * Lay::kRowFloats + g_lo;
+            constexpr float kOnce = kSplitP ? 1.f : 1.f / kHalfScale;  // o holds fp16's P scaled
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
-                dst[dt * 16] = o[ht][dt][c];
-                dst[dt * 16 + 8] = o[ht][dt][2 + c];
+                dst[dt * 16] = o[ht][dt][c] * kOnce;
+                dst[dt * 16 + 8] = o[ht][dt][2 + c] * kOnce;
             }
             float sum = l[ht][c];
             sum += __shfl_xor_sync(kFull, sum, 4);
