@@ -888,7 +888,10 @@ pkv_status paged_select_pages(const void* q, const void* bounds, const int32_t* 
  * come from paged_select_pages or any other rule.  Lengths are clamped to the
  * table row (PKV_DEV_BAD_LEN), a page id outside the pool is skipped
  * (PKV_DEV_BAD_PAGE).  max_pages >= 1; num_pages * n_kv_heads * page_size at
- * most 2^31 - 1 (UNSUPPORTED).  Arithmetic and errors as for
+ * most 2^31 - 1 (UNSUPPORTED).  Sums, maxima and weights in fp32; for the product
+ * with V a weight keeps 16 bits (bf16 pools) or 22 and at least 2^-39 of the
+ * largest (fp16).  An infinity in V under a weight of 2^-39 of the largest or more
+ * makes its element that infinity (two of unequal signs NaN).  Errors as for
  * paged_decode_attention; no workspace.  One launch. */
 pkv_status paged_decode_attention_selected(const void* q, const void* k_pool, const void* v_pool,
                                            const int32_t* page_table, int table_stride,

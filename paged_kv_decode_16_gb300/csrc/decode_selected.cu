@@ -16,7 +16,9 @@
 // half empty.  P^T comes from S^T's accumulators by an 8 x 8 transpose (movmatrix).  P enters
 // in two 16-bit pieces, so that it keeps 16 (bf16) or 22 (fp16) significant bits.  fp16's
 // range ends at steps of 2^-24, so its weights are taken 2^15 times: the largest, 1, still fits,
-// and what is lost of any is below 2^-39 of the largest.
+// and any is off by 2^-39 of the largest at most.  The first piece is cut, not rounded,
+// and the second never 0 beside one that is not: a product with an infinity is then that
+// infinity in both, where a rest below 0, or of 0, would make NaN of their sum.
 //
 // What bounds it: memory, 4 D bytes a token and KV head (256 units of 512 tokens, 134 MB:
 // 24 us, 5.6 TB/s, of which 4 are the chain below; 1024 units, 455 MB: 70 us, 6.5 TB/s); a
@@ -76,16 +78,28 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
     return v;
 }
 
-// P in two fp16 pieces, as split_bf16x2: what the first leaves keeps 11 bits more.  Both are
-// kHalfScale times P.
+// P (>= 0) in two fp16 pieces, kHalfScale times P: cut at 11 bits, and 11 bits of the rest, at
+// least fp16's smallest step (2^-24) where the first piece is that much.
 constexpr float kHalfScale = 32768.f;
-__device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split_cut(__half, float a, float b, uint32_t& hi, uint32_t& lo) {
     a *= kHalfScale;
     b *= kHalfScale;
-    const __half2 h = __floats2half2_rn(a, b);
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const __half2 h = *reinterpret_cast<const __half2*>(&hi);
     const float2 f = __half22float2(h);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = Cvt<__half>::pack2(a - f.x, b - f.y);
+    const __half2 rest = __floats2half2_rn(a - f.x, b - f.y);
+    const __half2_raw step = {1, 1};
+    const __half2 l = __hmax2(rest, __hmin2(h, __half2(step)));
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// In two bf16 pieces: cut at 8 bits (the upper half of its bits), and 8 bits of the rest, which
+// 2^-23 of P keep above 0.
+__device__ __forceinline__ void split_cut(__nv_bfloat16, float a, float b, uint32_t& hi,
+                                          uint32_t& lo) {
+    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
+    constexpr float kMore = 1.00000011920928955f;  // 1 + 2^-23
+    lo = Cvt<__nv_bfloat16>::pack2(fmaf(a, kMore, -ha), fmaf(b, kMore, -hb));
 }
 
 template <typename T, int D, int HT, int kWarps, int kStages>
@@ -95,7 +109,8 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
     using Lay = SelLayout<D, HT, kWarps, kStages>;
     constexpr int KSTEPS = D / 16;
     constexpr int DT = D / 16;  // tiles of the output
-    constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
+    // o holds fp16's P scaled
+    constexpr float kOnce = std::is_same<T, __half>::value ? 1.f / kHalfScale : 1.f;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -270,7 +285,7 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
             for (int ht = 0; ht < HT; ++ht)
                 Mma<T>::run(s[ht][kk & 1], ka, qb[ht][kk][0], qb[ht][kk][1]);
         }
-        uint32_t pb[HT][2], pl[HT][2];  // B fragments of P^T (and of what its bf16s leave)
+        uint32_t pb[HT][2], pl[HT][2];  // B fragments of P^T's two pieces
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
             float e[4], alpha[2];  // e: (token g_lo, heads tq, tq + 1), (token g_lo + 8, ..)
@@ -300,13 +315,8 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
                 o[ht][dt][2] *= alpha[0];
                 o[ht][dt][3] *= alpha[1];
             }
-            if constexpr (kSplitP) {
-                split_bf16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
-                split_bf16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
-            } else {
-                split_f16x2(e[0], e[1], pb[ht][0], pl[ht][0]);
-                split_f16x2(e[2], e[3], pb[ht][1], pl[ht][1]);
-            }
+            split_cut(T(), e[0], e[1], pb[ht][0], pl[ht][0]);
+            split_cut(T(), e[2], e[3], pb[ht][1], pl[ht][1]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 pb[ht][x] = transpose8(pb[ht][x]);
@@ -339,7 +349,6 @@ selected_kernel(const SelectedParams p, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float* dst = s_o + warp * Lay::kStateFloats + (g + c) * Lay::kRowFloats + g_lo;
-            constexpr float kOnce = kSplitP ? 1.f : 1.f / kHalfScale;  // o holds fp16's P scaled
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
                 dst[dt * 16] = o[ht][dt][c] * kOnce;

@@ -1,5 +1,6 @@
-"""The weights of the attention over selected pages: both 16-bit pieces of them, and their
-range."""
+"""The weights of the attention over selected pages: both 16-bit pieces of them, their range,
+and values that are not finite."""
+import math
 import random
 
 import pytest
@@ -50,3 +51,41 @@ def test_attend_within_the_bound_of_two_pieces(hq, hkv, d, page, dtype, keep, le
     k, v = (rand(gen, NP, hkv, page, d, dtype=dtype) for _ in range(2))
     check(rand(gen, len(lens), hq, d, dtype=dtype), k, v, table, lens,
           some_lists(rng, lens, hkv, page, keep), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,keep", [(40, 3), (1600, 100)])
+def test_attend_infinite_values(dtype, n, keep):
+    """An infinity in V under a weight that is not 0 makes its element infinite, two of
+    unequal signs NaN, whatever the weight: 1, of few bits, or of many."""
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    pages = -(-n // 16)
+    k, v = (rand(gen, pages, 1, 16, 64, dtype=dtype) for _ in range(2))
+    q = torch.zeros(1, 4, 64, dtype=dtype, device=DEV)
+    q[0, :, 0] = torch.tensor([1.0, 2.0, 0.0, -1.0])
+    k[..., 0] = torch.randint(-3, 4, (pages, 1, 16), generator=gen, device=DEV).to(dtype)
+    k[..., 0][1, 0, 3] = 0.7
+    k[..., 0][0, 0, 3] = 4.0                      # the largest score: a weight of 1
+    for t, (d, x) in enumerate([(1, math.inf), (2, -math.inf), (3, math.inf), (3, -math.inf)]):
+        v[0, 0, 3 + t, d] = x
+    v[1, 0, 3, 4] = math.inf                      # a weight of many bits
+    v[2, 0, 1, 5] = -math.inf
+    table, lists = [list(range(pages))], [[list(range(pages)) + [-1] * (keep - pages)]]
+    got = run_attend(q, k, v, i32(table), i32([n]), i32(lists), math.log(2.0))
+    x = got[0].float()
+    assert (x[:, 1] == math.inf).all() and (x[:, 2] == -math.inf).all() and x[:, 3].isnan().all()
+    assert (x[:, 4] == math.inf).all() and (x[:, 5] == -math.inf).all()
+    fine = [0] + list(range(6, 64))
+    v[..., 1:6] = 0.0
+    want, bound = sb.attend(q, k, v, table, [n], lists, math.log(2.0))
+    ref.close(got[..., fine], want[..., fine], bound[..., fine])
+
+
+@pytest.mark.parametrize("dtype,drop", [(F16, 20), (F16, 38), (BF16, 60)])
+def test_attend_infinite_value_of_a_small_weight(dtype, drop):
+    q, k, v, table, lens, lists, scale = sb.tail(dtype, drop, tokens=512)
+    v[1, 0, 7, 9] = math.inf
+    v[1, 0, 9, 10] = -math.inf
+    got = run_attend(q.to(DEV), k.to(DEV), v.to(DEV), i32(table), i32(lens), i32(lists), scale)
+    assert (got[..., 9] == math.inf).all() and (got[..., 10] == -math.inf).all()
+    assert got[..., :9].isfinite().all() and got[..., 11:].isfinite().all()
