@@ -80,7 +80,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     if not os.path.exists(path):
         if not build_if_missing:
             raise RuntimeError(f"CUDA library not built: {path}")
-        _build.build()
+        _build.build_library()
     lib = ctypes.CDLL(path)
     V, I, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     D, L = ctypes.c_double, ctypes.c_int64

@@ -5,7 +5,9 @@ Each translation unit is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and the objects are
 linked into ``paged_kv_decode_16_gb300/_build/libpagedkv.so`` (static CUDA
 runtime, so loading it needs no GPU).  Rebuilds only when a source or header
-is newer than the library.  Concurrent builds (two test processes, a test and
+is newer than the library.  The library needs neither torch nor Python's headers
+(build_library; ``python build.py`` without a torch); the binding is built after it
+and for itself.  Concurrent builds (two test processes, a test and
 the benchmark) take an exclusive file lock on ``_build/.lock`` and compile
 into an object directory of their own, so they never share a half-written
 object; the second one to get the lock finds the library up to date.
@@ -22,6 +24,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -61,14 +64,18 @@ def binding_path() -> str:
     return os.path.join(OUT_DIR, f"_pagedkv_calls_{tag}.so")
 
 
-def up_to_date() -> bool:
+def _newest(paths) -> float:
+    return max(os.path.getmtime(f) for f in paths)
+
+
+def library_up_to_date() -> bool:
+    return os.path.exists(LIB) and _newest(_inputs()) <= os.path.getmtime(LIB)
+
+
+def binding_up_to_date() -> bool:
     calls = binding_path()
-    if not os.path.exists(LIB) or not os.path.exists(calls):
-        return False
-    t = os.path.getmtime(LIB)
     header = os.path.join(INCLUDE, "pagedkv.h")
-    return all(os.path.getmtime(f) <= t for f in _inputs()) and all(
-        os.path.getmtime(f) <= os.path.getmtime(calls) for f in (BINDING, header, __file__))
+    return os.path.exists(calls) and _newest((BINDING, header, __file__)) <= os.path.getmtime(calls)
 
 
 def _compile_binding(out: str) -> subprocess.CompletedProcess:
@@ -110,17 +117,40 @@ def _build_lock():
             fcntl.flock(f, fcntl.LOCK_UN)
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every source for sm_103a and link libpagedkv.so; return its path."""
-    if not force and up_to_date():
+def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Compile every source for sm_103a and link libpagedkv.so; return its path.  Needs
+    nvcc and a host compiler, nothing else."""
+    if not force and library_up_to_date():
         return LIB
     with _build_lock():
-        if not force and up_to_date():  # built by another process meanwhile
-            return LIB
-        return _build_locked(verbose, ptxas_verbose)
+        if force or not library_up_to_date():  # (built by another process meanwhile)
+            _build_library_locked(verbose, ptxas_verbose)
+        return LIB
 
 
-def _build_locked(verbose: bool, ptxas_verbose: bool) -> str:
+def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """The library and the Python binding's native part; return the library's path.  Where
+    the binding does not compile, the library is there all the same when this raises."""
+    if not force and library_up_to_date() and binding_up_to_date():
+        return LIB
+    with _build_lock():
+        library = force or not library_up_to_date()
+        binding = force or not binding_up_to_date()
+        with tempfile.TemporaryDirectory() as tmp, cf.ThreadPoolExecutor(max_workers=1) as ex:
+            obj = os.path.join(tmp, "calls.o")
+            calls = ex.submit(_compile_binding, obj) if binding else None
+            if library:
+                _build_library_locked(verbose, ptxas_verbose)
+            if calls:
+                r = calls.result()
+                if r.returncode != 0:
+                    raise RuntimeError("the Python binding's native part does not compile:\n"
+                                       + r.stderr)
+                _link_binding(obj)
+    return LIB
+
+
+def _build_library_locked(verbose: bool, ptxas_verbose: bool) -> None:
     nvcc = _nvcc()
     obj_dir = os.path.join(OUT_DIR, f"obj{os.getpid()}")
     os.makedirs(obj_dir, exist_ok=True)
@@ -139,19 +169,15 @@ def _build_locked(verbose: bool, ptxas_verbose: bool) -> str:
 
     objs = []
     errors = []
-    calls_obj = os.path.join(obj_dir, "calls.o")
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(_compile_binding, calls_obj)
         for src, obj, r in ex.map(compile_one, sources()):
             if verbose or ptxas_verbose:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
                 errors.append(f"{os.path.basename(src)}:\n{r.stderr}")
             objs.append(obj)
-        if calls.result().returncode != 0:
-            errors.append(f"calls.cpp:\n{calls.result().stderr}")
     if errors:
-        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
+        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     # the temporary name keeps the .so suffix: nvcc picks the link step from it
     tmp = os.path.join(OUT_DIR, f"libpagedkv.tmp{os.getpid()}.so")
     cmd = [nvcc, "-shared", *ARCH, "-o", tmp, *objs]
@@ -159,10 +185,20 @@ def _build_locked(verbose: bool, ptxas_verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB)
-    _link_binding(calls_obj)
     shutil.rmtree(obj_dir, ignore_errors=True)
-    return LIB
+
+
+def main(argv) -> None:
+    """The library, and the binding where there is a torch to build it against."""
+    options = dict(force="--force" in argv, verbose=True, ptxas_verbose="-v" in argv)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print(build_library(**options))
+        sys.stderr.write("no torch: the Python binding's native part is not built\n")
+        return
+    print(build(**options))
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True, ptxas_verbose="-v" in sys.argv))
+    main(sys.argv[1:])
