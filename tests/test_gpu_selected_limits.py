@@ -10,6 +10,15 @@ import paged_kv_decode_16_gb300 as pkv
 from test_gpu_selected import DEV, i32, status_word
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def memory_back():
+    """The largest tests take tens of GB: not kept for the tests behind them."""
+    yield
+    torch.cuda.empty_cache()
+
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BATCHES = """
