@@ -10,8 +10,9 @@
  * a common prefix once per KV head, several causal query tokens per sequence,
  * a host radix cache of prompt prefixes over the pool, the append and the
  * attention of a cache held in 8 bits, and a step that attends to selected pages
- * only (tables built on the GPU, appends of any tokens with every form of the
- * rotary embedding, page bounds, selection, attention).
+ * only (tables built on the GPU, appends of any tokens with the rotary embedding
+ * in halves or interleaved pairs, on part of a head, plain or scaled for long
+ * contexts, page bounds, selection, attention).
  *
  * Where the operations are defined (page title, section):
  *   - CacheIR, "Compiler Example": the decode graph lowers attention into
@@ -841,8 +842,8 @@ pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_s
  * and [1] the max.  bounds [num_pages][n_kv_heads][2][head_dim] (device, the
  * pool's dtype); other pages' are left as they are.  A NaN key gives NaN.  Call
  * it behind the append of the same slots; a page's tokens have to be one run,
- * in ascending order, in one call (else the page's bounds are those of one of
- * its runs).  Rows behind x are not read; a page whose tokens are taken back
+ * in ascending order, in one call (else the page's bounds are put together from
+ * those of its runs, some elements of one and some of another).  Rows behind x are not read; a page whose tokens are taken back
  * keeps its (then wider) bounds until a row of it is written again.  8-bit
  * pool: UNSUPPORTED; bounds over the pool or the slots: ALIAS.  One launch. */
 pkv_status kv_page_bounds(const pkv_pool* pool, const int64_t* slots, int n_tokens, void* bounds,

@@ -1,5 +1,5 @@
-// append_tokens.cu -- rotary embedding of new tokens' q and k in every form, and
-// the write of k and v into their slots.
+// append_tokens.cu -- rotary embedding of new tokens' q and k (in halves or interleaved
+// pairs, on part of a head, any frequencies), and the write of k and v into their slots.
 //
 // One pass over the rows: a task is two 16-byte vectors of one row that turn together
 // (half layout: vector j and vector j + rotary_dim / 16, elements i and i + rotary_dim
@@ -162,8 +162,8 @@ append_tokens_kernel(const AppendTokensArgs a, const GroupShape gs) {
         }
         if (tid < gs.tokens * pairs) {
             const int tk = tid / pairs, p = tid - tk * pairs, pos = s_pos[buf][tk];
-            // the turns' product wraps modulo one turn by itself; its top 32 bits as a
-            // signed fraction of half a turn give the angle to 2^-32 turns
+            // the turns' product wraps modulo one turn by itself; its top 32 bits are a signed
+            // fraction of half a turn, which fp32 then rounds (2^-26 turns at most)
             const uint64_t ph = (uint64_t)(int64_t)pos * a.rope.turns[p];
             float s, c;
             sincospif((float)(int)(ph >> 32) * 4.6566128730773926e-10f, &s, &c);

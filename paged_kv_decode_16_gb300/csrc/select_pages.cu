@@ -7,12 +7,13 @@
 // tensor cores (mma.sync m16n8k16: 16 pages x 8 queries), fed straight from global memory:
 // the contraction's order is free, so a lane takes 16 contiguous bytes of a row as its
 // fragments of two k-steps.  What bounds it: memory, 4 D bytes a page and head (256 units of
-// 8192 pages, 1.07 GB: 139 us with the choice), and for less the grid's start and the choice's
-// phases (256 uneven units of 256 to 2048 pages, 113 MB: 29.6 us, of which 7 the choice;
-// 256 units of 64 pages 7.6 us, of which 1.5 where scores near the border are told apart).
+// 8192 pages, 1.07 GB: 187 us with the choice, 5.7 TB/s), and for less the grid's start and
+// the choice's phases (256 uneven units of 256 to 2048 pages, 113 MB: 30.4 us, of which 7 the
+// choice; 256 units of 64 pages 7.7 us, of which 1.5 where scores near the border are told
+// apart).
 //
-// The choice is that of exact scores, so that it does not depend on how a product is
-// summed.  A product of two 16-bit values is exact in fp32; each of the 2 D / 16 steps adds 16
+// The choice does not depend on how the product is summed: it tells scores apart to 47 bits of
+// the sum of their terms' sizes (long_score).  A product of two 16-bit values is exact in fp32; each of the 2 D / 16 steps adds 16
 // of them to the sum, every addend cut at 2^-24 of the largest at worst: 17 addends, 2 D /
 // 16 <= 16 steps, so a score is off by at most e = 2^-15 S (S = sum |q_d| max |bound|; the
 // count gives 2^-15.9, the last sum of two chains included).  The k-th largest score is then
@@ -355,7 +356,7 @@ struct PickScratch {
     int few_at[kFew];              // pages that are not settled, the keys of their scores,
     uint32_t few[kFew];
     unsigned long long far[kFew];  // and of their 64-bit scores
-    int open_n, bin, above;
+    int open_n, bin;
     uint32_t kth;
 };
 
