@@ -843,9 +843,10 @@ pkv_status kv_append_tokens(const pkv_pool* pool, const void* k_new, int64_t k_s
  * pool's dtype); other pages' are left as they are.  A NaN key gives NaN.  Call
  * it behind the append of the same slots; a page's tokens have to be one run,
  * in ascending order, in one call (else the page's bounds are put together from
- * those of its runs, some elements of one and some of another).  Rows behind x are not read; a page whose tokens are taken back
- * keeps its (then wider) bounds until a row of it is written again.  8-bit
- * pool: UNSUPPORTED; bounds over the pool or the slots: ALIAS.  One launch. */
+ * those of its runs, some elements of one and some of another).  Rows behind x
+ * are not read; a page whose tokens are taken back keeps its (then wider) bounds
+ * until a row of it is written again.  8-bit pool: UNSUPPORTED; bounds over the
+ * pool or the slots: ALIAS.  One launch. */
 pkv_status kv_page_bounds(const pkv_pool* pool, const int64_t* slots, int n_tokens, void* bounds,
                           uint32_t* dev_status, pkv_stream stream);
 
